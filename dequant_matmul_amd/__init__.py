@@ -13,6 +13,9 @@ CPU fallback: if the library is missing, importing this package fails.
     H = qmm.embed(table, qmm.Q8_0, vocab, k, ids)      # ids int32 [seq] -> fp32 [seq, k]
     B = qmm.quantize(kv_f16, qmm.Q8_0)                 # fp16 [n, k] -> Q8_0 blocks
 
+Rotary positions, the paged KV cache and attention over it are in kv.py (C ABI
+include/qkv.h) and re-exported here.
+
 Block types and layouts follow shimmy "Architecture" (Quantization table) and
 dotLLM "GPU Inference" (Quantization on GPU table); see include/qmm.h.
 """
@@ -26,7 +29,7 @@ LIB_PATH = os.path.join(_HERE, "libqmm.so")
 
 Q4_0, Q8_0, Q4_K, Q6_K, Q5_0, Q5_K = 0, 1, 2, 3, 4, 5
 TYPE_NAMES = {Q4_0: "Q4_0", Q8_0: "Q8_0", Q4_K: "Q4_K", Q6_K: "Q6_K", Q5_0: "Q5_0", Q5_K: "Q5_K"}
-OK, ERR_NULL, ERR_TYPE, ERR_SHAPE, ERR_ALIGN, ERR_HIP = range(6)
+OK, ERR_NULL, ERR_TYPE, ERR_SHAPE, ERR_ALIGN, ERR_HIP, ERR_WORKSPACE = range(7)
 
 # C-ABI entry points and their ctypes signatures (mirrors include/qmm.h).
 _P, _I, _I64, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
@@ -286,3 +289,7 @@ def gemm_prefill(w, qtype: int, n: int, k: int, x, out=None):
     _call(lib.qmm_gemm_prefill(qtype, w.data_ptr(), n, k, x.data_ptr(), m, out.data_ptr(),
                                _stream_ptr(w.device)), "qmm_gemm_prefill")
     return out
+
+
+from .kv import (F16, KVCache, attention, attention_workspace, kv_append, kv_move, kv_read,  # noqa: E402
+                 rope, rope_angles, rope_freqs)

@@ -1,0 +1,709 @@
+// qkv_attn.h -- attention of a few query rows over the paged cache (single
+// tokens, drafted trees, short chunks), on the fp16 matrix cores.
+//
+// The rows of a kv head are its query heads times the new tokens, r = token *
+// group + head of the group, in tiles of 16.  A wave walks tiles of 64 tokens
+// with RT row tiles; four waves of a workgroup take every fourth tile of a split
+// of the sequence and join at the end; the splits are joined by
+// attn_join_kernel (one launch fewer where there is one split).
+//
+// Per tile, transposed throughout so that everything stays in registers:
+//   S^T[token][row] = K Q^T   per 32-dim block, A = K codes, B = Q^T; each
+//                             block's sums get the token's scale in fp32
+//   P = exp2(S - m)           running maximum m and sum l per row; the lane that
+//                             holds S^T[token][row] holds operand B of
+//   O^T[dim][row] += V^T P    A = V codes, B = P times the token's V scale
+// The codes are exact fp16 integers, so quantization adds no rounding; with two
+// parts P and Q carry about 22 bits, with one part P is rounded to fp16 (Q is
+// fp16 already).
+//
+// Bound: HBM.  A tile of Q8_0 at 128 dims is 17 KB per wave, loaded whole before
+// its first use (32 loads in flight per wave).
+#pragma once
+
+#include "qkv_layout.h"
+#include "qkv_launch.h"
+
+namespace qmm {
+
+typedef _Float16 h16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x3 __attribute__((ext_vector_type(3), aligned(4)));
+
+struct AttnArgs {
+    const void *q;
+    void *out;
+    const uint8_t *k, *v;
+    const int32_t *table, *ctx, *qstart;
+    const uint64_t *mask;
+    float *ws;
+    int64_t q_stride, out_stride, pages, columns;
+    int32_t tokens, per_seq, heads, kv_heads, group, dim, page_shift, mask_words, max_q, max_tiles, splits;
+    float scale;
+};
+
+// ------------------------------------------------------------ small helpers --
+
+template <int N>
+__device__ __forceinline__ void load_dw(const uint8_t *p, uint32_t *r)
+{
+    if constexpr (N == 4) {
+        const u32x4 v = *(const u32x4 *)p;
+        r[0] = v[0]; r[1] = v[1]; r[2] = v[2]; r[3] = v[3];
+    } else if constexpr (N == 3) {
+        const u32x3 v = *(const u32x3 *)p;
+        r[0] = v[0]; r[1] = v[1]; r[2] = v[2];
+    } else {
+        static_assert(N == 2, "");
+        const u32x2 v = *(const u32x2 *)p;
+        r[0] = v[0]; r[1] = v[1];
+    }
+}
+
+__device__ __forceinline__ h16x2 as_h2(uint32_t v) { return __builtin_bit_cast(h16x2, v); }
+__device__ __forceinline__ uint32_t as_u(h16x2 v) { return __builtin_bit_cast(uint32_t, v); }
+__device__ __forceinline__ h16x8 as_h8(uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    return __builtin_bit_cast(h16x8, (u32x4){a, b, c, d});
+}
+// Two values as fp16 (nearest even), and what that leaves of them.  The first
+// is opaque: folded into a multiply-add on one of its two uses only, it would be
+// one rounding there and another here, a whole fp16 step apart.
+__device__ __forceinline__ uint32_t to_h2(float a, float b) { return opaque(as_u((h16x2){(_Float16)a, (_Float16)b})); }
+__device__ __forceinline__ uint32_t rest_h2(float a, float b, uint32_t h)
+{
+    return as_u((h16x2){(_Float16)(a - (float)as_h2(h)[0]), (_Float16)(b - (float)as_h2(h)[1])});
+}
+// half i (compile time) of an array of dwords, as fp32
+__device__ __forceinline__ float half_of(const uint32_t *w, int i) { return (float)as_h2(w[i >> 1])[i & 1]; }
+
+// Bytes 2 j, 2 j + 1 of x (codes + 128) as two exact fp16 codes: 0x64bb is
+// 1024 + bb.
+__device__ __forceinline__ uint32_t q8_pair(uint32_t x, int j)
+{
+    const h16x2 off = {(_Float16)1152.f, (_Float16)1152.f};
+    return as_u(as_h2(__builtin_amdgcn_perm(0x64646464u, x, j ? 0x04030402u : 0x04010400u)) - off);
+}
+// Nibbles at bits 0 and 16 (HI: 4 and 20) of x, code + 8: the high nibble reads
+// as 1024 + 16 n.
+template <bool HI>
+__device__ __forceinline__ uint32_t q4_pair(uint32_t x)
+{
+    if constexpr (HI) {
+        const h16x2 f = {(_Float16)0.0625f, (_Float16)0.0625f}, off = {(_Float16)-72.f, (_Float16)-72.f};
+        return as_u(as_h2((x & 0x00f000f0u) | 0x64006400u) * f + off);
+    } else {
+        const h16x2 off = {(_Float16)1032.f, (_Float16)1032.f};
+        return as_u(as_h2((x & 0x000f000fu) | 0x64006400u) - off);
+    }
+}
+
+// Eight codes as operand A, and the order in which they stand: position p holds
+// element ORD(p).
+template <int KT>
+struct Codes;
+template <>
+struct Codes<KV_Q8> {
+    static __device__ __forceinline__ constexpr int k_ord(int p) { return p; }
+    static __device__ __forceinline__ constexpr int v_ord(int p) { return p; }
+    static __device__ __forceinline__ h16x8 k(const uint32_t *w)
+    {
+        return as_h8(q8_pair(w[0], 0), q8_pair(w[0], 1), q8_pair(w[1], 0), q8_pair(w[1], 1));
+    }
+    static __device__ __forceinline__ h16x8 v(const uint32_t *w, int) { return k(w); }
+};
+template <>
+struct Codes<KV_Q4> {
+    static __device__ __forceinline__ constexpr int k_ord(int p) { return (p >> 1) + 4 * (p & 1); }
+    static __device__ __forceinline__ constexpr int v_ord(int p) { return (p & 4) + ((p >> 1) & 1) + 2 * (p & 1); }
+    // one dword, dim j at nibble j
+    static __device__ __forceinline__ h16x8 k(const uint32_t *w)
+    {
+        const uint32_t x = w[0], y = x >> 8;
+        return as_h8(q4_pair<false>(x), q4_pair<true>(x), q4_pair<false>(y), q4_pair<true>(y));
+    }
+    // two dwords, token j in byte j: the low or the high nibbles
+    static __device__ __forceinline__ h16x8 v(const uint32_t *w, int hi)
+    {
+        const uint32_t a = w[0], b = w[0] >> 8, c = w[1], d = w[1] >> 8;
+        return hi ? as_h8(q4_pair<true>(a), q4_pair<true>(b), q4_pair<true>(c), q4_pair<true>(d))
+                  : as_h8(q4_pair<false>(a), q4_pair<false>(b), q4_pair<false>(c), q4_pair<false>(d));
+    }
+};
+template <>
+struct Codes<KV_F16> {
+    static __device__ __forceinline__ constexpr int k_ord(int p) { return p; }
+    static __device__ __forceinline__ constexpr int v_ord(int p) { return p; }
+    static __device__ __forceinline__ h16x8 k(const uint32_t *w) { return as_h8(w[0], w[1], w[2], w[3]); }
+    static __device__ __forceinline__ h16x8 v(const uint32_t *w, int) { return k(w); }
+};
+
+// Maximum (sum) over the four lanes of a query row: lanes n, n + 16, n + 32,
+// n + 48.  v_permlane*_swap exchanges the odd rows (the upper half) of one
+// register with the even rows (the lower half) of another; of a value and its
+// copy that leaves the two sides of the exchange.  Written out, with the two
+// wait states it needs behind a VALU write, because the compiler's builtin
+// returns its first result twice.
+template <class F>
+__device__ __forceinline__ float over_rows(float v, F f)
+{
+    float x = v, y = v;
+    asm volatile("s_nop 1\n\tv_permlane16_swap_b32 %0, %1" : "+v"(x), "+v"(y));
+    float z = f(x, y), w = z;
+    asm volatile("s_nop 1\n\tv_permlane32_swap_b32 %0, %1" : "+v"(z), "+v"(w));
+    return f(z, w);
+}
+__device__ __forceinline__ float rows_max(float v) { return over_rows(v, [](float a, float b) { return fmaxf(a, b); }); }
+__device__ __forceinline__ float rows_sum(float v) { return over_rows(v, [](float a, float b) { return a + b; }); }
+
+// 16 bits of row `row` of the mask from bit `rel` on; negative bits are
+// committed tokens (seen), bits past the words are not.
+__device__ __forceinline__ uint32_t mask16(const uint64_t *row, int words, int64_t rel)
+{
+    const int64_t w = rel >> 6;
+    const int sh = (int)(rel & 63);
+    const uint64_t a = w < 0 ? ~0ull : w < words ? row[w] : 0ull;
+    const uint64_t b = w + 1 < 0 ? ~0ull : w + 1 < words ? row[w + 1] : 0ull;
+    return (uint32_t)((a >> sh) | (sh ? b << (64 - sh) : 0ull)) & 0xffffu;
+}
+
+// The rows of q and the tokens of one sequence, from index arrays that are not
+// trusted.
+struct Seq {
+    int q0, tq;     // first row of q, new tokens
+    int64_t ctx;    // committed tokens
+};
+__device__ __forceinline__ Seq sequence(const AttnArgs &a, int b)
+{
+    Seq s;
+    int q1;
+    if (a.qstart) {
+        s.q0 = a.qstart[b];
+        q1 = a.qstart[b + 1];
+        s.q0 = s.q0 < 0 ? 0 : s.q0 > a.tokens ? a.tokens : s.q0;
+        q1 = q1 < s.q0 ? s.q0 : q1 > a.tokens ? a.tokens : q1;
+    } else {
+        s.q0 = b * a.per_seq;
+        q1 = s.q0 + a.per_seq;
+    }
+    s.tq = q1 - s.q0;
+    s.ctx = a.ctx[b] > 0 ? a.ctx[b] : 0;
+    return s;
+}
+
+// Tokens of the sequence that rows up to new token `last` can see at all.
+__device__ __forceinline__ int64_t seen(const AttnArgs &a, const Seq &s, int last)
+{
+    const int64_t fresh = a.mask ? (s.tq < 64 * (int64_t)a.mask_words ? s.tq : 64 * (int64_t)a.mask_words) : last + 1;
+    const int64_t n = s.ctx + fresh, cap = a.columns << a.page_shift, most = (int64_t)a.max_tiles * KV_TILE;
+    return n < cap ? (n < most ? n : most) : (cap < most ? cap : most);
+}
+
+__device__ __forceinline__ void read8(const _Float16 *p, float v[8])
+{
+    const u32x4 r = *(const u32x4 *)p;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] = (float)as_h2(r[i >> 1])[i & 1];
+}
+__device__ __forceinline__ void read8(const float *p, float v[8])
+{
+    const f32x4 a = *(const f32x4 *)p, b = *(const f32x4 *)(p + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] = a[i];
+        v[4 + i] = b[i];
+    }
+}
+__device__ __forceinline__ void write4(float *p, f32x4 v) { *(f32x4 *)p = v; }
+__device__ __forceinline__ void write4(_Float16 *p, f32x4 v)
+{
+    *(u32x2 *)p = (u32x2){as_u((h16x2){(_Float16)v[0], (_Float16)v[1]}), as_u((h16x2){(_Float16)v[2], (_Float16)v[3]})};
+}
+
+constexpr float LOG2E = 1.44269504088896341f;
+
+// The softmax weights are taken relative to 2^(M - P_TOP), M the running maximum
+// of score + exponent of the V scale: weight times V scale, the number that is
+// rounded to fp16 parts, is then at most 2^P_TOP and stays a normal fp16 down to
+// 2^-28 of the largest, whatever the size of V.  (F16 has no scale: exponent 0.)
+constexpr float P_TOP = 14.f;
+
+// Largest exponent e (value < 2^e, at least -14) of the fp16 scales in w[0..n),
+// of either sign.
+template <int N>
+__device__ __forceinline__ float scale_exponent(const uint32_t (*w)[8])
+{
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    u16x2 m = {0, 0};
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, w[i][j] & 0x7fff7fffu));
+    const int top = m[0] > m[1] ? m[0] : m[1];
+    const int e = top >> 10;
+    return (float)((e > 1 ? e : 1) - 14);
+}
+
+// ---------------------------------------------------------------- the kernel --
+
+template <int NB, int KT, int RT, int PARTS, typename IO>
+__global__ void __launch_bounds__(256, RT >= 4 || NB > 4 ? 1 : 2)
+attn_kernel(AttnArgs a)
+{
+    using L = KvLay<NB, KT>;
+    using C = Codes<KT>;
+    constexpr int KDW = NB * L::UNIT / 4;              // dwords of a lane's K row piece of one row tile
+    constexpr int CDW = L::G * L::UNIT / 4;            // dwords of one load of it
+    constexpr int VDW = KT == KV_F16 ? 8 : 4;          // dwords of a V piece
+    constexpr int VN = KT == KV_Q4 ? NB : 2 * NB;      // V pieces
+    constexpr bool QREG = RT * PARTS * NB <= 16;       // Q fragments in registers, else in LDS
+
+    __shared__ __align__(16) f32x4 joined[4][2 * NB][64];
+    __shared__ float join_m[4][16], join_l[4][16];
+    __shared__ __align__(16) h16x8 qlds[QREG ? 1 : RT * PARTS * NB][64];
+    __shared__ float qscale[RT][16];
+
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, h = lane >> 4;
+    const int split = blockIdx.x, head = blockIdx.y % a.kv_heads, b = blockIdx.z;
+    const int r0 = (int)(blockIdx.y / a.kv_heads) * 16 * RT;
+
+    const Seq s = sequence(a, b);
+    const int rows = (s.tq < a.max_q ? s.tq : a.max_q) * a.group;
+    if (r0 >= rows)
+        return;
+    const int last = ((rows < r0 + 16 * RT ? rows : r0 + 16 * RT) - 1) / a.group;
+    const int64_t nseen = seen(a, s, last);
+    const int ntiles = (int)((nseen + KV_TILE - 1) / KV_TILE);
+    const int per = (ntiles + a.splits - 1) / a.splits;
+    const int t_begin = split * per, t_end = t_begin + per < ntiles ? t_begin + per : ntiles;
+
+    // ---- the rows of q as operand B, scaled by a power of two per row so that
+    // both fp16 parts are normal numbers
+    h16x8 qreg[QREG ? RT * PARTS * NB : 1];
+    float rs[RT];
+    int tok[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        const int r = r0 + 16 * rt + n;
+        tok[rt] = r < rows ? r / a.group : -1;
+        if (!QREG && rt % 4 != wave)
+            continue;
+        float x[NB][8], amax = 0.f;
+        const IO *row = (const IO *)a.q + (int64_t)(s.q0 + (r < rows ? tok[rt] : 0)) * a.q_stride +
+                        (int64_t)(head * a.group + (r < rows ? r % a.group : 0)) * a.dim;
+#pragma unroll
+        for (int bl = 0; bl < NB; ++bl) {
+            const int d0 = 32 * bl + 8 * h;
+            if (r < rows && d0 < a.dim) {
+                read8(row + d0, x[bl]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    x[bl][j] = 0.f;
+            }
+        }
+        float scale;
+        if constexpr (PARTS == 2) {
+#pragma unroll
+            for (int bl = 0; bl < NB; ++bl)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    x[bl][j] *= a.scale * LOG2E;
+                    amax = fmaxf(amax, fabsf(x[bl][j]));
+                }
+            amax = rows_max(amax);
+            int e;
+            (void)frexpf(amax, &e);
+            e = amax > 0.f && amax < 3.0e38f ? 15 - e : 0;      // maximum to [2^14, 2^15)
+            e = e < 120 ? e : 120;
+            scale = ldexpf(1.f, -e);
+#pragma unroll
+            for (int bl = 0; bl < NB; ++bl)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    x[bl][j] = ldexpf(x[bl][j], e);
+        } else {
+            scale = fmaxf(fabsf(a.scale) * LOG2E, 1e-37f);      // not 0: unseen tokens score -inf times it
+            if (a.scale < 0.f)
+#pragma unroll
+                for (int bl = 0; bl < NB; ++bl)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        x[bl][j] = -x[bl][j];
+        }
+#pragma unroll
+        for (int bl = 0; bl < NB; ++bl) {
+            uint32_t w[4], r[4];
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const float y = x[bl][C::k_ord(2 * p)], z = x[bl][C::k_ord(2 * p + 1)];
+                w[p] = to_h2(y, z);
+                r[p] = rest_h2(y, z, w[p]);
+            }
+            const h16x8 hi = as_h8(w[0], w[1], w[2], w[3]), lo = as_h8(r[0], r[1], r[2], r[3]);
+            if constexpr (QREG) {
+                qreg[(rt * PARTS) * NB + bl] = hi;
+                if constexpr (PARTS == 2)
+                    qreg[(rt * PARTS + 1) * NB + bl] = lo;
+            } else {
+                qlds[(rt * PARTS) * NB + bl][lane] = hi;
+                if constexpr (PARTS == 2)
+                    qlds[(rt * PARTS + 1) * NB + bl][lane] = lo;
+            }
+        }
+        if constexpr (QREG)
+            rs[rt] = scale;
+        else if (h == 0)
+            qscale[rt][n] = scale;
+    }
+    if constexpr (!QREG) {
+        __syncthreads();
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+            rs[rt] = qscale[rt][n];
+    }
+    auto qf = [&](int rt, int part, int bl) -> h16x8 {
+        if constexpr (QREG)
+            return qreg[(rt * PARTS + part) * NB + bl];
+        else
+            return qlds[(rt * PARTS + part) * NB + bl][lane];
+    };
+
+    f32x4 o[RT][2 * NB];
+    float m[RT], l[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        m[rt] = -INFINITY;
+        l[rt] = 0.f;
+#pragma unroll
+        for (int t = 0; t < 2 * NB; ++t)
+            o[rt][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    }
+
+    const int32_t *pages = a.table + (int64_t)b * a.columns;
+    const int tshift = a.page_shift - 6;
+    for (int tile = t_begin + wave; tile < t_end; tile += 4) {
+        const int page = pages[tile >> tshift];
+        if (page < 0 || page >= a.pages)
+            continue;                                   // nothing of it is seen
+        const int64_t at = ((((int64_t)page * a.kv_heads + head) << tshift) + (tile & ((1 << tshift) - 1))) *
+                           (int64_t)L::TILE_BYTES;
+        const uint8_t *kp = a.k + at, *vp = a.v + at;
+
+        // ---- every load of the tile
+        uint32_t kr[4][KDW], vr[VN][VDW], ks[KT == KV_F16 ? 1 : 8 * NB], vs[KT == KV_F16 ? 1 : NB][8];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int g = 0; g < NB / L::G; ++g)
+                load_dw<CDW>(kp + ((c * (NB / L::G) + g) * 64 + lane) * (L::G * L::UNIT), &kr[c][g * CDW]);
+        if constexpr (KT != KV_F16) {
+#pragma unroll
+            for (int i = 0; i < 2 * NB; ++i)
+                load_dw<4>(kp + L::CODE_BYTES + h * 32 * NB + 16 * i, &ks[4 * i]);
+        }
+#pragma unroll
+        for (int t = 0; t < VN; ++t) {
+            if constexpr (KT == KV_F16) {
+                load_dw<4>(vp + ((t * 2) * 64 + lane) * 16, &vr[t][0]);
+                load_dw<4>(vp + ((t * 2 + 1) * 64 + lane) * 16, &vr[t][4]);
+            } else {
+                load_dw<4>(vp + (t * 64 + lane) * 16, &vr[t][0]);
+            }
+        }
+        if constexpr (KT != KV_F16) {
+#pragma unroll
+            for (int bl = 0; bl < NB; ++bl) {
+                load_dw<4>(vp + L::CODE_BYTES + (bl * 64 + 16 * h) * 2, &vs[bl][0]);
+                load_dw<4>(vp + L::CODE_BYTES + (bl * 64 + 16 * h) * 2 + 16, &vs[bl][4]);
+            }
+        }
+
+        // ---- scores
+        f32x4 sc[RT][4];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                sc[rt][c] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int bl = 0; bl < NB; ++bl) {
+            h16x8 kf[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                kf[c] = C::k(&kr[c][bl * (L::UNIT / 4)]);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                const h16x8 q0 = qf(rt, 0, bl), q1 = qf(rt, PARTS - 1, bl);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if constexpr (KT == KV_F16) {
+                        sc[rt][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[c], q0, sc[rt][c], 0, 0, 0);
+                        if constexpr (PARTS == 2)
+                            sc[rt][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[c], q1, sc[rt][c], 0, 0, 0);
+                    } else {
+                        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+                        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[c], q0, acc, 0, 0, 0);
+                        if constexpr (PARTS == 2)
+                            acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[c], q1, acc, 0, 0, 0);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            sc[rt][c][i] = fmaf(acc[i], half_of(ks, (4 * c + i) * NB + bl), sc[rt][c][i]);
+                    }
+                }
+            }
+        }
+
+        // ---- the part of the tile that a row does not see; what lies behind the
+        // last token may be any bits: its scores are replaced, its V zeroed
+        const int64_t k0 = (int64_t)tile * KV_TILE;
+        const bool edge = k0 + KV_TILE > s.ctx;
+        if (edge) {
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                const int64_t rel = k0 + 16 * h - s.ctx;
+                uint32_t bits = 0;
+                if (tok[rt] >= 0) {
+                    if (a.mask) {
+                        bits = mask16(a.mask + (int64_t)(s.q0 + tok[rt]) * a.mask_words, a.mask_words, rel);
+                    } else {
+                        const int64_t cnt = tok[rt] + 1 - rel;
+                        bits = cnt <= 0 ? 0u : cnt >= 16 ? 0xffffu : (1u << cnt) - 1u;
+                    }
+                    const int64_t left = nseen - k0 - 16 * h;
+                    bits &= left <= 0 ? 0u : left >= 16 ? 0xffffu : (1u << left) - 1u;
+                }
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        sc[rt][c][i] = (bits >> (4 * c + i)) & 1u ? sc[rt][c][i] : -INFINITY;
+            }
+            if (k0 + KV_TILE > nseen) {
+                const int left = (int)(nseen - k0) - 16 * h;
+#pragma unroll
+                for (int w = 0; w < 8; ++w) {
+                    const uint32_t keep = (2 * w < left ? 0xffffu : 0u) | (2 * w + 1 < left ? 0xffff0000u : 0u);
+                    if constexpr (KT == KV_F16) {
+#pragma unroll
+                        for (int t = 0; t < VN; ++t)
+                            vr[t][w] &= keep;
+                    } else {
+#pragma unroll
+                        for (int bl = 0; bl < NB; ++bl)
+                            vs[bl][w] &= keep;
+                    }
+                }
+            }
+        }
+
+        // ---- running maximum and sum; P takes the place of the scores
+        float ev = 0.f;
+        if constexpr (KT != KV_F16)
+            ev = scale_exponent<NB>(vs);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    mx = fmaxf(mx, sc[rt][c][i]);
+            mx = rows_max(fmaf(mx, rs[rt], ev));
+            const float mn = fmaxf(m[rt], mx), mu = mn == -INFINITY ? 0.f : mn;
+            const float alpha = exp2f(m[rt] - mu), shift = P_TOP - mu;
+            m[rt] = mn;
+            float sum = 0.f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float p = exp2f(fmaf(sc[rt][c][i], rs[rt], shift));
+                    sc[rt][c][i] = p;
+                    sum += p;
+                }
+            l[rt] = fmaf(l[rt], alpha, sum);
+            if (__any(alpha != 1.f)) {
+#pragma unroll
+                for (int t = 0; t < 2 * NB; ++t)
+                    o[rt][t] *= alpha;
+            }
+        }
+
+        // ---- output
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+#pragma unroll
+            for (int bl = 0; bl < NB; ++bl) {
+                const h16x8 v0 = KT == KV_F16 ? C::v(&vr[2 * bl][4 * st], 0)
+                                 : KT == KV_Q8 ? C::v(&vr[2 * bl][2 * st], 0) : C::v(&vr[bl][2 * st], 0);
+                const h16x8 v1 = KT == KV_F16 ? C::v(&vr[VN > NB ? 2 * bl + 1 : 0][4 * st], 0)
+                                 : KT == KV_Q8 ? C::v(&vr[VN > NB ? 2 * bl + 1 : 0][2 * st], 0) : C::v(&vr[bl][2 * st], 1);
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    uint32_t w[4], r[4];
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        const int i = 8 * st + C::v_ord(2 * p), j = 8 * st + C::v_ord(2 * p + 1);
+                        float y = sc[rt][i >> 2][i & 3], z = sc[rt][j >> 2][j & 3];
+                        if constexpr (KT != KV_F16) {
+                            y *= half_of(vs[bl], i);
+                            z *= half_of(vs[bl], j);
+                        }
+                        w[p] = to_h2(y, z);
+                        r[p] = rest_h2(y, z, w[p]);
+                    }
+                    const h16x8 hi = as_h8(w[0], w[1], w[2], w[3]), lo = as_h8(r[0], r[1], r[2], r[3]);
+                    o[rt][2 * bl] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, hi, o[rt][2 * bl], 0, 0, 0);
+                    o[rt][2 * bl + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, hi, o[rt][2 * bl + 1], 0, 0, 0);
+                    if constexpr (PARTS == 2) {
+                        o[rt][2 * bl] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, lo, o[rt][2 * bl], 0, 0, 0);
+                        o[rt][2 * bl + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, lo, o[rt][2 * bl + 1], 0, 0, 0);
+                    }
+                }
+            }
+        }
+    }
+
+    // ---- join the four waves, one row tile at a time; every wave then finishes
+    // every fourth 16-dim tile
+    const int64_t wrows = (int64_t)a.tokens * a.heads;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        if (rt > 0)
+            __syncthreads();
+        const float lsum = rows_sum(l[rt]);
+        if (h == 0) {
+            join_m[wave][n] = m[rt];
+            join_l[wave][n] = lsum;
+        }
+#pragma unroll
+        for (int t = 0; t < 2 * NB; ++t)
+            joined[wave][t][lane] = o[rt][t];
+        __syncthreads();
+        float mm = -INFINITY, w[4], lt = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            mm = fmaxf(mm, join_m[i][n]);
+        const float mu = mm == -INFINITY ? 0.f : mm;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w[i] = exp2f(join_m[i][n] - mu);
+            lt = fmaf(w[i], join_l[i][n], lt);
+        }
+        if (tok[rt] >= 0) {
+            const int r = r0 + 16 * rt + n, hq = head * a.group + (r - tok[rt] * a.group);
+            const int64_t row = (int64_t)(s.q0 + tok[rt]) * a.heads + hq;
+            const float inv = lt > 0.f ? 1.f / lt : 0.f;
+            for (int t = wave; t < 2 * NB; t += 4) {
+                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc += joined[i][t][lane] * w[i];
+                const int d0 = 16 * t + 4 * h;
+                if (a.splits > 1)
+                    *(f32x4 *)(a.ws + ((int64_t)split * wrows + row) * L::DP + d0) = acc;
+                else if (d0 < a.dim)
+                    write4((IO *)a.out + (int64_t)(s.q0 + tok[rt]) * a.out_stride + (int64_t)hq * a.dim + d0, acc * inv);
+            }
+            if (a.splits > 1 && wave == 0 && h == 0) {
+                float2 *ml = (float2 *)(a.ws + (int64_t)a.splits * wrows * L::DP) + (int64_t)split * wrows + row;
+                *ml = make_float2(mm, lt);
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------- joining the splits --
+
+// A quarter of a wave row: each thread takes 4 dims of one row of q.  blockIdx.y
+// is the sequence, so that rows of no sequence are left alone; splits that saw
+// nothing wrote l = 0 and (for all this kernel knows) no output.
+template <int NB, typename IO>
+__global__ void __launch_bounds__(256)
+attn_join_kernel(AttnArgs a)
+{
+    constexpr int PER = 8 * NB, ROWS = 256 / PER;
+    const int r = threadIdx.x / PER, d0 = 4 * (threadIdx.x % PER);
+    const Seq s = sequence(a, blockIdx.y);
+    const int64_t i = (int64_t)blockIdx.x * ROWS + r;
+    const int64_t rows = (int64_t)(s.tq < a.max_q ? s.tq : a.max_q) * a.heads;
+    if (r >= ROWS || i >= rows || d0 >= a.dim)
+        return;
+    const int64_t wrows = (int64_t)a.tokens * a.heads, row = (int64_t)s.q0 * a.heads + i;
+    const float2 *ml = (const float2 *)(a.ws + (int64_t)a.splits * wrows * (32 * NB)) + row;
+    float mm = -INFINITY;
+    for (int sp = 0; sp < a.splits; ++sp)
+        mm = fmaxf(mm, ml[sp * wrows].x);
+    const float mu = mm == -INFINITY ? 0.f : mm;
+    float lt = 0.f;
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int sp = 0; sp < a.splits; ++sp) {
+        const float2 x = ml[sp * wrows];
+        const f32x4 part = *(const f32x4 *)(a.ws + (sp * wrows + row) * (32 * NB) + d0);
+        const float w = exp2f(x.x - mu);
+        if (x.y > 0.f) {
+            lt = fmaf(w, x.y, lt);
+            acc += part * w;
+        }
+    }
+    const float inv = lt > 0.f ? 1.f / lt : 0.f;
+    const int64_t t = i / a.heads;
+    write4((IO *)a.out + (s.q0 + t) * a.out_stride + (i - t * a.heads) * a.dim + d0, acc * inv);
+}
+
+// ------------------------------------------------------------------- launch --
+
+template <int NB, int KT, int RT, typename IO>
+hipError_t attn_rows(const AttnArgs &a, const dim3 &grid, hipStream_t s)
+{
+    constexpr int PARTS = sizeof(IO) == 4 ? 2 : 1;
+    hipLaunchKernelGGL((attn_kernel<NB, KT, RT, PARTS, IO>), grid, dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+template <int NB, int KT, typename IO>
+hipError_t attn_blocks(const AttnArgs &a, const AttnPlan &p, int64_t batch, hipStream_t s)
+{
+    const dim3 grid((unsigned)p.splits, (unsigned)(a.kv_heads * p.groups), (unsigned)batch);
+    hipError_t e = hipErrorInvalidValue;
+    if (p.rt == 1)
+        e = attn_rows<NB, KT, 1, IO>(a, grid, s);
+    else if (p.rt == 2)
+        e = attn_rows<NB, KT, 2, IO>(a, grid, s);
+    else if constexpr (NB <= 4)
+        e = attn_rows<NB, KT, 4, IO>(a, grid, s);
+    if (e != hipSuccess || p.splits == 1)
+        return e;
+    constexpr int ROWS = 256 / (8 * NB);
+    const int64_t most = (a.max_q < a.tokens ? a.max_q : a.tokens) * (int64_t)a.heads;
+    hipLaunchKernelGGL((attn_join_kernel<NB, IO>), dim3((unsigned)((most + ROWS - 1) / ROWS), (unsigned)batch), dim3(256),
+                       0, s, a);
+    return hipGetLastError();
+}
+
+// One translation unit per cache type.
+template <int KT>
+hipError_t attn_type(const AttnArgs &a, const AttnPlan &p, int64_t batch, int nb, int half, hipStream_t s)
+{
+    switch (nb) {
+#define QKV_CASE(N)                                                                                              \
+    case N:                                                                                                      \
+        return half ? attn_blocks<N, KT, _Float16>(a, p, batch, s) : attn_blocks<N, KT, float>(a, p, batch, s)
+        QKV_CASE(2);
+        QKV_CASE(3);
+        QKV_CASE(4);
+        QKV_CASE(8);
+#undef QKV_CASE
+    default: return hipErrorInvalidValue;
+    }
+}
+
+hipError_t attn_f16(const AttnArgs &a, const AttnPlan &p, int64_t batch, int nb, int half, hipStream_t s);
+hipError_t attn_q8(const AttnArgs &a, const AttnPlan &p, int64_t batch, int nb, int half, hipStream_t s);
+hipError_t attn_q4(const AttnArgs &a, const AttnPlan &p, int64_t batch, int nb, int half, hipStream_t s);
+
+}  // namespace qmm

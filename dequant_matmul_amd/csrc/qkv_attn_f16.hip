@@ -1,0 +1,12 @@
+// qkv_attn_f16.hip -- the attention kernels of qkv_attn.h for one cache type (a
+// translation unit each, so that they compile side by side).
+#include "qkv_attn.h"
+
+namespace qmm {
+
+hipError_t attn_f16(const AttnArgs &a, const AttnPlan &p, int64_t batch, int nb, int half, hipStream_t s)
+{
+    return attn_type<KV_F16>(a, p, batch, nb, half, s);
+}
+
+}  // namespace qmm

@@ -1,0 +1,580 @@
+// qkv_cache.hip -- rotary positions and the paged KV cache on gfx950: angles,
+// rotation, append (rotate, quantize, scatter), read back, move.
+//
+// shimmy "Airframe GPU pipeline" rotates q and k and writes a resident KV
+// cache per layer; dotLLM "GPU Inference" keeps it quantized (Q8_0 / Q4_0).
+// All of these move data and are bound by HBM at length and by the launch for
+// a few tokens; every kernel is one launch.
+//
+// Rounding: rotation products and sums are separate fp32 roundings (contraction
+// off) and the quantizer is the rule of qmm_quant.hip, so the stored bytes are
+// those of any exact fp32 evaluation.
+#include "qkv_layout.h"
+#include "qkv_launch.h"
+
+namespace qmm {
+
+namespace {
+
+__device__ __forceinline__ void load8(const _Float16 *p, float v[8])
+{
+    const u32x4 r = *(const u32x4 *)p;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = h2f(r[i] & 0xffffu);
+        v[2 * i + 1] = h2f(r[i] >> 16);
+    }
+}
+
+__device__ __forceinline__ void load8(const float *p, float v[8])
+{
+    const f32x4 a = *(const f32x4 *)p, b = *(const f32x4 *)(p + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] = a[i];
+        v[4 + i] = b[i];
+    }
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b)
+{
+    return __builtin_bit_cast(uint32_t, (h16x2){(_Float16)a, (_Float16)b});
+}
+
+__device__ __forceinline__ void store8(_Float16 *p, const float v[8])
+{
+    *(u32x4 *)p = (u32x4){pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7])};
+}
+
+__device__ __forceinline__ void store8(float *p, const float v[8])
+{
+    *(f32x4 *)p = (f32x4){v[0], v[1], v[2], v[3]};
+    *(f32x4 *)(p + 4) = (f32x4){v[4], v[5], v[6], v[7]};
+}
+
+// (c, s) of 4 consecutive pairs
+__device__ __forceinline__ void load_cs4(const float *cs, float c[4], float s[4])
+{
+    const f32x4 a = *(const f32x4 *)cs, b = *(const f32x4 *)(cs + 4);
+    c[0] = a[0]; s[0] = a[1]; c[1] = a[2]; s[1] = a[3];
+    c[2] = b[0]; s[2] = b[1]; c[3] = b[2]; s[3] = b[3];
+}
+
+// x holds dims d0 .. d0 + 7 (d0 a multiple of 8) of the head row at `row`;
+// rotate those below 2 * pairs.  cs: the token's (c, s) pairs.  Rows of cs start
+// 16-byte aligned only where pairs is even, and 8-dim groups meet whole pairs'
+// groups only where pairs is a multiple of 8 (4 interleaved): those take vector
+// loads, the rest element by element.
+template <typename I>
+__device__ __forceinline__ void rotate8(float x[8], int d0, const I *row, const float *cs, int pairs, int inter)
+{
+#pragma clang fp contract(off)
+    const int rot = 2 * pairs;
+    if (d0 >= rot)
+        return;
+    if (inter) {
+        float c[4], s[4];
+        const int p0 = d0 >> 1;
+        if ((pairs & 3) == 0) {
+            load_cs4(cs + 2 * p0, c, s);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int p = p0 + i < pairs ? p0 + i : pairs - 1;
+                c[i] = cs[2 * p];
+                s[i] = cs[2 * p + 1];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (p0 + i < pairs) {
+                const float a = x[2 * i], b = x[2 * i + 1];
+                x[2 * i] = a * c[i] - b * s[i];
+                x[2 * i + 1] = b * c[i] + a * s[i];
+            }
+    } else if ((pairs & 7) == 0) {
+        const bool lo = d0 < pairs;
+        const int p0 = lo ? d0 : d0 - pairs;
+        float y[8], c[8], s[8];
+        load8(row + (lo ? d0 + pairs : p0), y);
+        load_cs4(cs + 2 * p0, c, s);
+        load_cs4(cs + 2 * p0 + 8, c + 4, s + 4);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            x[i] = lo ? x[i] * c[i] - y[i] * s[i] : x[i] * c[i] + y[i] * s[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int d = d0 + i;
+            if (d < rot) {
+                const bool lo = d < pairs;
+                const int p = lo ? d : d - pairs;
+                const float y = (float)row[lo ? d + pairs : p], c = cs[2 * p], s = cs[2 * p + 1];
+                x[i] = lo ? x[i] * c - y * s : x[i] * c + y * s;
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------- the angles --
+
+// One thread per (token, pair).  The angle is one 64-bit product: at position
+// 2^20 its rounding is 2^-33 of a radian, below the fp32 rounding of the result.
+__global__ void __launch_bounds__(256)
+angles_kernel(const int32_t *__restrict__ pos, int64_t total, const double *__restrict__ freqs, uint32_t pairs,
+              double mag, float2 *__restrict__ cs)
+{
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int64_t t = i / pairs;
+        double s, c;
+        sincos((double)pos[t] * freqs[i - t * pairs], &s, &c);
+        cs[i] = make_float2((float)(mag * c), (float)(mag * s));
+    }
+}
+
+// ------------------------------------------------------------ the rotation --
+
+// 256 threads take `tpb` whole tokens; a thread holds one 8-dim group of a
+// head (half layout with vector groups: the group and its partner group, so
+// that a row may be rotated in place).
+template <typename I>
+__global__ void __launch_bounds__(256)
+rope_kernel(const I *x, int64_t stride, int64_t tokens, int heads, int dim, const float *__restrict__ cs, int pairs,
+            int inter, I *out, int64_t out_stride, int tpb, int units)
+{
+#pragma clang fp contract(off)
+    const bool twin = !inter && (pairs & 7) == 0;
+    const int per = heads * units;
+    const int64_t t0 = (int64_t)blockIdx.x * tpb;
+    for (int it = threadIdx.x; it < tpb * per; it += 256) {
+        const int tt = it / per, r = it - tt * per, head = r / units, u = r - head * units;
+        const int64_t t = t0 + tt;
+        if (t >= tokens)
+            return;
+        const I *row = x + t * stride + (int64_t)head * dim;
+        I *dst = out + t * out_stride + (int64_t)head * dim;
+        const float *ct = cs + t * 2 * pairs;
+        float a[8];
+        if (twin) {
+            const int nr = pairs >> 3;                  // rotated groups come as pairs
+            if (u < nr) {
+                float b[8], c[8], s[8], p[8], q[8];
+                load8(row + 8 * u, a);
+                load8(row + 8 * u + pairs, b);
+                load_cs4(ct + 16 * u, c, s);
+                load_cs4(ct + 16 * u + 8, c + 4, s + 4);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    p[i] = a[i] * c[i] - b[i] * s[i];
+                    q[i] = b[i] * c[i] + a[i] * s[i];
+                }
+                store8(dst + 8 * u, p);
+                store8(dst + 8 * u + pairs, q);
+            } else if (row != dst) {
+                const int d0 = 2 * pairs + 8 * (u - nr);
+                load8(row + d0, a);
+                store8(dst + d0, a);
+            }
+        } else if (inter) {
+            load8(row + 8 * u, a);
+            rotate8(a, 8 * u, row, ct, pairs, 1);
+            store8(dst + 8 * u, a);
+        } else {
+            // odd pair counts: one thread takes pair u of the head, the last
+            // ones the untouched dims
+            if (u < pairs) {
+                const float e = (float)row[u], f = (float)row[u + pairs], c = ct[2 * u], s = ct[2 * u + 1];
+                dst[u] = (I)(e * c - f * s);
+                dst[u + pairs] = (I)(f * c + e * s);
+            } else {
+                dst[u + pairs] = row[u + pairs];
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ append --
+
+__device__ __forceinline__ float swap_f(float v) { return dpp_f(v, 0xB1); }   // with the neighbouring lane
+__device__ __forceinline__ uint32_t swap_u(uint32_t v)
+{
+    return __builtin_bit_cast(uint32_t, dpp_f(__builtin_bit_cast(float, v), 0xB1));
+}
+
+// A thread takes 16 values of a row (half a block): blockIdx.x a window of
+// tokens, y the kv head, z 0 for K and 1 for V.  Two neighbouring lanes share
+// a block and exchange its maximum.  K goes out in 8-dim units, V byte by byte
+// (a token is one byte of every 16): a window's tokens are usually neighbours,
+// so that the L2 gathers whole lines.
+template <int NB, int KT, typename I>
+__global__ void __launch_bounds__(256)
+append_kernel(KvView c, const I *__restrict__ kin, int64_t k_stride, const I *__restrict__ vin, int64_t v_stride,
+              int64_t tokens, const int32_t *__restrict__ slots, const float *__restrict__ cs, int pairs, int inter)
+{
+#pragma clang fp contract(off)
+    using L = KvLay<NB, KT>;
+    constexpr int HB = 2 * NB, WIN = 256 / HB;
+    const bool is_v = blockIdx.z != 0;
+    const int head = blockIdx.y, dim = c.head_dim;
+    const int tt = threadIdx.x / HB, hb = threadIdx.x % HB;
+    const int64_t t = (int64_t)blockIdx.x * WIN + tt;
+    int64_t tile;
+    int key;
+    if (tt >= WIN || t >= tokens || !slot_at<L>(c, slots[t], head, tile, key))
+        return;
+
+    const I *row = is_v ? vin + t * v_stride + (int64_t)head * dim : kin + t * k_stride + (int64_t)head * dim;
+    float x[16];
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        const int d0 = 16 * hb + 8 * g;
+        float *y = x + 8 * g;
+        if (d0 < dim) {
+            load8(row + d0, y);
+            if (!is_v && pairs > 0)
+                rotate8(y, d0, row, cs + t * 2 * pairs, pairs, inter);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                y[i] = 0.f;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        x[i] = x[i] == x[i] ? fminf(fmaxf(x[i], -65504.f), 65504.f) : 0.f;
+
+    uint8_t *base = (is_v ? c.v : c.k) + tile;
+    const int b = hb >> 1, h0 = 2 * (hb & 1);
+    if constexpr (KT == KV_F16) {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            w[i] = pack2(x[2 * i], x[2 * i + 1]);
+        if (!is_v) {
+            *(u32x4 *)(base + L::k_unit(key, b, h0)) = (u32x4){w[0], w[1], w[2], w[3]};
+            *(u32x4 *)(base + L::k_unit(key, b, h0 + 1)) = (u32x4){w[4], w[5], w[6], w[7]};
+        } else {
+#pragma unroll
+            for (int m = 0; m < 16; ++m)
+                *(uint16_t *)(base + L::v_code(key, hb, m)) = (uint16_t)(w[m >> 1] >> (16 * (m & 1)));
+        }
+    } else {
+        float d;
+        uint32_t code[16];
+        if constexpr (KT == KV_Q8) {
+            float amax = 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                amax = fmaxf(amax, fabsf(x[i]));
+            amax = fmaxf(amax, swap_f(amax));
+            d = amax / 127.f;
+            const float id = d != 0.f ? 1.f / d : 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                code[i] = (uint32_t)((int)roundf(x[i] * id) + 128);
+        } else {
+            // the first value of largest magnitude decides; on a tie between
+            // the lanes the lower one holds it
+            float amax = 0.f, vmax = 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (fabsf(x[i]) > amax) {
+                    amax = fabsf(x[i]);
+                    vmax = x[i];
+                }
+            const float oa = swap_f(amax), ov = swap_f(vmax);
+            if (oa > amax || (oa == amax && (hb & 1)))
+                vmax = ov;
+            d = vmax / -8.f;
+            const float id = d != 0.f ? 1.f / d : 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int q = (int)truncf(x[i] * id + 8.5f);
+                code[i] = (uint32_t)(q < 15 ? q : 15);
+            }
+        }
+        if ((hb & 1) == 0)
+            *(_Float16 *)(base + (is_v ? L::v_scale(key, b) : L::k_scale(key, b))) = (_Float16)d;
+        if constexpr (KT == KV_Q8) {
+            if (!is_v) {
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    uint2 w;
+                    w.x = code[8 * g] | code[8 * g + 1] << 8 | code[8 * g + 2] << 16 | code[8 * g + 3] << 24;
+                    w.y = code[8 * g + 4] | code[8 * g + 5] << 8 | code[8 * g + 6] << 16 | code[8 * g + 7] << 24;
+                    *(uint2 *)(base + L::k_unit(key, b, h0 + g)) = w;
+                }
+            } else {
+#pragma unroll
+                for (int m = 0; m < 16; ++m)
+                    base[L::v_code(key, hb, m)] = (uint8_t)code[m];
+            }
+        } else {
+            uint32_t w[2] = {0, 0};
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                w[i >> 3] |= code[i] << (4 * (i & 7));
+            if (!is_v) {
+                *(uint32_t *)(base + L::k_unit(key, b, h0)) = w[0];
+                *(uint32_t *)(base + L::k_unit(key, b, h0 + 1)) = w[1];
+            } else {
+                // dims m and 16 + m of the block share a byte: the even lane
+                // writes m = 0..7, the odd one 8..15
+                const uint32_t o0 = swap_u(w[0]), o1 = swap_u(w[1]);
+                const uint32_t lo = (hb & 1) ? o1 : w[0], hi = (hb & 1) ? w[1] : o0;
+                const int m0 = 8 * (hb & 1);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    base[L::v_code(key, hb & ~1, m0 + i)] =
+                        (uint8_t)(((lo >> (4 * i)) & 15u) | (((hi >> (4 * i)) & 15u) << 4));
+            }
+        }
+    }
+}
+
+// -------------------------------------------------------------------- read --
+
+// A thread decodes 8 dims of a row; blockIdx.y the kv head, z 0 for K, 1 for V.
+template <int NB, int KT, typename O>
+__global__ void __launch_bounds__(256)
+read_kernel(KvView c, const int32_t *__restrict__ slots, int64_t n, O *__restrict__ k_out, O *__restrict__ v_out)
+{
+    using L = KvLay<NB, KT>;
+    constexpr int U = 4 * NB, ROWS = 256 / U;
+    const bool is_v = blockIdx.z != 0;
+    O *out = is_v ? v_out : k_out;
+    const int r = threadIdx.x / U, u = threadIdx.x % U, head = blockIdx.y;
+    const int64_t i = (int64_t)blockIdx.x * ROWS + r;
+    if (out == nullptr || r >= ROWS || i >= n || 8 * u >= c.head_dim)
+        return;
+    float x[8];
+    int64_t tile;
+    int key;
+    if (!slot_at<L>(c, slots[i], head, tile, key)) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            x[j] = 0.f;
+    } else {
+        const uint8_t *base = (is_v ? c.v : c.k) + tile;
+        const int b = u >> 2, t = u >> 1, m0 = 8 * (u & 1);
+        if constexpr (KT == KV_F16) {
+            if (!is_v) {
+                load8((const _Float16 *)(base + L::k_unit(key, b, u & 3)), x);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    x[j] = h2f(*(const uint16_t *)(base + L::v_code(key, t, m0 + j)));
+            }
+        } else {
+            const float d = h2f(*(const uint16_t *)(base + (is_v ? L::v_scale(key, b) : L::k_scale(key, b))));
+            int q[8];
+            if constexpr (KT == KV_Q8) {
+                if (!is_v) {
+                    const uint2 w = *(const uint2 *)(base + L::k_unit(key, b, u & 3));
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        q[j] = (int)(((j < 4 ? w.x : w.y) >> (8 * (j & 3))) & 255u) - 128;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        q[j] = (int)base[L::v_code(key, t, m0 + j)] - 128;
+                }
+            } else {
+                if (!is_v) {
+                    const uint32_t w = *(const uint32_t *)(base + L::k_unit(key, b, u & 3));
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        q[j] = (int)((w >> (4 * j)) & 15u) - 8;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        q[j] = (int)((base[L::v_code(key, t, m0 + j)] >> (4 * (t & 1))) & 15u) - 8;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                x[j] = d * (float)q[j];
+        }
+    }
+    store8(out + ((int64_t)i * c.kv_heads + head) * c.head_dim + 8 * u, x);
+}
+
+// -------------------------------------------------------------------- move --
+
+// One workgroup moves the rows of one group, kv head and buffer: every source
+// piece into LDS, then every piece out.  K pieces are 8-dim units, V pieces
+// single codes (16 tokens share a 16-byte run), scales fp16 in both.
+template <int NB, int KT>
+__global__ void __launch_bounds__(256)
+move_kernel(KvView c, const int32_t *__restrict__ src, const int32_t *__restrict__ dst, int n)
+{
+    using L = KvLay<NB, KT>;
+    constexpr int KU = 4 * NB;                                   // K units of a row
+    constexpr int VB = KT == KV_F16 ? 2 : 1;                     // bytes of a V piece
+    constexpr int VU = KT == KV_Q4 ? L::DP / 2 : L::DP;          // V pieces of a row
+    constexpr int SC = KT == KV_F16 ? 0 : NB;
+    __shared__ __align__(16) uint8_t rows[KV_MOVE_MAX * 64 * NB];
+    const bool is_v = blockIdx.z != 0;
+    const int head = blockIdx.y;
+    src += (int64_t)blockIdx.x * n;
+    dst += (int64_t)blockIdx.x * n;
+    uint8_t *buf = is_v ? c.v : c.k;
+    const int pieces = (is_v ? VU : KU) + SC;
+#pragma unroll
+    for (int phase = 0; phase < 2; ++phase) {
+        for (int it = threadIdx.x; it < n * pieces; it += 256) {
+            const int i = it / pieces, p = it - i * pieces;
+            int64_t ts, td;
+            int ks, kd;
+            if (!slot_at<L>(c, src[i], head, ts, ks) || !slot_at<L>(c, dst[i], head, td, kd))
+                continue;
+            const int key = phase ? kd : ks;
+            uint8_t *base = buf + (phase ? td : ts), *loc = rows + i * (64 * NB);
+            if (p < SC) {
+                uint8_t *g = base + (is_v ? L::v_scale(key, p) : L::k_scale(key, p));
+                uint16_t *l = (uint16_t *)(loc + L::ROW_BYTES - 2 * NB) + p;
+                if (phase)
+                    *(uint16_t *)g = *l;
+                else
+                    *l = *(const uint16_t *)g;
+            } else if (!is_v) {
+                const int u = p - SC;
+                uint8_t *g = base + L::k_unit(key, u >> 2, u & 3);
+                uint32_t *l = (uint32_t *)(loc + u * L::UNIT);
+#pragma unroll
+                for (int w = 0; w < L::UNIT / 4; ++w) {
+                    if (phase)
+                        ((uint32_t *)g)[w] = l[w];
+                    else
+                        l[w] = ((const uint32_t *)g)[w];
+                }
+            } else {
+                const int u = p - SC, m = u & 15, t = KT == KV_Q4 ? 2 * (u >> 4) : u >> 4;
+                uint8_t *g = base + L::v_code(key, t, m), *l = loc + u * VB;
+                if constexpr (VB == 2) {
+                    if (phase)
+                        *(uint16_t *)g = *(const uint16_t *)l;
+                    else
+                        *(uint16_t *)l = *(const uint16_t *)g;
+                } else {
+                    if (phase)
+                        *g = *l;
+                    else
+                        *l = *g;
+                }
+            }
+        }
+        __syncthreads();
+    }
+}
+
+template <class F>
+hipError_t by_blocks(int nb, F f)
+{
+    switch (nb) {
+    case 2: return f(std::integral_constant<int, 2>());
+    case 3: return f(std::integral_constant<int, 3>());
+    case 4: return f(std::integral_constant<int, 4>());
+    case 8: return f(std::integral_constant<int, 8>());
+    default: return hipErrorInvalidValue;
+    }
+}
+
+template <class F>
+hipError_t by_type(int kt, F f)
+{
+    switch (kt) {
+    case KV_F16: return f(std::integral_constant<int, KV_F16>());
+    case KV_Q8: return f(std::integral_constant<int, KV_Q8>());
+    case KV_Q4: return f(std::integral_constant<int, KV_Q4>());
+    default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+hipError_t launch_rope_angles(const int32_t *pos, int64_t tokens, const double *freqs, int64_t pairs, double mag,
+                              float *cs, hipStream_t s)
+{
+    const int64_t total = tokens * pairs, groups = (total + 255) / 256;
+    hipLaunchKernelGGL(angles_kernel, dim3((unsigned)(groups < (1 << 20) ? groups : (1 << 20))), dim3(256), 0, s, pos,
+                       total, freqs, (uint32_t)pairs, mag, (float2 *)cs);
+    return hipGetLastError();
+}
+
+template <typename I>
+static hipError_t rope_of(const I *x, int64_t stride, int64_t tokens, int heads, int dim, const float *cs, int pairs,
+                          int inter, I *out, int64_t out_stride, hipStream_t s)
+{
+    const bool twin = !inter && (pairs & 7) == 0;
+    const int units = twin ? dim / 8 - pairs / 8 : inter ? dim / 8 : dim - pairs;
+    const int per = heads * units, tpb = per >= 256 ? 1 : 256 / per;
+    const int64_t grid = (tokens + tpb - 1) / tpb;
+    hipLaunchKernelGGL(rope_kernel<I>, dim3((unsigned)grid), dim3(256), 0, s, x, stride, tokens, heads, dim, cs, pairs,
+                       inter, out, out_stride, tpb, units);
+    return hipGetLastError();
+}
+
+hipError_t launch_rope(int half, const void *x, int64_t stride, int64_t tokens, int heads, int dim, const float *cs,
+                       int pairs, int inter, void *out, int64_t out_stride, hipStream_t s)
+{
+    if (half)
+        return rope_of((const _Float16 *)x, stride, tokens, heads, dim, cs, pairs, inter, (_Float16 *)out, out_stride, s);
+    return rope_of((const float *)x, stride, tokens, heads, dim, cs, pairs, inter, (float *)out, out_stride, s);
+}
+
+template <int NB, int KT, typename I>
+static hipError_t append_of(const KvView &c, const void *k, int64_t ks, const void *v, int64_t vs, int64_t tokens,
+                            const int32_t *slots, const float *cs, int pairs, int inter, hipStream_t s)
+{
+    constexpr int WIN = 256 / (2 * NB);
+    const dim3 grid((unsigned)((tokens + WIN - 1) / WIN), (unsigned)c.kv_heads, 2);
+    hipLaunchKernelGGL((append_kernel<NB, KT, I>), grid, dim3(256), 0, s, c, (const I *)k, ks, (const I *)v, vs, tokens,
+                       slots, cs, pairs, inter);
+    return hipGetLastError();
+}
+
+hipError_t launch_append(int kt, int half, const KvView &c, const void *k, int64_t ks, const void *v, int64_t vs,
+                         int64_t tokens, const int32_t *slots, const float *cs, int pairs, int inter, hipStream_t s)
+{
+    return by_type(kt, [&](auto T) {
+        return by_blocks(c.nb, [&](auto N) {
+            constexpr int KT = decltype(T)::value, NB = decltype(N)::value;
+            return half ? append_of<NB, KT, _Float16>(c, k, ks, v, vs, tokens, slots, cs, pairs, inter, s)
+                        : append_of<NB, KT, float>(c, k, ks, v, vs, tokens, slots, cs, pairs, inter, s);
+        });
+    });
+}
+
+hipError_t launch_read(int kt, int half, const KvView &c, const int32_t *slots, int64_t n, void *k_out, void *v_out,
+                       hipStream_t s)
+{
+    return by_type(kt, [&](auto T) {
+        return by_blocks(c.nb, [&](auto N) {
+            constexpr int KT = decltype(T)::value, NB = decltype(N)::value, ROWS = 256 / (4 * NB);
+            const dim3 grid((unsigned)((n + ROWS - 1) / ROWS), (unsigned)c.kv_heads, 2);
+            if (half)
+                hipLaunchKernelGGL((read_kernel<NB, KT, _Float16>), grid, dim3(256), 0, s, c, slots, n,
+                                   (_Float16 *)k_out, (_Float16 *)v_out);
+            else
+                hipLaunchKernelGGL((read_kernel<NB, KT, float>), grid, dim3(256), 0, s, c, slots, n, (float *)k_out,
+                                   (float *)v_out);
+            return hipGetLastError();
+        });
+    });
+}
+
+hipError_t launch_move(int kt, const KvView &c, const int32_t *src, const int32_t *dst, int64_t groups, int n,
+                       hipStream_t s)
+{
+    return by_type(kt, [&](auto T) {
+        return by_blocks(c.nb, [&](auto N) {
+            constexpr int KT = decltype(T)::value, NB = decltype(N)::value;
+            hipLaunchKernelGGL((move_kernel<NB, KT>), dim3((unsigned)groups, (unsigned)c.kv_heads, 2), dim3(256), 0, s,
+                               c, src, dst, n);
+            return hipGetLastError();
+        });
+    });
+}
+
+}  // namespace qmm

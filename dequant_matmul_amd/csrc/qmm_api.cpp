@@ -385,6 +385,7 @@ const char *qmm_status_str(int status)
     case QMM_ERR_SHAPE: return "invalid shape";
     case QMM_ERR_ALIGN: return "pointer not 16-byte aligned";
     case QMM_ERR_HIP: return "HIP launch error";
+    case QMM_ERR_WORKSPACE: return "workspace too small";
     default: return "unknown status";
     }
 }

@@ -97,7 +97,8 @@ typedef enum qmm_status {
     QMM_ERR_TYPE = 2,  /* unknown block type                             */
     QMM_ERR_SHAPE = 3, /* negative size, k not a block multiple, batch>8 */
     QMM_ERR_ALIGN = 4, /* a pointer is not 16-byte aligned               */
-    QMM_ERR_HIP = 5    /* the HIP runtime rejected a launch              */
+    QMM_ERR_HIP = 5,   /* the HIP runtime rejected a launch              */
+    QMM_ERR_WORKSPACE = 6 /* a workspace is smaller than the call needs  */
 } qmm_status;
 
 /* Elements per block (32 or 256); 0 for an unknown type. */
