@@ -229,158 +229,204 @@ constexpr float LOG2E = 1.44269504088896341f;
 // 2^-28 of the largest, whatever the size of V.  (F16 has no scale: exponent 0.)
 constexpr float P_TOP = 14.f;
 
-// Largest exponent e (value < 2^e, at least -14) of the fp16 scales in w[0..n),
-// of either sign.
-template <int N>
-__device__ __forceinline__ float scale_exponent(const uint32_t (*w)[8])
+// Largest exponent e (value < 2^e, at least -14) of the lane's fp16 scales, of
+// either sign.
+template <int NB>
+__device__ __forceinline__ float scale_exponent(const uint32_t (&w)[8 * NB])
 {
     typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
     u16x2 m = {0, 0};
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, w[i][j] & 0x7fff7fffu));
+    for (int i = 0; i < 8 * NB; ++i)
+        m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, w[i] & 0x7fff7fffu));
     const int top = m[0] > m[1] ? m[0] : m[1];
     const int e = top >> 10;
     return (float)((e > 1 ? e : 1) - 14);
 }
 
+// One row of q (r, a row of kv head `head`'s; nothing if r >= rows) as operand B:
+// this lane's eighth of every block, in PARTS fp16 parts.  Returns what the
+// products have to be multiplied by to be scores in base 2.  Two parts: the row
+// is scaled by a power of two so that both parts are normal numbers.
+template <int NB, int KT, int PARTS, typename IO>
+__device__ __forceinline__ float load_row(const AttnArgs &a, const Seq &s, int head, int r, int rows, int h,
+                                          h16x8 (&out)[PARTS][NB])
+{
+    using C = Codes<KT>;
+    const bool live = r < rows;
+    const int t = live ? r / a.group : 0, g = live ? r - t * a.group : 0;
+    const IO *row = (const IO *)a.q + (int64_t)(s.q0 + t) * a.q_stride + (int64_t)(head * a.group + g) * a.dim;
+    float x[NB][8];
+#pragma unroll
+    for (int bl = 0; bl < NB; ++bl) {
+        const int d0 = 32 * bl + 8 * h;
+        if (live && d0 < a.dim) {
+            read8(row + d0, x[bl]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                x[bl][j] = 0.f;
+        }
+    }
+    float scale;
+    if constexpr (PARTS == 2) {
+        float amax = 0.f;
+#pragma unroll
+        for (int bl = 0; bl < NB; ++bl)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                x[bl][j] *= a.scale * LOG2E;
+                amax = fmaxf(amax, fabsf(x[bl][j]));
+            }
+        amax = rows_max(amax);
+        int e;
+        (void)frexpf(amax, &e);
+        e = amax > 0.f && amax < 3.0e38f ? 15 - e : 0;      // maximum to [2^14, 2^15)
+        e = e < 120 ? e : 120;
+        scale = ldexpf(1.f, -e);
+#pragma unroll
+        for (int bl = 0; bl < NB; ++bl)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                x[bl][j] = ldexpf(x[bl][j], e);
+    } else {
+        scale = fmaxf(fabsf(a.scale) * LOG2E, 1e-37f);      // not 0: unseen tokens score -inf times it
+        if (a.scale < 0.f)
+#pragma unroll
+            for (int bl = 0; bl < NB; ++bl)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    x[bl][j] = -x[bl][j];
+    }
+#pragma unroll
+    for (int bl = 0; bl < NB; ++bl) {
+        uint32_t w[4], r[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const float y = x[bl][C::k_ord(2 * p)], z = x[bl][C::k_ord(2 * p + 1)];
+            w[p] = to_h2(y, z);
+            r[p] = rest_h2(y, z, w[p]);
+        }
+        out[0][bl] = as_h8(w[0], w[1], w[2], w[3]);
+        if constexpr (PARTS == 2)
+            out[1][bl] = as_h8(r[0], r[1], r[2], r[3]);
+    }
+    return scale;
+}
+
+// Which of the 16 tokens from position k0 on (a lane's) row `tok` of q sees;
+// nseen bounds them all.
+__device__ __forceinline__ uint32_t seen16(const AttnArgs &a, const Seq &s, int tok, int64_t k0, int64_t nseen)
+{
+    if (tok < 0)
+        return 0;
+    const int64_t rel = k0 - s.ctx, left = nseen - k0;
+    uint32_t bits;
+    if (a.mask) {
+        bits = mask16(a.mask + (int64_t)(s.q0 + tok) * a.mask_words, a.mask_words, rel);
+    } else {
+        const int64_t cnt = tok + 1 - rel;
+        bits = cnt <= 0 ? 0u : cnt >= 16 ? 0xffffu : (1u << cnt) - 1u;
+    }
+    return bits & (left <= 0 ? 0u : left >= 16 ? 0xffffu : (1u << left) - 1u);
+}
+
+// The scores of one row tile (products, factor rs; ev the exponent of the lane's
+// V scales) become weights relative to the running maximum m; l and o follow.
+template <int NB>
+__device__ __forceinline__ void soften(f32x4 (&sc)[4], float rs, float ev, float &m, float &l, f32x4 (&o)[2 * NB])
+{
+    float mx = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            mx = fmaxf(mx, sc[c][i]);
+    mx = rows_max(fmaf(mx, rs, ev));
+    const float mn = fmaxf(m, mx), mu = mn == -INFINITY ? 0.f : mn;
+    const float alpha = __builtin_amdgcn_exp2f(m - mu), shift = P_TOP - mu;
+    m = mn;
+    float sum = 0.f;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float p = __builtin_amdgcn_exp2f(fmaf(sc[c][i], rs, shift));
+            sc[c][i] = p;
+            sum += p;
+        }
+    l = fmaf(l, alpha, sum);
+    if (__any(alpha != 1.f)) {
+#pragma unroll
+        for (int t = 0; t < 2 * NB; ++t)
+            o[t] *= alpha;
+    }
+}
+
+// Weights of the eight tokens of contraction step st, times their V scales
+// (SCALED; vs: fp16 of the lane's 16 tokens), as operand B.
+template <int KT, int PARTS, bool SCALED>
+__device__ __forceinline__ void weights(const f32x4 (&sc)[4], const uint32_t *vs, int st, h16x8 &hi, h16x8 &lo)
+{
+    using C = Codes<KT>;
+    uint32_t w[4], r[4];
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        const int i = 8 * st + C::v_ord(2 * p), j = 8 * st + C::v_ord(2 * p + 1);
+        float y = sc[i >> 2][i & 3], z = sc[j >> 2][j & 3];
+        if constexpr (SCALED) {
+            y *= half_of(vs, i);
+            z *= half_of(vs, j);
+        }
+        w[p] = to_h2(y, z);
+        if constexpr (PARTS == 2)
+            r[p] = rest_h2(y, z, w[p]);
+    }
+    hi = as_h8(w[0], w[1], w[2], w[3]);
+    if constexpr (PARTS == 2)
+        lo = as_h8(r[0], r[1], r[2], r[3]);
+}
+
 // ---------------------------------------------------------------- the kernel --
 
-template <int NB, int KT, int RT, int PARTS, typename IO>
-__global__ void __launch_bounds__(256, RT >= 4 || NB > 4 ? 1 : 2)
+template <int NB, int KT, int PARTS, typename IO>
+__global__ void __launch_bounds__(256, NB > 4 ? 1 : 2)
 attn_kernel(AttnArgs a)
 {
     using L = KvLay<NB, KT>;
     using C = Codes<KT>;
-    constexpr int KDW = NB * L::UNIT / 4;              // dwords of a lane's K row piece of one row tile
-    constexpr int CDW = L::G * L::UNIT / 4;            // dwords of one load of it
+    constexpr int KDW = NB * L::UNIT / 4;              // dwords of a lane's K pieces of one row tile
+    constexpr int CDW = L::G * L::UNIT / 4;            // dwords of one load of them
     constexpr int VDW = KT == KV_F16 ? 8 : 4;          // dwords of a V piece
     constexpr int VN = KT == KV_Q4 ? NB : 2 * NB;      // V pieces
-    constexpr bool QREG = RT * PARTS * NB <= 16;       // Q fragments in registers, else in LDS
+    constexpr bool SCALED = KT != KV_F16;
 
     __shared__ __align__(16) f32x4 joined[4][2 * NB][64];
     __shared__ float join_m[4][16], join_l[4][16];
-    __shared__ __align__(16) h16x8 qlds[QREG ? 1 : RT * PARTS * NB][64];
-    __shared__ float qscale[RT][16];
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, h = lane >> 4;
     const int split = blockIdx.x, head = blockIdx.y % a.kv_heads, b = blockIdx.z;
-    const int r0 = (int)(blockIdx.y / a.kv_heads) * 16 * RT;
+    const int r0 = (int)(blockIdx.y / a.kv_heads) * 16;
 
     const Seq s = sequence(a, b);
     const int rows = (s.tq < a.max_q ? s.tq : a.max_q) * a.group;
     if (r0 >= rows)
         return;
-    const int last = ((rows < r0 + 16 * RT ? rows : r0 + 16 * RT) - 1) / a.group;
+    const int last = ((rows < r0 + 16 ? rows : r0 + 16) - 1) / a.group;
     const int64_t nseen = seen(a, s, last);
     const int ntiles = (int)((nseen + KV_TILE - 1) / KV_TILE);
     const int per = (ntiles + a.splits - 1) / a.splits;
     const int t_begin = split * per, t_end = t_begin + per < ntiles ? t_begin + per : ntiles;
 
-    // ---- the rows of q as operand B, scaled by a power of two per row so that
-    // both fp16 parts are normal numbers
-    h16x8 qreg[QREG ? RT * PARTS * NB : 1];
-    float rs[RT];
-    int tok[RT];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        const int r = r0 + 16 * rt + n;
-        tok[rt] = r < rows ? r / a.group : -1;
-        if (!QREG && rt % 4 != wave)
-            continue;
-        float x[NB][8], amax = 0.f;
-        const IO *row = (const IO *)a.q + (int64_t)(s.q0 + (r < rows ? tok[rt] : 0)) * a.q_stride +
-                        (int64_t)(head * a.group + (r < rows ? r % a.group : 0)) * a.dim;
-#pragma unroll
-        for (int bl = 0; bl < NB; ++bl) {
-            const int d0 = 32 * bl + 8 * h;
-            if (r < rows && d0 < a.dim) {
-                read8(row + d0, x[bl]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    x[bl][j] = 0.f;
-            }
-        }
-        float scale;
-        if constexpr (PARTS == 2) {
-#pragma unroll
-            for (int bl = 0; bl < NB; ++bl)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    x[bl][j] *= a.scale * LOG2E;
-                    amax = fmaxf(amax, fabsf(x[bl][j]));
-                }
-            amax = rows_max(amax);
-            int e;
-            (void)frexpf(amax, &e);
-            e = amax > 0.f && amax < 3.0e38f ? 15 - e : 0;      // maximum to [2^14, 2^15)
-            e = e < 120 ? e : 120;
-            scale = ldexpf(1.f, -e);
-#pragma unroll
-            for (int bl = 0; bl < NB; ++bl)
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    x[bl][j] = ldexpf(x[bl][j], e);
-        } else {
-            scale = fmaxf(fabsf(a.scale) * LOG2E, 1e-37f);      // not 0: unseen tokens score -inf times it
-            if (a.scale < 0.f)
-#pragma unroll
-                for (int bl = 0; bl < NB; ++bl)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        x[bl][j] = -x[bl][j];
-        }
-#pragma unroll
-        for (int bl = 0; bl < NB; ++bl) {
-            uint32_t w[4], r[4];
-#pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                const float y = x[bl][C::k_ord(2 * p)], z = x[bl][C::k_ord(2 * p + 1)];
-                w[p] = to_h2(y, z);
-                r[p] = rest_h2(y, z, w[p]);
-            }
-            const h16x8 hi = as_h8(w[0], w[1], w[2], w[3]), lo = as_h8(r[0], r[1], r[2], r[3]);
-            if constexpr (QREG) {
-                qreg[(rt * PARTS) * NB + bl] = hi;
-                if constexpr (PARTS == 2)
-                    qreg[(rt * PARTS + 1) * NB + bl] = lo;
-            } else {
-                qlds[(rt * PARTS) * NB + bl][lane] = hi;
-                if constexpr (PARTS == 2)
-                    qlds[(rt * PARTS + 1) * NB + bl][lane] = lo;
-            }
-        }
-        if constexpr (QREG)
-            rs[rt] = scale;
-        else if (h == 0)
-            qscale[rt][n] = scale;
-    }
-    if constexpr (!QREG) {
-        __syncthreads();
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-            rs[rt] = qscale[rt][n];
-    }
-    auto qf = [&](int rt, int part, int bl) -> h16x8 {
-        if constexpr (QREG)
-            return qreg[(rt * PARTS + part) * NB + bl];
-        else
-            return qlds[(rt * PARTS + part) * NB + bl][lane];
-    };
+    h16x8 qf[PARTS][NB];
+    const float rs = load_row<NB, KT, PARTS, IO>(a, s, head, r0 + n, rows, h, qf);
+    const int tok = r0 + n < rows ? (r0 + n) / a.group : -1;
 
-    f32x4 o[RT][2 * NB];
-    float m[RT], l[RT];
+    f32x4 o[2 * NB];
+    float m = -INFINITY, l = 0.f;
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        m[rt] = -INFINITY;
-        l[rt] = 0.f;
-#pragma unroll
-        for (int t = 0; t < 2 * NB; ++t)
-            o[rt][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
-    }
+    for (int t = 0; t < 2 * NB; ++t)
+        o[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
 
     const int32_t *pages = a.table + (int64_t)b * a.columns;
     const int tshift = a.page_shift - 6;
@@ -393,13 +439,13 @@ attn_kernel(AttnArgs a)
         const uint8_t *kp = a.k + at, *vp = a.v + at;
 
         // ---- every load of the tile
-        uint32_t kr[4][KDW], vr[VN][VDW], ks[KT == KV_F16 ? 1 : 8 * NB], vs[KT == KV_F16 ? 1 : NB][8];
+        uint32_t kr[4][KDW], vr[VN][VDW], ks[SCALED ? 8 * NB : 1], vs[SCALED ? 8 * NB : 1];
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
             for (int g = 0; g < NB / L::G; ++g)
                 load_dw<CDW>(kp + ((c * (NB / L::G) + g) * 64 + lane) * (L::G * L::UNIT), &kr[c][g * CDW]);
-        if constexpr (KT != KV_F16) {
+        if constexpr (SCALED) {
 #pragma unroll
             for (int i = 0; i < 2 * NB; ++i)
                 load_dw<4>(kp + L::CODE_BYTES + h * 32 * NB + 16 * i, &ks[4 * i]);
@@ -413,293 +459,192 @@ attn_kernel(AttnArgs a)
                 load_dw<4>(vp + (t * 64 + lane) * 16, &vr[t][0]);
             }
         }
-        if constexpr (KT != KV_F16) {
+        if constexpr (SCALED) {
 #pragma unroll
             for (int bl = 0; bl < NB; ++bl) {
-                load_dw<4>(vp + L::CODE_BYTES + (bl * 64 + 16 * h) * 2, &vs[bl][0]);
-                load_dw<4>(vp + L::CODE_BYTES + (bl * 64 + 16 * h) * 2 + 16, &vs[bl][4]);
+                load_dw<4>(vp + L::CODE_BYTES + (bl * 64 + 16 * h) * 2, &vs[8 * bl]);
+                load_dw<4>(vp + L::CODE_BYTES + (bl * 64 + 16 * h) * 2 + 16, &vs[8 * bl + 4]);
             }
         }
 
         // ---- scores
-        f32x4 sc[RT][4];
+        f32x4 sc[4];
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
+        for (int c = 0; c < 4; ++c)
+            sc[c] = (f32x4){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                sc[rt][c] = (f32x4){0.f, 0.f, 0.f, 0.f};
+        for (int c = 0; c < 4; ++c)
 #pragma unroll
-        for (int bl = 0; bl < NB; ++bl) {
-            h16x8 kf[4];
+            for (int bl = 0; bl < NB; ++bl) {
+                const h16x8 kf = C::k(&kr[c][bl * (L::UNIT / 4)]);
+                f32x4 acc = SCALED ? (f32x4){0.f, 0.f, 0.f, 0.f} : sc[c];
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                kf[c] = C::k(&kr[c][bl * (L::UNIT / 4)]);
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                const h16x8 q0 = qf(rt, 0, bl), q1 = qf(rt, PARTS - 1, bl);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if constexpr (KT == KV_F16) {
-                        sc[rt][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[c], q0, sc[rt][c], 0, 0, 0);
-                        if constexpr (PARTS == 2)
-                            sc[rt][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[c], q1, sc[rt][c], 0, 0, 0);
-                    } else {
-                        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-                        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[c], q0, acc, 0, 0, 0);
-                        if constexpr (PARTS == 2)
-                            acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[c], q1, acc, 0, 0, 0);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            sc[rt][c][i] = fmaf(acc[i], half_of(ks, (4 * c + i) * NB + bl), sc[rt][c][i]);
-                    }
-                }
-            }
-        }
-
-        // ---- the part of the tile that a row does not see; what lies behind the
-        // last token may be any bits: its scores are replaced, its V zeroed
-        const int64_t k0 = (int64_t)tile * KV_TILE;
-        const bool edge = k0 + KV_TILE > s.ctx;
-        if (edge) {
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                const int64_t rel = k0 + 16 * h - s.ctx;
-                uint32_t bits = 0;
-                if (tok[rt] >= 0) {
-                    if (a.mask) {
-                        bits = mask16(a.mask + (int64_t)(s.q0 + tok[rt]) * a.mask_words, a.mask_words, rel);
-                    } else {
-                        const int64_t cnt = tok[rt] + 1 - rel;
-                        bits = cnt <= 0 ? 0u : cnt >= 16 ? 0xffffu : (1u << cnt) - 1u;
-                    }
-                    const int64_t left = nseen - k0 - 16 * h;
-                    bits &= left <= 0 ? 0u : left >= 16 ? 0xffffu : (1u << left) - 1u;
-                }
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
+                for (int part = 0; part < PARTS; ++part)
+                    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[part][bl], acc, 0, 0, 0);
+                if constexpr (SCALED) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        sc[rt][c][i] = (bits >> (4 * c + i)) & 1u ? sc[rt][c][i] : -INFINITY;
-            }
-            if (k0 + KV_TILE > nseen) {
-                const int left = (int)(nseen - k0) - 16 * h;
-#pragma unroll
-                for (int w = 0; w < 8; ++w) {
-                    const uint32_t keep = (2 * w < left ? 0xffffu : 0u) | (2 * w + 1 < left ? 0xffff0000u : 0u);
-                    if constexpr (KT == KV_F16) {
-#pragma unroll
-                        for (int t = 0; t < VN; ++t)
-                            vr[t][w] &= keep;
-                    } else {
-#pragma unroll
-                        for (int bl = 0; bl < NB; ++bl)
-                            vs[bl][w] &= keep;
-                    }
+                        sc[c][i] = fmaf(acc[i], half_of(ks, (4 * c + i) * NB + bl), sc[c][i]);
+                } else {
+                    sc[c] = acc;
                 }
             }
-        }
 
-        // ---- running maximum and sum; P takes the place of the scores
-        float ev = 0.f;
-        if constexpr (KT != KV_F16)
-            ev = scale_exponent<NB>(vs);
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            float mx = -INFINITY;
+        // ---- the part of the tile that a row does not see; what lies behind the
+        // last token may be any bits: its scores are replaced, its V (scales)
+        // zeroed
+        const int64_t k0 = (int64_t)tile * KV_TILE;
+        if (k0 + KV_TILE > s.ctx) {
+            const uint32_t bits = seen16(a, s, tok, k0 + 16 * h, nseen);
 #pragma unroll
             for (int c = 0; c < 4; ++c)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    mx = fmaxf(mx, sc[rt][c][i]);
-            mx = rows_max(fmaf(mx, rs[rt], ev));
-            const float mn = fmaxf(m[rt], mx), mu = mn == -INFINITY ? 0.f : mn;
-            const float alpha = exp2f(m[rt] - mu), shift = P_TOP - mu;
-            m[rt] = mn;
-            float sum = 0.f;
+                    sc[c][i] = (bits >> (4 * c + i)) & 1u ? sc[c][i] : -INFINITY;
+        }
+        if (k0 + KV_TILE > nseen) {
+            const int left = (int)(nseen - k0) - 16 * h;
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+            for (int w = 0; w < 8; ++w) {
+                const uint32_t keep = (2 * w < left ? 0xffffu : 0u) | (2 * w + 1 < left ? 0xffff0000u : 0u);
+                if constexpr (SCALED) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float p = exp2f(fmaf(sc[rt][c][i], rs[rt], shift));
-                    sc[rt][c][i] = p;
-                    sum += p;
+                    for (int bl = 0; bl < NB; ++bl)
+                        vs[8 * bl + w] &= keep;
+                } else {
+#pragma unroll
+                    for (int t = 0; t < VN; ++t)
+                        vr[t][w] &= keep;
                 }
-            l[rt] = fmaf(l[rt], alpha, sum);
-            if (__any(alpha != 1.f)) {
-#pragma unroll
-                for (int t = 0; t < 2 * NB; ++t)
-                    o[rt][t] *= alpha;
             }
         }
+
+        float ev = 0.f;
+        if constexpr (SCALED)
+            ev = scale_exponent<NB>(vs);
+        soften<NB>(sc, rs, ev, m, l, o);
 
         // ---- output
 #pragma unroll
         for (int st = 0; st < 2; ++st) {
+            h16x8 hi, lo;
+            if constexpr (!SCALED)
+                weights<KT, PARTS, false>(sc, vs, st, hi, lo);
 #pragma unroll
             for (int bl = 0; bl < NB; ++bl) {
-                const h16x8 v0 = KT == KV_F16 ? C::v(&vr[2 * bl][4 * st], 0)
-                                 : KT == KV_Q8 ? C::v(&vr[2 * bl][2 * st], 0) : C::v(&vr[bl][2 * st], 0);
-                const h16x8 v1 = KT == KV_F16 ? C::v(&vr[VN > NB ? 2 * bl + 1 : 0][4 * st], 0)
-                                 : KT == KV_Q8 ? C::v(&vr[VN > NB ? 2 * bl + 1 : 0][2 * st], 0) : C::v(&vr[bl][2 * st], 1);
+                if constexpr (SCALED)
+                    weights<KT, PARTS, true>(sc, &vs[8 * bl], st, hi, lo);
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    uint32_t w[4], r[4];
-#pragma unroll
-                    for (int p = 0; p < 4; ++p) {
-                        const int i = 8 * st + C::v_ord(2 * p), j = 8 * st + C::v_ord(2 * p + 1);
-                        float y = sc[rt][i >> 2][i & 3], z = sc[rt][j >> 2][j & 3];
-                        if constexpr (KT != KV_F16) {
-                            y *= half_of(vs[bl], i);
-                            z *= half_of(vs[bl], j);
-                        }
-                        w[p] = to_h2(y, z);
-                        r[p] = rest_h2(y, z, w[p]);
-                    }
-                    const h16x8 hi = as_h8(w[0], w[1], w[2], w[3]), lo = as_h8(r[0], r[1], r[2], r[3]);
-                    o[rt][2 * bl] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, hi, o[rt][2 * bl], 0, 0, 0);
-                    o[rt][2 * bl + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, hi, o[rt][2 * bl + 1], 0, 0, 0);
-                    if constexpr (PARTS == 2) {
-                        o[rt][2 * bl] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, lo, o[rt][2 * bl], 0, 0, 0);
-                        o[rt][2 * bl + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, lo, o[rt][2 * bl + 1], 0, 0, 0);
-                    }
+                for (int u = 0; u < 2; ++u) {
+                    const h16x8 vf = KT == KV_F16  ? C::v(&vr[VN > NB ? 2 * bl + u : 0][VDW > 4 ? 4 * st : 0], 0)
+                                     : KT == KV_Q8 ? C::v(&vr[VN > NB ? 2 * bl + u : 0][2 * st], 0)
+                                                   : C::v(&vr[bl][2 * st], u);
+                    o[2 * bl + u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, hi, o[2 * bl + u], 0, 0, 0);
+                    if constexpr (PARTS == 2)
+                        o[2 * bl + u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, lo, o[2 * bl + u], 0, 0, 0);
                 }
             }
         }
     }
 
-    // ---- join the four waves, one row tile at a time; every wave then finishes
-    // every fourth 16-dim tile
+    // ---- join the four waves; every wave then finishes every fourth 16-dim tile
     const int64_t wrows = (int64_t)a.tokens * a.heads;
+    const float lsum = rows_sum(l);
+    if (h == 0) {
+        join_m[wave][n] = m;
+        join_l[wave][n] = lsum;
+    }
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        if (rt > 0)
-            __syncthreads();
-        const float lsum = rows_sum(l[rt]);
-        if (h == 0) {
-            join_m[wave][n] = m[rt];
-            join_l[wave][n] = lsum;
+    for (int t = 0; t < 2 * NB; ++t)
+        joined[wave][t][lane] = o[t];
+    __syncthreads();
+    float mm = -INFINITY, w[4], lt = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        mm = fmaxf(mm, join_m[i][n]);
+    const float mu = mm == -INFINITY ? 0.f : mm;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w[i] = __builtin_amdgcn_exp2f(join_m[i][n] - mu);
+        lt = fmaf(w[i], join_l[i][n], lt);
+    }
+    if (tok >= 0) {
+        const int hq = head * a.group + (r0 + n - tok * a.group);
+        const int64_t row = (int64_t)(s.q0 + tok) * a.heads + hq;
+        const float inv = lt > 0.f ? 1.f / lt : 0.f;
+        for (int t = wave; t < 2 * NB; t += 4) {
+            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                acc += joined[i][t][lane] * w[i];
+            const int d0 = 16 * t + 4 * h;
+            if (a.splits > 1)
+                *(f32x4 *)(a.ws + ((int64_t)split * wrows + row) * L::DP + d0) = acc;
+            else if (d0 < a.dim)
+                write4((IO *)a.out + (int64_t)(s.q0 + tok) * a.out_stride + (int64_t)hq * a.dim + d0, acc * inv);
         }
-#pragma unroll
-        for (int t = 0; t < 2 * NB; ++t)
-            joined[wave][t][lane] = o[rt][t];
-        __syncthreads();
-        float mm = -INFINITY, w[4], lt = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            mm = fmaxf(mm, join_m[i][n]);
-        const float mu = mm == -INFINITY ? 0.f : mm;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            w[i] = exp2f(join_m[i][n] - mu);
-            lt = fmaf(w[i], join_l[i][n], lt);
-        }
-        if (tok[rt] >= 0) {
-            const int r = r0 + 16 * rt + n, hq = head * a.group + (r - tok[rt] * a.group);
-            const int64_t row = (int64_t)(s.q0 + tok[rt]) * a.heads + hq;
-            const float inv = lt > 0.f ? 1.f / lt : 0.f;
-            for (int t = wave; t < 2 * NB; t += 4) {
-                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    acc += joined[i][t][lane] * w[i];
-                const int d0 = 16 * t + 4 * h;
-                if (a.splits > 1)
-                    *(f32x4 *)(a.ws + ((int64_t)split * wrows + row) * L::DP + d0) = acc;
-                else if (d0 < a.dim)
-                    write4((IO *)a.out + (int64_t)(s.q0 + tok[rt]) * a.out_stride + (int64_t)hq * a.dim + d0, acc * inv);
-            }
-            if (a.splits > 1 && wave == 0 && h == 0) {
-                float2 *ml = (float2 *)(a.ws + (int64_t)a.splits * wrows * L::DP) + (int64_t)split * wrows + row;
-                *ml = make_float2(mm, lt);
-            }
+        if (a.splits > 1 && wave == 0 && h == 0) {
+            float2 *ml = (float2 *)(a.ws + (int64_t)a.splits * wrows * L::DP) + (int64_t)split * wrows + row;
+            *ml = make_float2(mm, lt);
         }
     }
 }
 
 // ------------------------------------------------------- joining the splits --
 
-// A quarter of a wave row: each thread takes 4 dims of one row of q.  blockIdx.y
-// is the sequence, so that rows of no sequence are left alone; splits that saw
-// nothing wrote l = 0 and (for all this kernel knows) no output.
+// `slices` groups of 8 * NB threads share a row of q, each taking every
+// slices-th split for 4 dims a thread.  blockIdx.y is the sequence, so that rows
+// of no sequence are left alone; splits that saw nothing wrote l = 0.
 template <int NB, typename IO>
 __global__ void __launch_bounds__(256)
-attn_join_kernel(AttnArgs a)
+attn_join_kernel(AttnArgs a, int slices)
 {
-    constexpr int PER = 8 * NB, ROWS = 256 / PER;
-    const int r = threadIdx.x / PER, d0 = 4 * (threadIdx.x % PER);
+    constexpr int PER = 8 * NB;
+    __shared__ __align__(16) f32x4 part[256];
+    __shared__ float part_l[256];
+    const int u = threadIdx.x / PER, d0 = 4 * (threadIdx.x % PER);
+    const int here = 256 / PER / slices, r = u / slices, slice = u - r * slices;
     const Seq s = sequence(a, blockIdx.y);
-    const int64_t i = (int64_t)blockIdx.x * ROWS + r;
+    const int64_t i = (int64_t)blockIdx.x * here + r;
     const int64_t rows = (int64_t)(s.tq < a.max_q ? s.tq : a.max_q) * a.heads;
-    if (r >= ROWS || i >= rows || d0 >= a.dim)
-        return;
+    const bool live = r < here && i < rows;
     const int64_t wrows = (int64_t)a.tokens * a.heads, row = (int64_t)s.q0 * a.heads + i;
-    const float2 *ml = (const float2 *)(a.ws + (int64_t)a.splits * wrows * (32 * NB)) + row;
-    float mm = -INFINITY;
-    for (int sp = 0; sp < a.splits; ++sp)
-        mm = fmaxf(mm, ml[sp * wrows].x);
-    const float mu = mm == -INFINITY ? 0.f : mm;
-    float lt = 0.f;
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    float lt = 0.f;
+    if (live) {
+        const float2 *ml = (const float2 *)(a.ws + (int64_t)a.splits * wrows * PER * 4) + row;
+        float mm = -INFINITY;
+#pragma unroll 8
+        for (int sp = 0; sp < a.splits; ++sp)
+            mm = fmaxf(mm, ml[sp * wrows].x);
+        const float mu = mm == -INFINITY ? 0.f : mm;
 #pragma unroll 4
-    for (int sp = 0; sp < a.splits; ++sp) {
-        const float2 x = ml[sp * wrows];
-        const f32x4 part = *(const f32x4 *)(a.ws + (sp * wrows + row) * (32 * NB) + d0);
-        const float w = exp2f(x.x - mu);
-        if (x.y > 0.f) {
-            lt = fmaf(w, x.y, lt);
-            acc += part * w;
+        for (int sp = slice; sp < a.splits; sp += slices) {
+            const float2 x = ml[sp * wrows];
+            const f32x4 y = *(const f32x4 *)(a.ws + (sp * wrows + row) * (PER * 4) + d0);
+            const float w = __builtin_amdgcn_exp2f(x.x - mu);
+            if (x.y > 0.f) {
+                lt = fmaf(w, x.y, lt);
+                acc += y * w;
+            }
         }
     }
+    if (slices > 1) {
+        part[threadIdx.x] = acc;
+        part_l[threadIdx.x] = lt;
+        __syncthreads();
+        if (slice > 0)
+            return;
+        for (int k = 1; live && k < slices; ++k) {
+            acc += part[threadIdx.x + k * PER];
+            lt += part_l[threadIdx.x + k * PER];
+        }
+    }
+    if (!live || d0 >= a.dim)
+        return;
     const float inv = lt > 0.f ? 1.f / lt : 0.f;
     const int64_t t = i / a.heads;
     write4((IO *)a.out + (s.q0 + t) * a.out_stride + (i - t * a.heads) * a.dim + d0, acc * inv);
-}
-
-// ------------------------------------------------------------------- launch --
-
-template <int NB, int KT, int RT, typename IO>
-hipError_t attn_rows(const AttnArgs &a, const dim3 &grid, hipStream_t s)
-{
-    constexpr int PARTS = sizeof(IO) == 4 ? 2 : 1;
-    hipLaunchKernelGGL((attn_kernel<NB, KT, RT, PARTS, IO>), grid, dim3(256), 0, s, a);
-    return hipGetLastError();
-}
-
-template <int NB, int KT, typename IO>
-hipError_t attn_blocks(const AttnArgs &a, const AttnPlan &p, int64_t batch, hipStream_t s)
-{
-    const dim3 grid((unsigned)p.splits, (unsigned)(a.kv_heads * p.groups), (unsigned)batch);
-    hipError_t e = hipErrorInvalidValue;
-    if (p.rt == 1)
-        e = attn_rows<NB, KT, 1, IO>(a, grid, s);
-    else if (p.rt == 2)
-        e = attn_rows<NB, KT, 2, IO>(a, grid, s);
-    else if constexpr (NB <= 4)
-        e = attn_rows<NB, KT, 4, IO>(a, grid, s);
-    if (e != hipSuccess || p.splits == 1)
-        return e;
-    constexpr int ROWS = 256 / (8 * NB);
-    const int64_t most = (a.max_q < a.tokens ? a.max_q : a.tokens) * (int64_t)a.heads;
-    hipLaunchKernelGGL((attn_join_kernel<NB, IO>), dim3((unsigned)((most + ROWS - 1) / ROWS), (unsigned)batch), dim3(256),
-                       0, s, a);
-    return hipGetLastError();
-}
-
-// One translation unit per cache type.
-template <int KT>
-hipError_t attn_type(const AttnArgs &a, const AttnPlan &p, int64_t batch, int nb, int half, hipStream_t s)
-{
-    switch (nb) {
-#define QKV_CASE(N)                                                                                              \
-    case N:                                                                                                      \
-        return half ? attn_blocks<N, KT, _Float16>(a, p, batch, s) : attn_blocks<N, KT, float>(a, p, batch, s)
-        QKV_CASE(2);
-        QKV_CASE(3);
-        QKV_CASE(4);
-        QKV_CASE(8);
-#undef QKV_CASE
-    default: return hipErrorInvalidValue;
-    }
 }
 
 hipError_t attn_f16(const AttnArgs &a, const AttnPlan &p, int64_t batch, int nb, int half, hipStream_t s);

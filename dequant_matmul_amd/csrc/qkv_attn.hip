@@ -7,8 +7,8 @@ AttnPlan attn_plan(const KvView &c, int64_t tokens, int64_t batch, int heads, in
 {
     AttnPlan p;
     const int64_t rows = max_q * (heads / c.kv_heads);
-    p.rt = rows <= 16 ? 1 : rows <= 32 || c.nb > 4 ? 2 : 4;
-    p.groups = (int)((rows + 16 * p.rt - 1) / (16 * p.rt));
+    p.rows = rows <= 16 ? 16 : rows <= 64 || !half || c.nb > 4 ? 64 : 128;
+    p.groups = (int)((rows + p.rows - 1) / p.rows);
     const int64_t tiles = (max_ctx + KV_TILE - 1) / KV_TILE;
     const int64_t wgs = batch * c.kv_heads * p.groups;
     const int cus = device_cu_count() > 0 ? device_cu_count() : 256;

@@ -1,6 +1,6 @@
-// qkv_attn_q8.hip -- the attention kernels of qkv_attn.h for one cache type (a
+// qkv_attn_q8.hip -- the attention kernels for one cache type (a
 // translation unit each, so that they compile side by side).
-#include "qkv_attn.h"
+#include "qkv_attn_rows.h"
 
 namespace qmm {
 

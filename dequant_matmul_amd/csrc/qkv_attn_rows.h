@@ -1,0 +1,370 @@
+// qkv_attn_rows.h -- attention of many query rows over the paged cache: trees
+// and prompt chunks whose rows (new tokens times heads of a kv head) exceed one
+// 16-row tile.
+//
+// As attn_kernel, but the four waves of a workgroup hold different rows (RT
+// tiles of 16 each) and walk the same tiles of 64 tokens: a tile is decoded once
+// into LDS, as fp16 operand fragments, for all of them.  Two LDS buffers: the
+// global loads of the next tile run under the products of this one, one barrier a
+// tile.
+//   PARTS 1 (fp16 rows): K and V are decoded with their scales, rounded to fp16
+//     once (exact for an F16 cache): a scale per weight and score would cost the
+//     VALU more than the whole softmax.
+//   PARTS 2 (fp32 rows): LDS holds the exact codes, the scales beside them; scores
+//     and weights are scaled in fp32 as in attn_kernel.
+#pragma once
+
+#include "qkv_attn.h"
+
+namespace qmm {
+
+template <int NB, int KT, int RT, int PARTS, typename IO>
+__global__ void __launch_bounds__(256, NB > 4 ? 1 : 2)
+attn_rows_kernel(AttnArgs a)
+{
+    using L = KvLay<NB, KT>;
+    using C = Codes<KT>;
+    constexpr bool SCALED = KT != KV_F16 && PARTS == 2;     // scales stay apart
+    constexpr bool FOLDED = KT != KV_F16 && PARTS == 1;     // scales go into the fragments
+    constexpr int CDW = L::G * L::UNIT / 4;                 // dwords of a lane's K piece
+    constexpr int KN = 4 * NB / L::G, KI = (KN + 3) / 4;    // K pieces of a tile, of a wave
+    constexpr int VN = KT == KV_F16 ? 4 * NB : KT == KV_Q8 ? 2 * NB : NB, VI = (VN + 3) / 4;
+    constexpr int SDW = (L::G + 1) / 2;                     // dwords of a K piece's scales
+
+    __shared__ __align__(16) h16x8 kb[2][4 * NB][64], vb[2][4 * NB][64];
+    __shared__ __align__(16) uint32_t kscale[2][SCALED ? 32 * NB : 4], vscale[2][SCALED ? 32 * NB : 4];
+
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, h = lane >> 4;
+    const int split = blockIdx.x, head = blockIdx.y % a.kv_heads, b = blockIdx.z;
+    const int g0 = (int)(blockIdx.y / a.kv_heads) * 64 * RT, r0 = g0 + wave * 16 * RT;
+
+    const Seq s = sequence(a, b);
+    const int rows = (s.tq < a.max_q ? s.tq : a.max_q) * a.group;
+    if (g0 >= rows)
+        return;
+    const int last = ((rows < g0 + 64 * RT ? rows : g0 + 64 * RT) - 1) / a.group;
+    const int64_t nseen = seen(a, s, last);
+    const int ntiles = (int)((nseen + KV_TILE - 1) / KV_TILE);
+    const int per = (ntiles + a.splits - 1) / a.splits;
+    const int t_begin = split * per, t_end = t_begin + per < ntiles ? t_begin + per : ntiles;
+    // tiles that this wave's rows see something of
+    const int my_last = ((rows < r0 + 16 * RT ? rows : r0 + 16 * RT) - 1) / a.group;
+    const int my_end = r0 >= rows ? 0 : (int)((seen(a, s, my_last) + KV_TILE - 1) / KV_TILE);
+
+    h16x8 qf[RT][PARTS][NB];
+    float rs[RT], m[RT], l[RT];
+    int tok[RT];
+    f32x4 o[RT][2 * NB];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        const int r = r0 + 16 * rt + n;
+        rs[rt] = load_row<NB, KT, PARTS, IO>(a, s, head, r, rows, h, qf[rt]);
+        tok[rt] = r < rows ? r / a.group : -1;
+        m[rt] = -INFINITY;
+        l[rt] = 0.f;
+#pragma unroll
+        for (int t = 0; t < 2 * NB; ++t)
+            o[rt][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    }
+
+    // ---- staging: a tile's pieces, dealt to the waves
+    uint32_t kr[KI][CDW], kd[FOLDED ? KI : 1][SDW], vr[VI][4], vd[FOLDED ? VI : 1][8], sd[4];
+    const int32_t *pages = a.table + (int64_t)b * a.columns;
+    const int tshift = a.page_shift - 6;
+
+    auto load_tile = [&](int tile) -> bool {
+        const int page = pages[tile >> tshift];
+        if (page < 0 || page >= a.pages)
+            return false;                               // nothing of it is seen
+        const int64_t at = ((((int64_t)page * a.kv_heads + head) << tshift) + (tile & ((1 << tshift) - 1))) *
+                           (int64_t)L::TILE_BYTES;
+        const uint8_t *kp = a.k + at, *vp = a.v + at;
+#pragma unroll
+        for (int i = 0; i < KI; ++i) {
+            const int j = wave + 4 * i;
+            if (KN % 4 == 0 || j < KN) {
+                load_dw<CDW>(kp + (j * 64 + lane) * (L::G * L::UNIT), kr[i]);
+                if constexpr (FOLDED) {
+                    const int c = j / (NB / L::G), key = 16 * (n >> 2) + 4 * c + (n & 3);
+                    const uint16_t *sp = (const uint16_t *)(kp + L::k_scale(key, (j % (NB / L::G)) * L::G));
+#pragma unroll
+                    for (int w = 0; w < SDW; ++w)
+                        kd[i][w] = 2 * w + 1 < L::G ? sp[2 * w] | (uint32_t)sp[2 * w + 1] << 16 : sp[2 * w];
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < VI; ++i) {
+            const int j = wave + 4 * i;
+            if (VN % 4 == 0 || j < VN) {
+                load_dw<4>(vp + (j * 64 + lane) * 16, vr[i]);
+                if constexpr (FOLDED) {
+                    const uint8_t *sp = vp + L::v_scale(16 * h, KT == KV_Q8 ? j >> 1 : j);
+                    load_dw<4>(sp, &vd[i][0]);
+                    load_dw<4>(sp + 16, &vd[i][4]);
+                }
+            }
+        }
+        if constexpr (SCALED) {
+            const int t = threadIdx.x;
+            if (t < 16 * NB)
+                load_dw<4>((t < 8 * NB ? kp + 16 * t : vp + 16 * (t - 8 * NB)) + L::CODE_BYTES, sd);
+        }
+        return true;
+    };
+
+    // what lies behind the last token may be any bits: V (or its scale) becomes 0
+    auto keep_pair = [&](int left, int i, int j) -> uint32_t {
+        return (i < left ? 0xffffu : 0u) | (j < left ? 0xffff0000u : 0u);
+    };
+    auto store_tile = [&](int buf, int tile) {
+        const int64_t rest = nseen - (int64_t)tile * KV_TILE;
+        const int left = (int)(rest < KV_TILE ? rest : KV_TILE) - 16 * h;
+        const bool tail = rest < KV_TILE;
+#pragma unroll
+        for (int i = 0; i < KI; ++i) {
+            const int j = wave + 4 * i;
+            if (KN % 4 == 0 || j < KN) {
+#pragma unroll
+                for (int u = 0; u < L::G; ++u) {
+                    h16x8 f = C::k(&kr[i][u * (L::UNIT / 4)]);
+                    if constexpr (FOLDED)
+                        f *= (h16x8)(as_h2(kd[i][u >> 1])[u & 1]);
+                    kb[buf][j * L::G + u][lane] = f;
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < VI; ++i) {
+            const int j = wave + 4 * i;
+            if (VN % 4 == 0 || j < VN) {
+                constexpr int FR = KT == KV_F16 ? 1 : KT == KV_Q8 ? 2 : 4;   // fragments of a piece
+#pragma unroll
+                for (int f = 0; f < FR; ++f) {
+                    // fragment (dim tile, step) of the piece
+                    const int st = KT == KV_F16 ? 0 : f & 1, hi = f >> 1;
+                    h16x8 x = C::v(&vr[i][KT == KV_F16 ? 0 : 2 * st], hi);
+                    if constexpr (FOLDED) {
+                        const uint32_t *d = &vd[i][4 * st];
+                        h16x8 dv;
+                        if constexpr (KT == KV_Q8)
+                            dv = as_h8(d[0], d[1], d[2], d[3]);
+                        else
+                            dv = as_h8(__builtin_amdgcn_perm(d[1], d[0], 0x05040100u),
+                                       __builtin_amdgcn_perm(d[1], d[0], 0x07060302u),
+                                       __builtin_amdgcn_perm(d[3], d[2], 0x05040100u),
+                                       __builtin_amdgcn_perm(d[3], d[2], 0x07060302u));
+                        x *= dv;
+                    }
+                    if (!SCALED && tail) {
+                        u32x4 y = __builtin_bit_cast(u32x4, x);
+                        const int first = 8 * (KT == KV_F16 ? j & 1 : st);
+#pragma unroll
+                        for (int p = 0; p < 4; ++p)
+                            y[p] &= keep_pair(left, first + C::v_ord(2 * p), first + C::v_ord(2 * p + 1));
+                        x = __builtin_bit_cast(h16x8, y);
+                    }
+                    // [dim tile][step]
+                    const int at = KT == KV_F16 ? j : KT == KV_Q8 ? 2 * j + st : 4 * j + 2 * hi + st;
+                    vb[buf][at][lane] = x;
+                }
+            }
+        }
+        if constexpr (SCALED) {
+            const int t = threadIdx.x;
+            if (t < 8 * NB) {
+                *(u32x4 *)&kscale[buf][4 * t] = (u32x4){sd[0], sd[1], sd[2], sd[3]};
+            } else if (t < 16 * NB) {
+                // 16 bytes are tokens 8 (t % 8) .. of block t / 8
+                const int key0 = 8 * ((t - 8 * NB) & 7), room = (int)(rest < KV_TILE ? rest : KV_TILE) - key0;
+                u32x4 y;
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+                    y[w] = sd[w] & keep_pair(room, 2 * w, 2 * w + 1);
+                *(u32x4 *)&vscale[buf][4 * (t - 8 * NB)] = y;
+            }
+        }
+    };
+
+    auto compute = [&](int buf, int tile) {
+        const int64_t k0 = (int64_t)tile * KV_TILE;
+        f32x4 sc[RT][4];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                sc[rt][c] = (f32x4){0.f, 0.f, 0.f, 0.f};
+        uint32_t ks[SCALED ? 8 * NB : 1];
+        if constexpr (SCALED) {
+#pragma unroll
+            for (int i = 0; i < 2 * NB; ++i) {
+                const u32x4 y = *(const u32x4 *)&kscale[buf][8 * NB * h + 4 * i];
+                ks[4 * i] = y[0]; ks[4 * i + 1] = y[1]; ks[4 * i + 2] = y[2]; ks[4 * i + 3] = y[3];
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int bl = 0; bl < NB; ++bl) {
+                const h16x8 kf = kb[buf][c * NB + bl][lane];
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    f32x4 acc = SCALED ? (f32x4){0.f, 0.f, 0.f, 0.f} : sc[rt][c];
+#pragma unroll
+                    for (int part = 0; part < PARTS; ++part)
+                        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[rt][part][bl], acc, 0, 0, 0);
+                    if constexpr (SCALED) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            sc[rt][c][i] = fmaf(acc[i], half_of(ks, (4 * c + i) * NB + bl), sc[rt][c][i]);
+                    } else {
+                        sc[rt][c] = acc;
+                    }
+                }
+            }
+        if (k0 + KV_TILE > s.ctx) {
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                const uint32_t bits = seen16(a, s, tok[rt], k0 + 16 * h, nseen);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        sc[rt][c][i] = (bits >> (4 * c + i)) & 1u ? sc[rt][c][i] : -INFINITY;
+            }
+        }
+        uint32_t vs[SCALED ? 8 * NB : 1];
+        float ev = 0.f;
+        if constexpr (SCALED) {
+#pragma unroll
+            for (int bl = 0; bl < NB; ++bl)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const u32x4 y = *(const u32x4 *)&vscale[buf][32 * bl + 8 * h + 4 * i];
+                    vs[8 * bl + 4 * i] = y[0]; vs[8 * bl + 4 * i + 1] = y[1];
+                    vs[8 * bl + 4 * i + 2] = y[2]; vs[8 * bl + 4 * i + 3] = y[3];
+                }
+            ev = scale_exponent<NB>(vs);
+        }
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+            soften<NB>(sc[rt], rs[rt], ev, m[rt], l[rt], o[rt]);
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+            h16x8 hi[RT], lo[RT];
+            if constexpr (!SCALED) {
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+                    weights<KT, PARTS, false>(sc[rt], vs, st, hi[rt], lo[rt]);
+            }
+#pragma unroll
+            for (int bl = 0; bl < NB; ++bl) {
+                if constexpr (SCALED) {
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt)
+                        weights<KT, PARTS, true>(sc[rt], &vs[8 * bl], st, hi[rt], lo[rt]);
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int t = 2 * bl + u;
+                    const h16x8 vf = vb[buf][2 * t + st][lane];
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) {
+                        o[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, hi[rt], o[rt][t], 0, 0, 0);
+                        if constexpr (PARTS == 2)
+                            o[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, lo[rt], o[rt][t], 0, 0, 0);
+                    }
+                }
+            }
+        }
+    };
+
+    // ---- the tiles; `live` is the same in every wave
+    bool live = t_begin < t_end && load_tile(t_begin);
+    if (live)
+        store_tile(0, t_begin);
+    __syncthreads();
+    for (int tile = t_begin; tile < t_end; ++tile) {
+        const int buf = (tile - t_begin) & 1;
+        const bool next = tile + 1 < t_end && load_tile(tile + 1);
+        if (live && tile < my_end)
+            compute(buf, tile);
+        if (next)
+            store_tile(buf ^ 1, tile + 1);
+        live = next;
+        __syncthreads();
+    }
+
+    // ---- this wave's rows
+    const int64_t wrows = (int64_t)a.tokens * a.heads;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        const float lt = rows_sum(l[rt]);
+        if (tok[rt] < 0)
+            continue;
+        const int hq = head * a.group + (r0 + 16 * rt + n - tok[rt] * a.group);
+        const int64_t row = (int64_t)(s.q0 + tok[rt]) * a.heads + hq;
+        const float inv = lt > 0.f ? 1.f / lt : 0.f;
+        IO *dst = (IO *)a.out + (int64_t)(s.q0 + tok[rt]) * a.out_stride + (int64_t)hq * a.dim;
+#pragma unroll
+        for (int t = 0; t < 2 * NB; ++t) {
+            const int d0 = 16 * t + 4 * h;
+            if (a.splits > 1)
+                *(f32x4 *)(a.ws + ((int64_t)split * wrows + row) * L::DP + d0) = o[rt][t];
+            else if (d0 < a.dim)
+                write4(dst + d0, o[rt][t] * inv);
+        }
+        if (a.splits > 1 && h == 0) {
+            float2 *ml = (float2 *)(a.ws + (int64_t)a.splits * wrows * L::DP) + (int64_t)split * wrows + row;
+            *ml = make_float2(m[rt], lt);
+        }
+    }
+}
+
+// ------------------------------------------------------------------- launch --
+
+template <int NB, int KT, typename IO>
+hipError_t attn_blocks(const AttnArgs &a, const AttnPlan &p, int64_t batch, hipStream_t s)
+{
+    constexpr int PARTS = sizeof(IO) == 4 ? 2 : 1;
+    const dim3 grid((unsigned)p.splits, (unsigned)(a.kv_heads * p.groups), (unsigned)batch);
+    if (p.rows == 16)
+        hipLaunchKernelGGL((attn_kernel<NB, KT, PARTS, IO>), grid, dim3(256), 0, s, a);
+    else if (p.rows == 64)
+        hipLaunchKernelGGL((attn_rows_kernel<NB, KT, 1, PARTS, IO>), grid, dim3(256), 0, s, a);
+    else if constexpr (PARTS == 1 && NB <= 4)
+        hipLaunchKernelGGL((attn_rows_kernel<NB, KT, 2, PARTS, IO>), grid, dim3(256), 0, s, a);
+    else
+        return hipErrorInvalidValue;
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.splits == 1)
+        return e;
+    constexpr int PER = 8 * NB, MOST = 256 / PER;
+    int slices = 1;
+    while (slices * 2 <= MOST && slices * 4 <= p.splits)
+        slices *= 2;
+    const int here = MOST / slices;
+    const int64_t rows = (int64_t)a.max_q * a.heads;
+    hipLaunchKernelGGL((attn_join_kernel<NB, IO>), dim3((unsigned)((rows + here - 1) / here), (unsigned)batch), dim3(256),
+                       0, s, a, slices);
+    return hipGetLastError();
+}
+
+// One translation unit per cache type.
+template <int KT>
+hipError_t attn_type(const AttnArgs &a, const AttnPlan &p, int64_t batch, int nb, int half, hipStream_t s)
+{
+    switch (nb) {
+#define QKV_CASE(N)                                                                                              \
+    case N:                                                                                                      \
+        return half ? attn_blocks<N, KT, _Float16>(a, p, batch, s) : attn_blocks<N, KT, float>(a, p, batch, s)
+        QKV_CASE(2);
+        QKV_CASE(3);
+        QKV_CASE(4);
+        QKV_CASE(8);
+#undef QKV_CASE
+    default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace qmm

@@ -37,10 +37,10 @@ struct AttnCall {
     float scale;
 };
 
-// How a call is cut up: rows of q (token, head of the group) come in groups of
-// 16 * rt, the tokens of a sequence in `splits` parts.
+// How a call is cut up: the rows of a kv head (new tokens times heads of the
+// group) come in groups of `rows`, the tokens of a sequence in `splits` parts.
 struct AttnPlan {
-    int rt;         // 16-row tiles of a workgroup
+    int rows;       // of a workgroup: 16 (attn_kernel), 64 or 128 (attn_rows_kernel)
     int groups;     // row groups of a kv head
     int splits;
     int64_t bytes;  // workspace

@@ -267,7 +267,10 @@ def test_strided_rows_and_uniform_sequences(dt):
     q.attention(c.cache, view, up(c.table), ctx, out=out)
     c.check(out, dt)
     assert (outw[:, :64] == 7).all()
-    assert torch.equal(out, q.attention(c.cache, up(c.q).to(dt), up(c.table), ctx, qstart=up(c.starts)))
+    # given starts and the same bound on the new tokens it is the same call;
+    # without the bound other kernels may run, within the same bar
+    assert torch.equal(out, q.attention(c.cache, up(c.q).to(dt), up(c.table), ctx, qstart=up(c.starts), max_q=2))
+    c.check(q.attention(c.cache, up(c.q).to(dt), up(c.table), ctx, qstart=up(c.starts)), dt)
 
 
 def test_nothing_to_do():
