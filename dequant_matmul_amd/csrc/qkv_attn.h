@@ -199,6 +199,35 @@ __device__ __forceinline__ int64_t seen(const AttnArgs &a, const Seq &s, int las
     return n < cap ? (n < most ? n : most) : (cap < most ? cap : most);
 }
 
+// The page ids of a wave's tiles, 64 at a time, one a lane: a tile's page is a
+// v_readlane instead of a load in front of its loads.
+struct PageIds {
+    const int32_t *ids;
+    int columns, shift, first, held;
+
+    __device__ __forceinline__ void start(const AttnArgs &a, int b, int tile)
+    {
+        ids = a.table + (int64_t)b * a.columns;
+        columns = (int)a.columns;
+        shift = a.page_shift - 6;
+        fetch(tile >> shift);
+    }
+    __device__ __forceinline__ void fetch(int col)
+    {
+        first = col;
+        const int i = col + (int)(threadIdx.x & 63);
+        held = i < columns ? ids[i] : -1;
+    }
+    // tiles may only go up; every lane of the wave calls
+    __device__ __forceinline__ int page(int tile)
+    {
+        const int col = tile >> shift;
+        if (col - first >= 64)
+            fetch(col);
+        return __builtin_amdgcn_readlane(held, col - first);
+    }
+};
+
 __device__ __forceinline__ void read8(const _Float16 *p, float v[8])
 {
     const u32x4 r = *(const u32x4 *)p;
@@ -229,19 +258,29 @@ constexpr float LOG2E = 1.44269504088896341f;
 // 2^-28 of the largest, whatever the size of V.  (F16 has no scale: exponent 0.)
 constexpr float P_TOP = 14.f;
 
-// Largest exponent e (value < 2^e, at least -14) of the lane's fp16 scales, of
-// either sign.
-template <int NB>
-__device__ __forceinline__ float scale_exponent(const uint32_t (&w)[8 * NB])
+// Largest exponent e (value < 2^e, at least -14) of eight fp16 scales of either
+// sign, over the lanes of a wave.  Lanes without V scales pass zeros.
+__device__ __forceinline__ float scale_exponent(const uint32_t (&w)[4])
 {
     typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
     u16x2 m = {0, 0};
 #pragma unroll
-    for (int i = 0; i < 8 * NB; ++i)
+    for (int i = 0; i < 4; ++i)
         m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, w[i] & 0x7fff7fffu));
-    const int top = m[0] > m[1] ? m[0] : m[1];
-    const int e = top >> 10;
-    return (float)((e > 1 ? e : 1) - 14);
+    const int e = (m[0] > m[1] ? m[0] : m[1]) >> 10;
+    float f = (float)((e > 1 ? e : 1) - 14);
+    f = fmaxf(f, dpp_f(f, 0xB1));
+    f = fmaxf(f, dpp_f(f, 0x4E));
+    f = fmaxf(f, dpp_f(f, 0x141));
+    f = fmaxf(f, dpp_f(f, 0x140));
+    return rows_max(f);
+}
+
+// A dword of two fp16 (tokens i and j of which `left` exist): what is past the
+// end becomes 0.
+__device__ __forceinline__ uint32_t keep_pair(int left, int i, int j)
+{
+    return (i < left ? 0xffffu : 0u) | (j < left ? 0xffff0000u : 0u);
 }
 
 // One row of q (r, a row of kv head `head`'s; nothing if r >= rows) as operand B:
@@ -331,8 +370,8 @@ __device__ __forceinline__ uint32_t seen16(const AttnArgs &a, const Seq &s, int 
     return bits & (left <= 0 ? 0u : left >= 16 ? 0xffffu : (1u << left) - 1u);
 }
 
-// The scores of one row tile (products, factor rs; ev the exponent of the lane's
-// V scales) become weights relative to the running maximum m; l and o follow.
+// The scores of one row tile (products, factor rs; ev the exponent of the V
+// scales) become weights relative to the running maximum m; l and o follow.
 template <int NB>
 __device__ __forceinline__ void soften(f32x4 (&sc)[4], float rs, float ev, float &m, float &l, f32x4 (&o)[2 * NB])
 {
@@ -401,10 +440,13 @@ attn_kernel(AttnArgs a)
     constexpr int VN = KT == KV_Q4 ? NB : 2 * NB;      // V pieces
     constexpr bool SCALED = KT != KV_F16;
 
+    constexpr int SP = (16 * NB + 63) / 64;            // 16-byte pieces of a tile's scales per lane
     __shared__ __align__(16) f32x4 joined[4][2 * NB][64];
     __shared__ float join_m[4][16], join_l[4][16];
+    __shared__ __align__(16) uint32_t scales[4][SCALED ? 64 * NB : 4];
 
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, h = lane >> 4;
+    const int lane = threadIdx.x & 63, n = lane & 15, h = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);     // the same in every lane, for the compiler too
     const int split = blockIdx.x, head = blockIdx.y % a.kv_heads, b = blockIdx.z;
     const int r0 = (int)(blockIdx.y / a.kv_heads) * 16;
 
@@ -416,10 +458,21 @@ attn_kernel(AttnArgs a)
     const int64_t nseen = seen(a, s, last);
     const int ntiles = (int)((nseen + KV_TILE - 1) / KV_TILE);
     const int per = (ntiles + a.splits - 1) / a.splits;
-    const int t_begin = split * per, t_end = t_begin + per < ntiles ? t_begin + per : ntiles;
+    const int t_begin = split * per;
+    const int t_end = a.pages == 0 ? 0 : t_begin + per < ntiles ? t_begin + per : ntiles;
 
     h16x8 qf[PARTS][NB];
     const float rs = load_row<NB, KT, PARTS, IO>(a, s, head, r0 + n, rows, h, qf);
+    // the low parts wait in LDS, where the wave's output goes at the end: with them
+    // the registers of a tile do not fit two waves a SIMD
+    constexpr bool QLDS = PARTS == 2 && SCALED && NB >= 4;
+    h16x8(*qlow)[64] = (h16x8(*)[64])joined[wave];
+    if constexpr (QLDS) {
+#pragma unroll
+        for (int bl = 0; bl < NB; ++bl)
+            qlow[bl][lane] = qf[PARTS - 1][bl];
+        wave_lds_sync();
+    }
     const int tok = r0 + n < rows ? (r0 + n) / a.group : -1;
 
     f32x4 o[2 * NB];
@@ -428,18 +481,20 @@ attn_kernel(AttnArgs a)
     for (int t = 0; t < 2 * NB; ++t)
         o[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
 
-    const int32_t *pages = a.table + (int64_t)b * a.columns;
-    const int tshift = a.page_shift - 6;
-    for (int tile = t_begin + wave; tile < t_end; tile += 4) {
-        const int page = pages[tile >> tshift];
-        if (page < 0 || page >= a.pages)
-            continue;                                   // nothing of it is seen
-        const int64_t at = ((((int64_t)page * a.kv_heads + head) << tshift) + (tile & ((1 << tshift) - 1))) *
-                           (int64_t)L::TILE_BYTES;
+    // ---- loads.  K of the next tile is loaded as soon as the scores are done, V
+    // when the output is: either runs under the other half of a tile.  The scales
+    // of a tile (one 16-byte piece a lane) pass through LDS, from where each lane
+    // takes those of its 16 tokens: loaded by every lane they would be two thirds
+    // of all loads.
+    uint32_t kr[4][KDW], vr[VN][VDW], sd[SCALED ? SP : 1][4];
+    PageIds pages;
+    auto tile_base = [&](int page, int tile) -> int64_t {
+        return ((((int64_t)page * a.kv_heads + head) << pages.shift) + (tile & ((1 << pages.shift) - 1))) *
+               (int64_t)L::TILE_BYTES;
+    };
+    auto load_k = [&](int64_t at) {
         const uint8_t *kp = a.k + at, *vp = a.v + at;
-
-        // ---- every load of the tile
-        uint32_t kr[4][KDW], vr[VN][VDW], ks[SCALED ? 8 * NB : 1], vs[SCALED ? 8 * NB : 1];
+        const uint32_t lane = opaque(threadIdx.x & 63);     // an offset to a uniform base, not an address of its own
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -447,9 +502,16 @@ attn_kernel(AttnArgs a)
                 load_dw<CDW>(kp + ((c * (NB / L::G) + g) * 64 + lane) * (L::G * L::UNIT), &kr[c][g * CDW]);
         if constexpr (SCALED) {
 #pragma unroll
-            for (int i = 0; i < 2 * NB; ++i)
-                load_dw<4>(kp + L::CODE_BYTES + h * 32 * NB + 16 * i, &ks[4 * i]);
+            for (int i = 0; i < SP; ++i) {
+                const int j = 64 * i + (int)lane;       // K scales, then V scales
+                if (16 * NB % 64 == 0 || j < 16 * NB)
+                    load_dw<4>((j < 8 * NB ? kp + 16 * j : vp + 16 * (j - 8 * NB)) + L::CODE_BYTES, sd[i]);
+            }
         }
+    };
+    auto load_v = [&](int64_t at) {
+        const uint8_t *vp = a.v + at;
+        const uint32_t lane = opaque(threadIdx.x & 63);
 #pragma unroll
         for (int t = 0; t < VN; ++t) {
             if constexpr (KT == KV_F16) {
@@ -459,92 +521,174 @@ attn_kernel(AttnArgs a)
                 load_dw<4>(vp + (t * 64 + lane) * 16, &vr[t][0]);
             }
         }
+    };
+
+    // A page id outside the cache: its tile is walked with nothing seen (and page
+    // 0 loaded in its place), so that every tile is the same straight line.
+    int tile = t_begin + wave;
+    bool hidden = true;
+    int64_t at = 0;
+    if (tile < t_end) {
+        pages.start(a, b, tile);
+        const int page = pages.page(tile);
+        hidden = page < 0 || page >= a.pages;
+        at = tile_base(hidden ? 0 : page, tile);
+        load_k(at);
+        load_v(at);
+    }
+    for (; tile < t_end; tile += 4) {
+        const int64_t k0 = (int64_t)tile * KV_TILE, seen_to = hidden ? k0 : nseen;
+        float ev = 0.f;
         if constexpr (SCALED) {
+            const int left = (int)(seen_to - k0 < KV_TILE ? seen_to - k0 : KV_TILE);
+            uint32_t big[4] = {0, 0, 0, 0};
 #pragma unroll
-            for (int bl = 0; bl < NB; ++bl) {
-                load_dw<4>(vp + L::CODE_BYTES + (bl * 64 + 16 * h) * 2, &vs[8 * bl]);
-                load_dw<4>(vp + L::CODE_BYTES + (bl * 64 + 16 * h) * 2 + 16, &vs[8 * bl + 4]);
+            for (int i = 0; i < SP; ++i) {
+                const int j = 64 * i + lane;
+                if (16 * NB % 64 == 0 || j < 16 * NB) {
+                    if (j >= 8 * NB) {
+                        // tokens 8 (j % 8) .. of block j / 8; what lies behind the last
+                        // token may be any bits
+                        if (left < KV_TILE) {
+                            const int room = left - 8 * (int)opaque(j & 7);
+#pragma unroll
+                            for (int w = 0; w < 4; ++w)
+                                sd[i][w] &= keep_pair(room, 2 * w, 2 * w + 1);
+                        }
+#pragma unroll
+                        for (int w = 0; w < 4; ++w)
+                            big[w] = sd[i][w];
+                    }
+                    *(u32x4 *)&scales[wave][4 * j] = (u32x4){sd[i][0], sd[i][1], sd[i][2], sd[i][3]};
+                }
             }
+            wave_lds_sync();
+            ev = scale_exponent(big);
         }
 
         // ---- scores
         f32x4 sc[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 4; ++c) {
             sc[c] = (f32x4){0.f, 0.f, 0.f, 0.f};
+            // (opaque: the conversions of the codes may not move in front of the
+            // fence before them, where they would hold twice the registers)
+            if constexpr (SCALED) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+                for (int w = 0; w < KDW; ++w)
+                    kr[c][w] = opaque(kr[c][w]);
+            }
+            uint32_t ks[SCALED ? 2 * NB : 1];           // of the lane's tokens 4 c .. 4 c + 3
+            if constexpr (SCALED) {
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+                    const u32x2 y = *(const u32x2 *)&scales[wave][8 * NB * h + 2 * NB * c + 2 * i];
+                    ks[2 * i] = y[0];
+                    ks[2 * i + 1] = y[1];
+                }
+            }
 #pragma unroll
             for (int bl = 0; bl < NB; ++bl) {
                 const h16x8 kf = C::k(&kr[c][bl * (L::UNIT / 4)]);
                 f32x4 acc = SCALED ? (f32x4){0.f, 0.f, 0.f, 0.f} : sc[c];
 #pragma unroll
                 for (int part = 0; part < PARTS; ++part)
-                    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[part][bl], acc, 0, 0, 0);
+                    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, QLDS && part == 1 ? qlow[bl][lane] : qf[part][bl],
+                                                                 acc, 0, 0, 0);
                 if constexpr (SCALED) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        sc[c][i] = fmaf(acc[i], half_of(ks, (4 * c + i) * NB + bl), sc[c][i]);
+                        sc[c][i] = fmaf(acc[i], half_of(ks, i * NB + bl), sc[c][i]);
                 } else {
                     sc[c] = acc;
                 }
             }
+            if constexpr (SCALED && NB >= 4)
+                __builtin_amdgcn_sched_barrier(0);
+        }
 
-        // ---- the part of the tile that a row does not see; what lies behind the
-        // last token may be any bits: its scores are replaced, its V (scales)
-        // zeroed
-        const int64_t k0 = (int64_t)tile * KV_TILE;
-        if (k0 + KV_TILE > s.ctx) {
-            const uint32_t bits = seen16(a, s, tok, k0 + 16 * h, nseen);
+        // ---- the next tile's K.  (Scheduling fences around the phases: moved into
+        // one another they need twice the registers.)
+        __builtin_amdgcn_sched_barrier(0);
+        const int next = tile + 4;
+        int64_t next_at = 0;
+        bool next_hidden = true;
+        if (next < t_end) {
+            const int page = pages.page(next);
+            next_hidden = page < 0 || page >= a.pages;
+            next_at = tile_base(next_hidden ? 0 : page, next);
+            load_k(next_at);
+        }
+
+        __builtin_amdgcn_sched_barrier(0);
+        // ---- what a row does not see; an F16 cache may hold any bits behind the
+        // last token
+        if (k0 + KV_TILE > s.ctx || hidden) {
+            // (opaque: kept from becoming induction variables, a register pair each)
+            const uint32_t bits = seen16(a, s, tok, k0 + 16 * (int)opaque(h), seen_to);
 #pragma unroll
             for (int c = 0; c < 4; ++c)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     sc[c][i] = (bits >> (4 * c + i)) & 1u ? sc[c][i] : -INFINITY;
         }
-        if (k0 + KV_TILE > nseen) {
-            const int left = (int)(nseen - k0) - 16 * h;
+        if constexpr (!SCALED) {
+            if (k0 + KV_TILE > seen_to) {
+                const int left = (int)(seen_to - k0) - 16 * (int)opaque(h);
 #pragma unroll
-            for (int w = 0; w < 8; ++w) {
-                const uint32_t keep = (2 * w < left ? 0xffffu : 0u) | (2 * w + 1 < left ? 0xffff0000u : 0u);
-                if constexpr (SCALED) {
-#pragma unroll
-                    for (int bl = 0; bl < NB; ++bl)
-                        vs[8 * bl + w] &= keep;
-                } else {
+                for (int w = 0; w < 8; ++w)
 #pragma unroll
                     for (int t = 0; t < VN; ++t)
-                        vr[t][w] &= keep;
-                }
+                        vr[t][w] &= keep_pair(left, 2 * w, 2 * w + 1);
             }
         }
-
-        float ev = 0.f;
-        if constexpr (SCALED)
-            ev = scale_exponent<NB>(vs);
         soften<NB>(sc, rs, ev, m, l, o);
+        __builtin_amdgcn_sched_barrier(0);
 
         // ---- output
+        h16x8 hi[2], lo[2];
+        if constexpr (!SCALED) {
 #pragma unroll
-        for (int st = 0; st < 2; ++st) {
-            h16x8 hi, lo;
-            if constexpr (!SCALED)
-                weights<KT, PARTS, false>(sc, vs, st, hi, lo);
+            for (int st = 0; st < 2; ++st)
+                weights<KT, PARTS, false>(sc, nullptr, st, hi[st], lo[st]);
+        }
 #pragma unroll
-            for (int bl = 0; bl < NB; ++bl) {
-                if constexpr (SCALED)
-                    weights<KT, PARTS, true>(sc, &vs[8 * bl], st, hi, lo);
+        for (int bl = 0; bl < NB; ++bl) {
+            if constexpr (SCALED) {
+                constexpr int VB = VN / NB;
+#pragma unroll
+                for (int u = 0; u < VB; ++u)
+#pragma unroll
+                    for (int w = 0; w < VDW; ++w)
+                        vr[VB * bl + u][w] = opaque(vr[VB * bl + u][w]);
+                uint32_t vs[8];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const u32x4 y = *(const u32x4 *)&scales[wave][32 * NB + 32 * bl + 8 * h + 4 * i];
+                    vs[4 * i] = y[0]; vs[4 * i + 1] = y[1]; vs[4 * i + 2] = y[2]; vs[4 * i + 3] = y[3];
+                }
+#pragma unroll
+                for (int st = 0; st < 2; ++st)
+                    weights<KT, PARTS, true>(sc, vs, st, hi[st], lo[st]);
+            }
+#pragma unroll
+            for (int st = 0; st < 2; ++st)
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const h16x8 vf = KT == KV_F16  ? C::v(&vr[VN > NB ? 2 * bl + u : 0][VDW > 4 ? 4 * st : 0], 0)
                                      : KT == KV_Q8 ? C::v(&vr[VN > NB ? 2 * bl + u : 0][2 * st], 0)
                                                    : C::v(&vr[bl][2 * st], u);
-                    o[2 * bl + u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, hi, o[2 * bl + u], 0, 0, 0);
+                    o[2 * bl + u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, hi[st], o[2 * bl + u], 0, 0, 0);
                     if constexpr (PARTS == 2)
-                        o[2 * bl + u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, lo, o[2 * bl + u], 0, 0, 0);
+                        o[2 * bl + u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, lo[st], o[2 * bl + u], 0, 0, 0);
                 }
-            }
+            if constexpr (SCALED && NB >= 4)
+                __builtin_amdgcn_sched_barrier(0);
         }
+        __builtin_amdgcn_sched_barrier(0);
+        if (next < t_end)
+            load_v(next_at);
+        hidden = next_hidden;
     }
 
     // ---- join the four waves; every wave then finishes every fourth 16-dim tile

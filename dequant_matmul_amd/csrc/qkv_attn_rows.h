@@ -33,8 +33,10 @@ attn_rows_kernel(AttnArgs a)
 
     __shared__ __align__(16) h16x8 kb[2][4 * NB][64], vb[2][4 * NB][64];
     __shared__ __align__(16) uint32_t kscale[2][SCALED ? 32 * NB : 4], vscale[2][SCALED ? 32 * NB : 4];
+    __shared__ float exponent[2];
 
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, h = lane >> 4;
+    const int lane = threadIdx.x & 63, n = lane & 15, h = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);     // the same in every lane, for the compiler too
     const int split = blockIdx.x, head = blockIdx.y % a.kv_heads, b = blockIdx.z;
     const int g0 = (int)(blockIdx.y / a.kv_heads) * 64 * RT, r0 = g0 + wave * 16 * RT;
 
@@ -69,11 +71,11 @@ attn_rows_kernel(AttnArgs a)
 
     // ---- staging: a tile's pieces, dealt to the waves
     uint32_t kr[KI][CDW], kd[FOLDED ? KI : 1][SDW], vr[VI][4], vd[FOLDED ? VI : 1][8], sd[4];
-    const int32_t *pages = a.table + (int64_t)b * a.columns;
-    const int tshift = a.page_shift - 6;
+    PageIds pages;
+    pages.start(a, b, t_begin);
 
     auto load_tile = [&](int tile) -> bool {
-        const int page = pages[tile >> tshift];
+        const int page = pages.page(tile), tshift = pages.shift;
         if (page < 0 || page >= a.pages)
             return false;                               // nothing of it is seen
         const int64_t at = ((((int64_t)page * a.kv_heads + head) << tshift) + (tile & ((1 << tshift) - 1))) *
@@ -114,9 +116,6 @@ attn_rows_kernel(AttnArgs a)
     };
 
     // what lies behind the last token may be any bits: V (or its scale) becomes 0
-    auto keep_pair = [&](int left, int i, int j) -> uint32_t {
-        return (i < left ? 0xffffu : 0u) | (j < left ? 0xffff0000u : 0u);
-    };
     auto store_tile = [&](int buf, int tile) {
         const int64_t rest = nseen - (int64_t)tile * KV_TILE;
         const int left = (int)(rest < KV_TILE ? rest : KV_TILE) - 16 * h;
@@ -171,17 +170,23 @@ attn_rows_kernel(AttnArgs a)
             }
         }
         if constexpr (SCALED) {
+            // threads of one wave hold the V scales of a tile
             const int t = threadIdx.x;
+            uint32_t big[4] = {0, 0, 0, 0};
             if (t < 8 * NB) {
                 *(u32x4 *)&kscale[buf][4 * t] = (u32x4){sd[0], sd[1], sd[2], sd[3]};
             } else if (t < 16 * NB) {
-                // 16 bytes are tokens 8 (t % 8) .. of block t / 8
-                const int key0 = 8 * ((t - 8 * NB) & 7), room = (int)(rest < KV_TILE ? rest : KV_TILE) - key0;
-                u32x4 y;
+                // tokens 8 (j % 8) .. of block j / 8
+                const int j = t - 8 * NB, room = (int)(rest < KV_TILE ? rest : KV_TILE) - 8 * (j & 7);
 #pragma unroll
                 for (int w = 0; w < 4; ++w)
-                    y[w] = sd[w] & keep_pair(room, 2 * w, 2 * w + 1);
-                *(u32x4 *)&vscale[buf][4 * (t - 8 * NB)] = y;
+                    big[w] = sd[w] & keep_pair(room, 2 * w, 2 * w + 1);
+                *(u32x4 *)&vscale[buf][4 * j] = (u32x4){big[0], big[1], big[2], big[3]};
+            }
+            if (wave == 8 * NB / 64) {
+                const float e = scale_exponent(big);
+                if (lane == 0)
+                    exponent[buf] = e;
             }
         }
     };
@@ -244,7 +249,7 @@ attn_rows_kernel(AttnArgs a)
                     vs[8 * bl + 4 * i] = y[0]; vs[8 * bl + 4 * i + 1] = y[1];
                     vs[8 * bl + 4 * i + 2] = y[2]; vs[8 * bl + 4 * i + 3] = y[3];
                 }
-            ev = scale_exponent<NB>(vs);
+            ev = exponent[buf];
         }
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
