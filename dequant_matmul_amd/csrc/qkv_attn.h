@@ -587,21 +587,26 @@ attn_kernel(AttnArgs a)
                     ks[2 * i + 1] = y[1];
                 }
             }
+            // products that do not depend on one another in a row
+            f32x4 acc[SCALED ? NB : 1];
 #pragma unroll
-            for (int bl = 0; bl < NB; ++bl) {
-                const h16x8 kf = C::k(&kr[c][bl * (L::UNIT / 4)]);
-                f32x4 acc = SCALED ? (f32x4){0.f, 0.f, 0.f, 0.f} : sc[c];
+            for (int part = 0; part < PARTS; ++part)
 #pragma unroll
-                for (int part = 0; part < PARTS; ++part)
-                    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, QLDS && part == 1 ? qlow[bl][lane] : qf[part][bl],
-                                                                 acc, 0, 0, 0);
-                if constexpr (SCALED) {
+                for (int bl = 0; bl < NB; ++bl) {
+                    const h16x8 kf = C::k(&kr[c][bl * (L::UNIT / 4)]);
+                    const h16x8 y = QLDS && part == 1 ? qlow[bl][lane] : qf[part][bl];
+                    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+                    if constexpr (SCALED)
+                        acc[bl] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, y, part ? acc[bl] : zero, 0, 0, 0);
+                    else
+                        sc[c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, y, sc[c], 0, 0, 0);
+                }
+            if constexpr (SCALED) {
+#pragma unroll
+                for (int bl = 0; bl < NB; ++bl)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        sc[c][i] = fmaf(acc[i], half_of(ks, i * NB + bl), sc[c][i]);
-                } else {
-                    sc[c] = acc;
-                }
+                        sc[c][i] = fmaf(acc[bl][i], half_of(ks, i * NB + bl), sc[c][i]);
             }
             if constexpr (SCALED && NB >= 4)
                 __builtin_amdgcn_sched_barrier(0);
@@ -737,15 +742,19 @@ attn_kernel(AttnArgs a)
 // ------------------------------------------------------- joining the splits --
 
 // `slices` groups of 8 * NB threads share a row of q, each taking every
-// slices-th split for 4 dims a thread.  blockIdx.y is the sequence, so that rows
-// of no sequence are left alone; splits that saw nothing wrote l = 0.
+// slices-th split for 4 dims a thread: JOIN_MOST splits at a time, loaded
+// together, since what bounds this kernel is one load's latency.  blockIdx.y is
+// the sequence, so that rows of no sequence are left alone; splits that saw
+// nothing wrote l = 0 (and m of minus infinity), their output is never used.
+constexpr int JOIN_MOST = 8;
+
 template <int NB, typename IO>
 __global__ void __launch_bounds__(256)
 attn_join_kernel(AttnArgs a, int slices)
 {
     constexpr int PER = 8 * NB;
     __shared__ __align__(16) f32x4 part[256];
-    __shared__ float part_l[256];
+    __shared__ float2 part_ml[256];
     const int u = threadIdx.x / PER, d0 = 4 * (threadIdx.x % PER);
     const int here = 256 / PER / slices, r = u / slices, slice = u - r * slices;
     const Seq s = sequence(a, blockIdx.y);
@@ -754,34 +763,56 @@ attn_join_kernel(AttnArgs a, int slices)
     const bool live = r < here && i < rows;
     const int64_t wrows = (int64_t)a.tokens * a.heads, row = (int64_t)s.q0 * a.heads + i;
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-    float lt = 0.f;
+    float lt = 0.f, mm = -INFINITY;
     if (live) {
         const float2 *ml = (const float2 *)(a.ws + (int64_t)a.splits * wrows * PER * 4) + row;
-        float mm = -INFINITY;
-#pragma unroll 8
-        for (int sp = 0; sp < a.splits; ++sp)
-            mm = fmaxf(mm, ml[sp * wrows].x);
-        const float mu = mm == -INFINITY ? 0.f : mm;
-#pragma unroll 4
-        for (int sp = slice; sp < a.splits; sp += slices) {
-            const float2 x = ml[sp * wrows];
-            const f32x4 y = *(const f32x4 *)(a.ws + (sp * wrows + row) * (PER * 4) + d0);
-            const float w = __builtin_amdgcn_exp2f(x.x - mu);
-            if (x.y > 0.f) {
-                lt = fmaf(w, x.y, lt);
-                acc += y * w;
+        const float *po = a.ws + row * (PER * 4) + d0;
+        for (int first = slice; first < a.splits; first += JOIN_MOST * slices) {
+            float2 x[JOIN_MOST];
+            f32x4 y[JOIN_MOST];
+#pragma unroll
+            for (int k = 0; k < JOIN_MOST; ++k) {
+                const int sp = first + k * slices;
+                x[k] = make_float2(-INFINITY, 0.f);
+                if (sp < a.splits) {
+                    x[k] = ml[sp * wrows];
+                    y[k] = *(const f32x4 *)(po + sp * wrows * (PER * 4));
+                }
             }
+            float mn = mm;
+#pragma unroll
+            for (int k = 0; k < JOIN_MOST; ++k)
+                mn = fmaxf(mn, x[k].x);
+            const float mu = mn == -INFINITY ? 0.f : mn, alpha = __builtin_amdgcn_exp2f(mm - mu);
+            acc *= alpha;
+            lt *= alpha;
+            mm = mn;
+#pragma unroll
+            for (int k = 0; k < JOIN_MOST; ++k)
+                if (x[k].y > 0.f) {
+                    const float w = __builtin_amdgcn_exp2f(x[k].x - mu);
+                    lt = fmaf(w, x[k].y, lt);
+                    acc += y[k] * w;
+                }
         }
     }
     if (slices > 1) {
         part[threadIdx.x] = acc;
-        part_l[threadIdx.x] = lt;
+        part_ml[threadIdx.x] = make_float2(mm, lt);
         __syncthreads();
-        if (slice > 0)
+        if (slice > 0 || !live)
             return;
-        for (int k = 1; live && k < slices; ++k) {
-            acc += part[threadIdx.x + k * PER];
-            lt += part_l[threadIdx.x + k * PER];
+        const float own = mm;
+        for (int k = 1; k < slices; ++k)
+            mm = fmaxf(mm, part_ml[threadIdx.x + k * PER].x);
+        const float mu = mm == -INFINITY ? 0.f : mm, first = __builtin_amdgcn_exp2f(own - mu);
+        acc *= first;
+        lt *= first;
+        for (int k = 1; k < slices; ++k) {
+            const float2 x = part_ml[threadIdx.x + k * PER];
+            const float w = __builtin_amdgcn_exp2f(x.x - mu);
+            lt = fmaf(w, x.y, lt);
+            acc += part[threadIdx.x + k * PER] * w;
         }
     }
     if (!live || d0 >= a.dim)

@@ -207,26 +207,45 @@ attn_rows_kernel(AttnArgs a)
                 ks[4 * i] = y[0]; ks[4 * i + 1] = y[1]; ks[4 * i + 2] = y[2]; ks[4 * i + 3] = y[3];
             }
         }
+        // block by block: 4 RT products in a row that do not depend on one another
+        // (the matrix cores' latency is several times their rate); the fragments of
+        // the next block are read meanwhile
+        h16x8 kf[2][4];
 #pragma unroll
         for (int c = 0; c < 4; ++c)
+            kf[0][c] = kb[buf][c * NB][lane];
 #pragma unroll
-            for (int bl = 0; bl < NB; ++bl) {
-                const h16x8 kf = kb[buf][c * NB + bl][lane];
+        for (int bl = 0; bl < NB; ++bl) {
+            if (bl + 1 < NB) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    kf[(bl + 1) & 1][c] = kb[buf][c * NB + bl + 1][lane];
+            }
+            f32x4 acc[RT][4];
+#pragma unroll
+            for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) {
+                        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+                        acc[rt][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                            kf[bl & 1][c], qf[rt][part][bl], part > 0 ? acc[rt][c] : SCALED ? zero : sc[rt][c], 0, 0, 0);
+                    }
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
-                    f32x4 acc = SCALED ? (f32x4){0.f, 0.f, 0.f, 0.f} : sc[rt][c];
-#pragma unroll
-                    for (int part = 0; part < PARTS; ++part)
-                        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[rt][part][bl], acc, 0, 0, 0);
                     if constexpr (SCALED) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            sc[rt][c][i] = fmaf(acc[i], half_of(ks, (4 * c + i) * NB + bl), sc[rt][c][i]);
+                            sc[rt][c][i] = fmaf(acc[rt][c][i], half_of(ks, (4 * c + i) * NB + bl), sc[rt][c][i]);
                     } else {
-                        sc[rt][c] = acc;
+                        sc[rt][c] = acc[rt][c];
                     }
                 }
-            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
         if (k0 + KV_TILE > s.ctx) {
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
@@ -251,35 +270,48 @@ attn_rows_kernel(AttnArgs a)
                 }
             ev = exponent[buf];
         }
+        // fragments of V in groups of PB blocks: the first is read under the softmax,
+        // each next one under the products of the one before
+        constexpr int PB = NB % 2 == 0 && NB > 2 ? 2 : 1, GROUPS = NB / PB;
+        h16x8 vf[2][2 * PB];
+        auto read_v = [&](int g) {
+#pragma unroll
+            for (int i = 0; i < 2 * PB; ++i)
+                vf[g & 1][i] = vb[buf][2 * (2 * PB * (g % GROUPS) + i) + g / GROUPS][lane];
+        };
+        read_v(0);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
             soften<NB>(sc[rt], rs[rt], ev, m[rt], l[rt], o[rt]);
+        h16x8 hi[RT], lo[RT];
 #pragma unroll
-        for (int st = 0; st < 2; ++st) {
-            h16x8 hi[RT], lo[RT];
-            if constexpr (!SCALED) {
+        for (int g = 0; g < 2 * GROUPS; ++g) {
+            const int st = g / GROUPS;
+            __builtin_amdgcn_sched_barrier(0);
+            if (g + 1 < 2 * GROUPS)
+                read_v(g + 1);
+            if (!SCALED && g % GROUPS == 0) {
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt)
                     weights<KT, PARTS, false>(sc[rt], vs, st, hi[rt], lo[rt]);
             }
 #pragma unroll
-            for (int bl = 0; bl < NB; ++bl) {
+            for (int i = 0; i < PB; ++i) {
+                const int bl = (g % GROUPS) * PB + i;
                 if constexpr (SCALED) {
 #pragma unroll
                     for (int rt = 0; rt < RT; ++rt)
                         weights<KT, PARTS, true>(sc[rt], &vs[8 * bl], st, hi[rt], lo[rt]);
                 }
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int t = 2 * bl + u;
-                    const h16x8 vf = vb[buf][2 * t + st][lane];
+                for (int part = 0; part < PARTS; ++part)
 #pragma unroll
-                    for (int rt = 0; rt < RT; ++rt) {
-                        o[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, hi[rt], o[rt][t], 0, 0, 0);
-                        if constexpr (PARTS == 2)
-                            o[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, lo[rt], o[rt][t], 0, 0, 0);
-                    }
-                }
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int rt = 0; rt < RT; ++rt)
+                            o[rt][2 * bl + u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                                vf[g & 1][2 * i + u], part ? lo[rt] : hi[rt], o[rt][2 * bl + u], 0, 0, 0);
             }
         }
     };
@@ -346,7 +378,7 @@ hipError_t attn_blocks(const AttnArgs &a, const AttnPlan &p, int64_t batch, hipS
         return e;
     constexpr int PER = 8 * NB, MOST = 256 / PER;
     int slices = 1;
-    while (slices * 2 <= MOST && slices * 4 <= p.splits)
+    while (slices * 2 <= MOST && slices * JOIN_MOST < p.splits)
         slices *= 2;
     const int here = MOST / slices;
     const int64_t rows = (int64_t)a.max_q * a.heads;
