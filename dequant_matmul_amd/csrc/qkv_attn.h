@@ -252,11 +252,15 @@ __device__ __forceinline__ void write4(_Float16 *p, f32x4 v)
 
 constexpr float LOG2E = 1.44269504088896341f;
 
-// The softmax weights are taken relative to 2^(M - P_TOP), M the running maximum
-// of score + exponent of the V scale: weight times V scale, the number that is
-// rounded to fp16 parts, is then at most 2^P_TOP and stays a normal fp16 down to
-// 2^-28 of the largest, whatever the size of V.  (F16 has no scale: exponent 0.)
-constexpr float P_TOP = 14.f;
+// The softmax weights of a row are taken relative to a reference M, exp2(z + e -
+// M + P_TOP - e) for score z and e the exponent of the tile's V scales: weight
+// times V scale, the number that is rounded to fp16 parts, is near 2^P_TOP for the
+// largest, whatever the size of V, and a normal fp16 down to 2^-24 of it.  (F16
+// has no scale: e = 0.)  M need not be the maximum: it is raised only when a
+// product would pass 2^(P_TOP + P_SLACK) (fp16 ends at 2^16), which after a row's
+// first tile is rare; the exchange between lanes, the new reference and the
+// rescaled output are then skipped for the tile.
+constexpr float P_TOP = 10.f, P_SLACK = 5.f;
 
 // Largest exponent e (value < 2^e, at least -14) of eight fp16 scales of either
 // sign, over the lanes of a wave.  Lanes without V scales pass zeros.
@@ -370,10 +374,7 @@ __device__ __forceinline__ uint32_t seen16(const AttnArgs &a, const Seq &s, int 
     return bits & (left <= 0 ? 0u : left >= 16 ? 0xffffu : (1u << left) - 1u);
 }
 
-// The scores of one row tile (products, factor rs; ev the exponent of the V
-// scales) become weights relative to the running maximum m; l and o follow.
-template <int NB>
-__device__ __forceinline__ void soften(f32x4 (&sc)[4], float rs, float ev, float &m, float &l, f32x4 (&o)[2 * NB])
+__device__ __forceinline__ float lane_max(const f32x4 (&sc)[4])
 {
     float mx = -INFINITY;
 #pragma unroll
@@ -381,25 +382,49 @@ __device__ __forceinline__ void soften(f32x4 (&sc)[4], float rs, float ev, float
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             mx = fmaxf(mx, sc[c][i]);
-    mx = rows_max(fmaf(mx, rs, ev));
-    const float mn = fmaxf(m, mx), mu = mn == -INFINITY ? 0.f : mn;
-    const float alpha = __builtin_amdgcn_exp2f(m - mu), shift = P_TOP - mu;
+    return mx;
+}
+
+// Raise a row tile's reference m to its maximum, top (per lane: largest score
+// plus exponent of the V scales); l and o follow.  shift = P_TOP - m.
+template <int NB>
+__device__ __forceinline__ void raise(float top, float &m, float &shift, float &l, f32x4 (&o)[2 * NB])
+{
+    const float mn = fmaxf(m, rows_max(top)), mu = mn == -INFINITY ? 0.f : mn;
+    const float alpha = __builtin_amdgcn_exp2f(m - mu);
     m = mn;
-    float sum = 0.f;
+    shift = P_TOP - mu;
+    l *= alpha;
+#pragma unroll
+    for (int t = 0; t < 2 * NB; ++t)
+        o[t] *= alpha;
+}
+
+// Scores to weights, in place.
+__device__ __forceinline__ void soften(f32x4 (&sc)[4], float rs, float shift)
+{
 #pragma unroll
     for (int c = 0; c < 4; ++c)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float p = __builtin_amdgcn_exp2f(fmaf(sc[c][i], rs, shift));
-            sc[c][i] = p;
-            sum += p;
-        }
-    l = fmaf(l, alpha, sum);
-    if (__any(alpha != 1.f)) {
+        for (int i = 0; i < 4; ++i)
+            sc[c][i] = __builtin_amdgcn_exp2f(fmaf(sc[c][i], rs, shift));
+}
+
+__device__ __forceinline__ float sum16(const f32x4 (&sc)[4])
+{
+    const f32x4 y = (sc[0] + sc[1]) + (sc[2] + sc[3]);
+    return (y[0] + y[1]) + (y[2] + y[3]);
+}
+
+// Sum of the eight weights of operand B, as they are rounded.
+__device__ __forceinline__ float sum8(const h16x8 w, float l)
+{
+    const u32x4 y = __builtin_bit_cast(u32x4, w);
+    const h16x2 one = {(_Float16)1.f, (_Float16)1.f};
 #pragma unroll
-        for (int t = 0; t < 2 * NB; ++t)
-            o[t] *= alpha;
-    }
+    for (int i = 0; i < 4; ++i)
+        l = __builtin_amdgcn_fdot2(as_h2(y[i]), one, l, false);
+    return l;
 }
 
 // Weights of the eight tokens of contraction step st, times their V scales
@@ -476,7 +501,7 @@ attn_kernel(AttnArgs a)
     const int tok = r0 + n < rows ? (r0 + n) / a.group : -1;
 
     f32x4 o[2 * NB];
-    float m = -INFINITY, l = 0.f;
+    float m = -INFINITY, shift = P_TOP, l = 0.f;
 #pragma unroll
     for (int t = 0; t < 2 * NB; ++t)
         o[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
@@ -647,7 +672,11 @@ attn_kernel(AttnArgs a)
                         vr[t][w] &= keep_pair(left, 2 * w, 2 * w + 1);
             }
         }
-        soften<NB>(sc, rs, ev, m, l, o);
+        const float top = fmaf(lane_max(sc), rs, ev);
+        if (__any(top > m + P_SLACK))
+            raise<NB>(top, m, shift, l, o);
+        soften(sc, rs, shift);
+        l += sum16(sc);
         __builtin_amdgcn_sched_barrier(0);
 
         // ---- output

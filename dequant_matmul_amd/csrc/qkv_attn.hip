@@ -7,12 +7,13 @@ AttnPlan attn_plan(const KvView &c, int64_t tokens, int64_t batch, int heads, in
 {
     AttnPlan p;
     const int64_t rows = max_q * (heads / c.kv_heads);
-    p.rows = rows <= 16 ? 16 : rows <= 64 || !half || c.nb > 4 ? 64 : 128;
+    p.rows = rows <= 16 ? 16 : rows <= 64 || (!half && c.nb > 4) ? 64 : rows <= 128 || !half || c.nb > 4 ? 128 : 256;
     p.groups = (int)((rows + p.rows - 1) / p.rows);
     const int64_t tiles = (max_ctx + KV_TILE - 1) / KV_TILE;
     const int64_t wgs = batch * c.kv_heads * p.groups;
     const int cus = device_cu_count() > 0 ? device_cu_count() : 256;
-    int64_t splits = wgs > 0 ? (2 * cus + wgs - 1) / wgs : 1;
+    const int per_cu = p.rows >= 128 ? 1 : 2;
+    int64_t splits = wgs > 0 ? (per_cu * cus + wgs - 1) / wgs : 1;
     const int64_t most = (tiles + 3) / 4;
     splits = splits < most ? splits : most;
     p.splits = (int)(splits > 1 ? splits : 1);

@@ -2,8 +2,8 @@
 // and prompt chunks whose rows (new tokens times heads of a kv head) exceed one
 // 16-row tile.
 //
-// As attn_kernel, but the four waves of a workgroup hold different rows (RT
-// tiles of 16 each) and walk the same tiles of 64 tokens: a tile is decoded once
+// As attn_kernel, but the W waves of a workgroup hold different rows (RT tiles of
+// 16 each) and walk the same tiles of 64 tokens: a tile is decoded once
 // into LDS, as fp16 operand fragments, for all of them.  Two LDS buffers: the
 // global loads of the next tile run under the products of this one, one barrier a
 // tile.
@@ -18,8 +18,8 @@
 
 namespace qmm {
 
-template <int NB, int KT, int RT, int PARTS, typename IO>
-__global__ void __launch_bounds__(256, NB > 4 ? 1 : 2)
+template <int NB, int KT, int RT, int W, int PARTS, typename IO>
+__global__ void __launch_bounds__(64 * W, NB > 4 && W == 4 ? 1 : 2)
 attn_rows_kernel(AttnArgs a)
 {
     using L = KvLay<NB, KT>;
@@ -27,9 +27,10 @@ attn_rows_kernel(AttnArgs a)
     constexpr bool SCALED = KT != KV_F16 && PARTS == 2;     // scales stay apart
     constexpr bool FOLDED = KT != KV_F16 && PARTS == 1;     // scales go into the fragments
     constexpr int CDW = L::G * L::UNIT / 4;                 // dwords of a lane's K piece
-    constexpr int KN = 4 * NB / L::G, KI = (KN + 3) / 4;    // K pieces of a tile, of a wave
-    constexpr int VN = KT == KV_F16 ? 4 * NB : KT == KV_Q8 ? 2 * NB : NB, VI = (VN + 3) / 4;
-    constexpr int SDW = (L::G + 1) / 2;                     // dwords of a K piece's scales
+    constexpr int KN = 4 * NB / L::G, KI = (KN + W - 1) / W;    // K pieces of a tile, of a wave
+    constexpr int VN = KT == KV_F16 ? 4 * NB : KT == KV_Q8 ? 2 * NB : NB, VI = (VN + W - 1) / W;
+    constexpr bool SPAIR = L::G % 2 == 0;                   // scales of a K piece: two a dword, or one
+    constexpr int SDW = SPAIR ? L::G / 2 : L::G;
 
     __shared__ __align__(16) h16x8 kb[2][4 * NB][64], vb[2][4 * NB][64];
     __shared__ __align__(16) uint32_t kscale[2][SCALED ? 32 * NB : 4], vscale[2][SCALED ? 32 * NB : 4];
@@ -38,13 +39,13 @@ attn_rows_kernel(AttnArgs a)
     const int lane = threadIdx.x & 63, n = lane & 15, h = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);     // the same in every lane, for the compiler too
     const int split = blockIdx.x, head = blockIdx.y % a.kv_heads, b = blockIdx.z;
-    const int g0 = (int)(blockIdx.y / a.kv_heads) * 64 * RT, r0 = g0 + wave * 16 * RT;
+    const int g0 = (int)(blockIdx.y / a.kv_heads) * 16 * W * RT, r0 = g0 + wave * 16 * RT;
 
     const Seq s = sequence(a, b);
     const int rows = (s.tq < a.max_q ? s.tq : a.max_q) * a.group;
     if (g0 >= rows)
         return;
-    const int last = ((rows < g0 + 64 * RT ? rows : g0 + 64 * RT) - 1) / a.group;
+    const int last = ((rows < g0 + 16 * W * RT ? rows : g0 + 16 * W * RT) - 1) / a.group;
     const int64_t nseen = seen(a, s, last);
     const int ntiles = (int)((nseen + KV_TILE - 1) / KV_TILE);
     const int per = (ntiles + a.splits - 1) / a.splits;
@@ -54,7 +55,7 @@ attn_rows_kernel(AttnArgs a)
     const int my_end = r0 >= rows ? 0 : (int)((seen(a, s, my_last) + KV_TILE - 1) / KV_TILE);
 
     h16x8 qf[RT][PARTS][NB];
-    float rs[RT], m[RT], l[RT];
+    float rs[RT], m[RT], shift[RT], l[RT];
     int tok[RT];
     f32x4 o[RT][2 * NB];
 #pragma unroll
@@ -63,6 +64,7 @@ attn_rows_kernel(AttnArgs a)
         rs[rt] = load_row<NB, KT, PARTS, IO>(a, s, head, r, rows, h, qf[rt]);
         tok[rt] = r < rows ? r / a.group : -1;
         m[rt] = -INFINITY;
+        shift[rt] = P_TOP;
         l[rt] = 0.f;
 #pragma unroll
         for (int t = 0; t < 2 * NB; ++t)
@@ -74,31 +76,33 @@ attn_rows_kernel(AttnArgs a)
     PageIds pages;
     pages.start(a, b, t_begin);
 
+    // whether the tile's page is in the cache: else nothing of it is seen
     auto load_tile = [&](int tile) -> bool {
         const int page = pages.page(tile), tshift = pages.shift;
         if (page < 0 || page >= a.pages)
-            return false;                               // nothing of it is seen
+            return false;
         const int64_t at = ((((int64_t)page * a.kv_heads + head) << tshift) + (tile & ((1 << tshift) - 1))) *
                            (int64_t)L::TILE_BYTES;
         const uint8_t *kp = a.k + at, *vp = a.v + at;
 #pragma unroll
         for (int i = 0; i < KI; ++i) {
-            const int j = wave + 4 * i;
-            if (KN % 4 == 0 || j < KN) {
+            const int j = wave + W * i;
+            if (KN % W == 0 || j < KN) {
                 load_dw<CDW>(kp + (j * 64 + lane) * (L::G * L::UNIT), kr[i]);
                 if constexpr (FOLDED) {
                     const int c = j / (NB / L::G), key = 16 * (n >> 2) + 4 * c + (n & 3);
                     const uint16_t *sp = (const uint16_t *)(kp + L::k_scale(key, (j % (NB / L::G)) * L::G));
+                    // (nothing is computed from a load here: that would wait for it)
 #pragma unroll
                     for (int w = 0; w < SDW; ++w)
-                        kd[i][w] = 2 * w + 1 < L::G ? sp[2 * w] | (uint32_t)sp[2 * w + 1] << 16 : sp[2 * w];
+                        kd[i][w] = SPAIR ? ((const uint32_t *)sp)[w] : sp[w];
                 }
             }
         }
 #pragma unroll
         for (int i = 0; i < VI; ++i) {
-            const int j = wave + 4 * i;
-            if (VN % 4 == 0 || j < VN) {
+            const int j = wave + W * i;
+            if (VN % W == 0 || j < VN) {
                 load_dw<4>(vp + (j * 64 + lane) * 16, vr[i]);
                 if constexpr (FOLDED) {
                     const uint8_t *sp = vp + L::v_scale(16 * h, KT == KV_Q8 ? j >> 1 : j);
@@ -122,21 +126,21 @@ attn_rows_kernel(AttnArgs a)
         const bool tail = rest < KV_TILE;
 #pragma unroll
         for (int i = 0; i < KI; ++i) {
-            const int j = wave + 4 * i;
-            if (KN % 4 == 0 || j < KN) {
+            const int j = wave + W * i;
+            if (KN % W == 0 || j < KN) {
 #pragma unroll
                 for (int u = 0; u < L::G; ++u) {
                     h16x8 f = C::k(&kr[i][u * (L::UNIT / 4)]);
                     if constexpr (FOLDED)
-                        f *= (h16x8)(as_h2(kd[i][u >> 1])[u & 1]);
+                        f *= (h16x8)(as_h2(kd[i][SPAIR ? u >> 1 : u])[SPAIR ? u & 1 : 0]);
                     kb[buf][j * L::G + u][lane] = f;
                 }
             }
         }
 #pragma unroll
         for (int i = 0; i < VI; ++i) {
-            const int j = wave + 4 * i;
-            if (VN % 4 == 0 || j < VN) {
+            const int j = wave + W * i;
+            if (VN % W == 0 || j < VN) {
                 constexpr int FR = KT == KV_F16 ? 1 : KT == KV_Q8 ? 2 : 4;   // fragments of a piece
 #pragma unroll
                 for (int f = 0; f < FR; ++f) {
@@ -270,40 +274,46 @@ attn_rows_kernel(AttnArgs a)
                 }
             ev = exponent[buf];
         }
-        // fragments of V in groups of PB blocks: the first is read under the softmax,
-        // each next one under the products of the one before
-        constexpr int PB = NB % 2 == 0 && NB > 2 ? 2 : 1, GROUPS = NB / PB;
-        h16x8 vf[2][2 * PB];
-        auto read_v = [&](int g) {
+        float top[RT];
+        bool more = false;
 #pragma unroll
-            for (int i = 0; i < 2 * PB; ++i)
-                vf[g & 1][i] = vb[buf][2 * (2 * PB * (g % GROUPS) + i) + g / GROUPS][lane];
-        };
-        read_v(0);
-        __builtin_amdgcn_sched_barrier(0);
+        for (int rt = 0; rt < RT; ++rt) {
+            top[rt] = fmaf(lane_max(sc[rt]), rs[rt], ev);
+            more |= top[rt] > m[rt] + P_SLACK;
+        }
+        if (__any(more)) {
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-            soften<NB>(sc[rt], rs[rt], ev, m[rt], l[rt], o[rt]);
-        h16x8 hi[RT], lo[RT];
+            for (int rt = 0; rt < RT; ++rt)
+                raise<NB>(top[rt], m[rt], shift[rt], l[rt], o[rt]);
+        }
 #pragma unroll
-        for (int g = 0; g < 2 * GROUPS; ++g) {
-            const int st = g / GROUPS;
-            __builtin_amdgcn_sched_barrier(0);
-            if (g + 1 < 2 * GROUPS)
-                read_v(g + 1);
-            if (!SCALED && g % GROUPS == 0) {
+        for (int rt = 0; rt < RT; ++rt) {
+            soften(sc[rt], rs[rt], shift[rt]);
+            if constexpr (PARTS == 2)
+                l[rt] += sum16(sc[rt]);
+        }
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
+        for (int st = 0; st < 2; ++st) {
+            h16x8 hi[RT], lo[RT];
+            if constexpr (!SCALED) {
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
                     weights<KT, PARTS, false>(sc[rt], vs, st, hi[rt], lo[rt]);
+                    if constexpr (PARTS == 1)
+                        l[rt] = sum8(hi[rt], l[rt]);
+                }
             }
 #pragma unroll
-            for (int i = 0; i < PB; ++i) {
-                const int bl = (g % GROUPS) * PB + i;
+            for (int bl = 0; bl < NB; ++bl) {
                 if constexpr (SCALED) {
 #pragma unroll
                     for (int rt = 0; rt < RT; ++rt)
                         weights<KT, PARTS, true>(sc[rt], &vs[8 * bl], st, hi[rt], lo[rt]);
                 }
+                h16x8 vf[2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    vf[u] = vb[buf][2 * (2 * bl + u) + st][lane];
 #pragma unroll
                 for (int part = 0; part < PARTS; ++part)
 #pragma unroll
@@ -311,7 +321,7 @@ attn_rows_kernel(AttnArgs a)
 #pragma unroll
                         for (int rt = 0; rt < RT; ++rt)
                             o[rt][2 * bl + u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                                vf[g & 1][2 * i + u], part ? lo[rt] : hi[rt], o[rt][2 * bl + u], 0, 0, 0);
+                                vf[u], part ? lo[rt] : hi[rt], o[rt][2 * bl + u], 0, 0, 0);
             }
         }
     };
@@ -368,11 +378,14 @@ hipError_t attn_blocks(const AttnArgs &a, const AttnPlan &p, int64_t batch, hipS
     if (p.rows == 16)
         hipLaunchKernelGGL((attn_kernel<NB, KT, PARTS, IO>), grid, dim3(256), 0, s, a);
     else if (p.rows == 64)
-        hipLaunchKernelGGL((attn_rows_kernel<NB, KT, 1, PARTS, IO>), grid, dim3(256), 0, s, a);
-    else if constexpr (PARTS == 1 && NB <= 4)
-        hipLaunchKernelGGL((attn_rows_kernel<NB, KT, 2, PARTS, IO>), grid, dim3(256), 0, s, a);
-    else
-        return hipErrorInvalidValue;
+        hipLaunchKernelGGL((attn_rows_kernel<NB, KT, 1, 4, PARTS, IO>), grid, dim3(256), 0, s, a);
+    else if constexpr (PARTS == 1 || NB <= 4) {
+        if (p.rows == 128) {
+            hipLaunchKernelGGL((attn_rows_kernel<NB, KT, 1, 8, PARTS, IO>), grid, dim3(512), 0, s, a);
+        } else if constexpr (PARTS == 1 && NB <= 4) {
+            hipLaunchKernelGGL((attn_rows_kernel<NB, KT, 2, 8, PARTS, IO>), grid, dim3(512), 0, s, a);
+        }
+    }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1)
         return e;

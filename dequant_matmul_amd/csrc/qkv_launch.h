@@ -40,7 +40,7 @@ struct AttnCall {
 // How a call is cut up: the rows of a kv head (new tokens times heads of the
 // group) come in groups of `rows`, the tokens of a sequence in `splits` parts.
 struct AttnPlan {
-    int rows;       // of a workgroup: 16 (attn_kernel), 64 or 128 (attn_rows_kernel)
+    int rows;       // of a workgroup: 16 (attn_kernel), 64, 128 or 256 (attn_rows_kernel)
     int groups;     // row groups of a kv head
     int splits;
     int64_t bytes;  // workspace
