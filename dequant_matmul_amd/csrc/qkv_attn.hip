@@ -3,21 +3,59 @@
 
 namespace qmm {
 
+// Few rows (attn_kernel): two workgroups for every CU, as long as each still has a
+// tile for each of its four waves; up to 8 tiles (512 tokens) are not split, since
+// joining costs 4 us, about what they take (one 4096-wide layer's token at 500
+// tokens: 9.1 us whole, 9.5 split; at 1000: 13.6 and 9.7).
+//
+// Many rows (attn_rows_kernel): the cheapest of a few row groups and splits by a
+// model whose figures are measured on the 512-token chunk and the tree of the
+// layer with 128-wide heads, in us: a tile's time for a workgroup of `rows` rows
+// alone on a CU (it hardly depends on how many rows its waves hold as long as they
+// do not share a CU), and the join's fixed part and traffic.  Chunk of 512 at 7680
+// tokens: 256 rows in 4 splits 90 us (model 91), 128 in 2 104 (104), 64 in 2 126
+// (128); at an empty cache: 64 rows whole 18 us, 256 rows 28.
 AttnPlan attn_plan(const KvView &c, int64_t tokens, int64_t batch, int heads, int half, int64_t max_q, int64_t max_ctx)
 {
     AttnPlan p;
     const int64_t rows = max_q * (heads / c.kv_heads);
-    p.rows = rows <= 16 ? 16 : rows <= 64 || (!half && c.nb > 4) ? 64 : rows <= 128 || !half || c.nb > 4 ? 128 : 256;
-    p.groups = (int)((rows + p.rows - 1) / p.rows);
-    const int64_t tiles = (max_ctx + KV_TILE - 1) / KV_TILE;
-    const int64_t wgs = batch * c.kv_heads * p.groups;
+    const int64_t tiles = (max_ctx + KV_TILE - 1) / KV_TILE, r = tokens * heads;
     const int cus = device_cu_count() > 0 ? device_cu_count() : 256;
-    const int per_cu = p.rows >= 128 ? 1 : 2;
-    int64_t splits = wgs > 0 ? (per_cu * cus + wgs - 1) / wgs : 1;
-    const int64_t most = (tiles + 3) / 4;
-    splits = splits < most ? splits : most;
-    p.splits = (int)(splits > 1 ? splits : 1);
-    const int64_t r = tokens * heads;
+    if (rows <= 32) {
+        p.rows = 16;
+        p.groups = (int)((rows + 15) / 16);
+        const int64_t wgs = batch * c.kv_heads * p.groups, most = tiles <= 8 ? 1 : (tiles + 3) / 4;
+        const int64_t splits = wgs > 0 ? (2 * cus + wgs - 1) / wgs : 1;
+        p.splits = (int)(splits < most ? splits : most > 1 ? most : 1);
+    } else {
+        struct Shape { int rows, per_cu; float alone, full; };
+        static const Shape one[] = {{64, 2, 1.37f, 1.65f}, {128, 1, 1.37f, 1.37f}, {256, 1, 2.1f, 2.1f}};
+        static const Shape two[] = {{64, 2, 2.3f, 3.4f}, {128, 1, 2.9f, 3.5f}};
+        static const int cuts[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
+        const Shape *shapes = half ? one : two;
+        const int n = half ? (c.nb > 4 ? 2 : 3) : (c.nb > 4 ? 1 : 2);
+        const float width = (float)c.nb / 4;
+        float best = 0;
+        p.splits = 0;
+        for (int i = 0; i < n; ++i) {
+            const int64_t groups = (rows + shapes[i].rows - 1) / shapes[i].rows, wgs = batch * c.kv_heads * groups;
+            for (int s : cuts) {
+                if (s > 1 && s > tiles / 2)
+                    break;
+                const int64_t all = wgs * s, at_once = (int64_t)shapes[i].per_cu * cus;
+                const float tile = width * (all > cus ? shapes[i].full : shapes[i].alone);
+                float t = (float)((all + at_once - 1) / at_once) * (float)((tiles + s - 1) / s) * tile;
+                if (s > 1)      // the parts, written and read at 4.5 TB/s
+                    t += 4.f + (float)r * (float)s * (float)(256 * c.nb) / 4.5e6f;
+                if (p.splits == 0 || t < best) {
+                    best = t;
+                    p.rows = shapes[i].rows;
+                    p.groups = (int)groups;
+                    p.splits = s;
+                }
+            }
+        }
+    }
     p.bytes = p.splits == 1 ? 0 : p.splits * r * (32 * c.nb + 2) * 4;
     return p;
 }

@@ -67,36 +67,39 @@ class AttnStruct(ctypes.Structure):
 
 
 _DTYPES = {torch.float32: 0, torch.float16: 1}
+_F32, _I32, _I64T, _U8 = torch.float32, torch.int32, torch.int64, torch.uint8
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+# The checks below stand on the path of every decoded token, where a call costs
+# the host about as much as its kernel: one condition each, the message only
+# made when it fails.
 
 
-def _stream(device) -> int:
-    return torch._C._cuda_getCurrentRawStream(device.index)
-
-
-def _rows(t, what, tokens=None, heads=None, dim=None):
-    """Checks an activation tensor [tokens, heads, dim]; its dtype code."""
+def _rows(t, what):
+    """(dtype code, tokens, heads, head_dim, token stride) of an activation
+    tensor, checked."""
+    shape, stride = t.shape, t.stride()
     code = _DTYPES.get(t.dtype)
-    if code is None or not t.is_cuda or t.dim() != 3:
+    if code is None or len(shape) != 3 or not t.is_cuda:
         raise ValueError("%s must be a float32 or float16 device tensor [tokens, heads, head_dim]" % what)
-    T, H, D = t.shape
-    if (tokens is not None and T != tokens) or (heads is not None and H != heads) or (dim is not None and D != dim):
-        raise ValueError("%s has shape %s, expected [%s, %s, %s]" % (what, tuple(t.shape), tokens, heads, dim))
-    s = t.stride()
-    if (D > 1 and s[2] != 1) or (H > 1 and s[1] != D):
+    T, H, D = shape
+    if (stride[2] != 1 and D > 1) or (stride[1] != D and H > 1):
         raise ValueError("the heads of a token of %s must be contiguous" % what)
-    return code
+    return code, T, H, D, stride[0]
 
 
 def _index(t, what, device, dim=1):
-    if t.dtype != torch.int32 or t.device != device or t.dim() != dim or not t.is_contiguous():
+    if t.dtype is not _I32 or t.device != device or t.dim() != dim or not t.is_contiguous():
         raise ValueError("%s must be a contiguous int32 tensor of %d dimension(s) on %s" % (what, dim, device))
 
 
 def _angles(cs, tokens, device):
-    if cs.dtype != torch.float32 or cs.device != device or not cs.is_contiguous() or cs.dim() != 3 \
-            or cs.shape[0] != tokens or cs.shape[2] != 2:
-        raise ValueError("cs must be a contiguous float32 tensor [tokens, pairs, 2] on %s" % device)
-    return cs.shape[1]
+    """The pairs of a table of angles, checked."""
+    shape = cs.shape
+    if cs.dtype is not _F32 or len(shape) != 3 or shape[0] != tokens or shape[2] != 2 or cs.device != device \
+            or not cs.is_contiguous():
+        raise ValueError("cs must be a contiguous float32 tensor [%d, pairs, 2] on %s" % (tokens, device))
+    return shape[1]
 
 
 def rope_freqs(rot, base=10000.0, scaling=None, factor=1.0, trained=0.0, beta_fast=None, beta_slow=1.0,
@@ -126,34 +129,41 @@ def rope_freqs(rot, base=10000.0, scaling=None, factor=1.0, trained=0.0, beta_fa
 def rope_angles(pos, freqs, magnitude=1.0, out=None):
     """fp32 [tokens, pairs, 2]: cos and sin (times magnitude) of pos[t] *
     freqs[i].  pos int32 [tokens], freqs float64 [pairs], both on the device."""
-    if not pos.is_cuda:
-        raise ValueError("pos must be on a HIP device")
     dev = pos.device
     _index(pos, "pos", dev)
-    if freqs.dtype != torch.float64 or freqs.device != dev or freqs.dim() != 1 or not freqs.is_contiguous():
-        raise ValueError("freqs must be a contiguous float64 tensor [pairs] on %s" % dev)
+    if not pos.is_cuda or freqs.dtype is not torch.float64 or freqs.device != dev or freqs.dim() != 1 \
+            or not freqs.is_contiguous():
+        raise ValueError("pos must be on a HIP device and freqs a contiguous float64 tensor [pairs] on the same")
     T, P = pos.shape[0], freqs.shape[0]
     if out is None:
-        out = torch.empty((T, P, 2), dtype=torch.float32, device=dev)
-    elif out.shape != (T, P, 2) or _angles(out, T, dev) != P:
+        out = torch.empty((T, P, 2), dtype=_F32, device=dev)
+    elif _angles(out, T, dev) != P:
         raise ValueError("out must be [tokens, pairs, 2]")
-    _call(lib.qkv_rope_angles(pos.data_ptr(), T, freqs.data_ptr(), P, magnitude, out.data_ptr(), _stream(dev)),
-          "qkv_rope_angles")
+    status = lib.qkv_rope_angles(pos.data_ptr(), T, freqs.data_ptr(), P, magnitude, out.data_ptr(),
+                                 _raw_stream(dev.index))
+    if status:
+        _call(status, "qkv_rope_angles")
     return out
 
 
 def rope(x, cs, interleaved=False, out=None):
     """x [tokens, heads, head_dim] with the first 2 * pairs dims of every head
     rotated by cs (rope_angles).  out may be x (in place)."""
-    code = _rows(x, "x")
-    T, H, D = x.shape
-    pairs = _angles(cs, T, x.device)
+    code, T, H, D, stride = _rows(x, "x")
+    dev = x.device
+    pairs = _angles(cs, T, dev)
     if out is None:
-        out = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
-    elif _rows(out, "out", T, H, D) != code or out.device != x.device:
-        raise ValueError("out must have the type and device of x")
-    _call(lib.qkv_rope(code, x.data_ptr(), x.stride(0), T, H, D, cs.data_ptr(), pairs, 1 if interleaved else 0,
-                       out.data_ptr(), out.stride(0), _stream(x.device)), "qkv_rope")
+        out = torch.empty_like(x) if x.is_contiguous() else torch.empty((T, H, D), dtype=x.dtype, device=dev)
+        out_stride = H * D
+    else:
+        got = _rows(out, "out")
+        out_stride = got[4]
+        if got[:4] != (code, T, H, D) or out.device != dev:
+            raise ValueError("out must have the type, shape and device of x")
+    status = lib.qkv_rope(code, x.data_ptr(), stride, T, H, D, cs.data_ptr(), pairs, 1 if interleaved else 0,
+                          out.data_ptr(), out_stride, _raw_stream(dev.index))
+    if status:
+        _call(status, "qkv_rope")
     return out
 
 
@@ -180,6 +190,7 @@ class KVCache:
         self.device = self.k.device
         self.type, self.kv_heads, self.head_dim = qtype, kv_heads, head_dim
         self.pages, self.page_size = pages, page_size
+        self.scale = 1.0 / math.sqrt(head_dim)
         self.struct = CacheStruct(self.k.data_ptr(), self.v.data_ptr(), pages, qtype, kv_heads, head_dim, page_size)
         self.ptr = ctypes.addressof(self.struct)
 
@@ -187,20 +198,20 @@ class KVCache:
 def kv_append(cache, k, v, slots, cs=None, interleaved=False):
     """Write k and v [tokens, kv_heads, head_dim] to the slots (int32; -1
     skips a token), k rotated by cs first if given."""
-    T = k.shape[0]
-    code = _rows(k, "k", None, cache.kv_heads, cache.head_dim)
-    if _rows(v, "v", T, cache.kv_heads, cache.head_dim) != code:
-        raise ValueError("k and v must have the same type")
+    code, T, H, D, k_stride = _rows(k, "k")
+    got = _rows(v, "v")
     dev = cache.device
-    if k.device != dev or v.device != dev:
-        raise ValueError("k, v and the cache must be on the same device")
+    if H != cache.kv_heads or D != cache.head_dim or got[:4] != (code, T, H, D) or k.device != dev or v.device != dev:
+        raise ValueError("k and v must be [tokens, %d, %d] of one type on %s" % (cache.kv_heads, cache.head_dim, dev))
     _index(slots, "slots", dev)
     if slots.shape[0] != T:
         raise ValueError("slots must have one entry per token")
     pairs = _angles(cs, T, dev) if cs is not None else 0
-    _call(lib.qkv_append(cache.ptr, code, k.data_ptr(), k.stride(0), v.data_ptr(), v.stride(0), T, slots.data_ptr(),
-                         cs.data_ptr() if cs is not None else None, pairs, 1 if interleaved else 0, _stream(dev)),
-          "qkv_append")
+    status = lib.qkv_append(cache.ptr, code, k.data_ptr(), k_stride, v.data_ptr(), got[4], T, slots.data_ptr(),
+                            cs.data_ptr() if cs is not None else None, pairs, 1 if interleaved else 0,
+                            _raw_stream(dev.index))
+    if status:
+        _call(status, "qkv_append")
 
 
 def kv_read(cache, slots, dtype=torch.float32, k_out=None, v_out=None):
@@ -213,16 +224,20 @@ def kv_read(cache, slots, dtype=torch.float32, k_out=None, v_out=None):
         raise ValueError("dtype must be torch.float32 or torch.float16")
     n = slots.shape[0]
     shape = (n, cache.kv_heads, cache.head_dim)
-    outs = []
-    for t in (k_out, v_out):
-        if t is None:
-            t = torch.empty(shape, dtype=dtype, device=dev)
-        elif t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != dev:
-            raise ValueError("outputs must be contiguous %s tensors of shape %s on %s" % (dtype, shape, dev))
-        outs.append(t)
-    _call(lib.qkv_read(cache.ptr, code, slots.data_ptr(), n, outs[0].data_ptr(), outs[1].data_ptr(), _stream(dev)),
-          "qkv_read")
-    return outs[0], outs[1]
+    if k_out is None and v_out is None:
+        k_out = torch.empty(shape, dtype=dtype, device=dev)
+        v_out = torch.empty_like(k_out)
+    else:
+        outs = [torch.empty(shape, dtype=dtype, device=dev) if t is None else t for t in (k_out, v_out)]
+        for t in outs:
+            if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != dev:
+                raise ValueError("outputs must be contiguous %s tensors of shape %s on %s" % (dtype, shape, dev))
+        k_out, v_out = outs
+    status = lib.qkv_read(cache.ptr, code, slots.data_ptr(), n, k_out.data_ptr(), v_out.data_ptr(),
+                          _raw_stream(dev.index))
+    if status:
+        _call(status, "qkv_read")
+    return k_out, v_out
 
 
 def kv_move(cache, src, dst):
@@ -231,53 +246,57 @@ def kv_move(cache, src, dst):
     dev = cache.device
     _index(src, "src", dev, 2)
     _index(dst, "dst", dev, 2)
-    if src.shape != dst.shape:
+    groups, n = src.shape
+    if dst.shape != src.shape:
         raise ValueError("src and dst must have the same shape")
-    _call(lib.qkv_move(cache.ptr, src.data_ptr(), dst.data_ptr(), src.shape[0], src.shape[1], _stream(dev)),
-          "qkv_move")
+    status = lib.qkv_move(cache.ptr, src.data_ptr(), dst.data_ptr(), groups, n, _raw_stream(dev.index))
+    if status:
+        _call(status, "qkv_move")
 
 
-def _attn_struct(cache, q, table, ctx, qstart, mask, max_q, max_ctx):
-    code = _rows(q, "q", None, None, cache.head_dim)
+def _sizes(cache, q, table, ctx, qstart, mask, max_q, max_ctx):
+    """The qkv_attn of a call without its output, scale and workspace."""
+    code, T, H, D, stride = _rows(q, "q")
     dev = cache.device
-    T, H, _ = q.shape
-    if q.device != dev:
-        raise ValueError("q and the cache must be on the same device")
+    if D != cache.head_dim or q.device != dev:
+        raise ValueError("q must be [tokens, heads, %d] on %s" % (cache.head_dim, dev))
     _index(table, "table", dev, 2)
     B, cols = table.shape
+    ctx_ptr = start_ptr = mask_ptr = None
+    words = 0
     if ctx is not None:
         _index(ctx, "ctx", dev)
         if ctx.shape[0] != B:
             raise ValueError("ctx must have one entry per sequence")
+        ctx_ptr = ctx.data_ptr()
     if qstart is not None:
         _index(qstart, "qstart", dev)
         if qstart.shape[0] != B + 1:
             raise ValueError("qstart must have batch + 1 entries")
-    words = 0
+        start_ptr = qstart.data_ptr()
     if mask is not None:
-        if mask.dtype != torch.int64 or mask.device != dev or mask.dim() != 2 or mask.shape[0] != T \
-                or not mask.is_contiguous():
+        if mask.dtype is not _I64T or mask.device != dev or mask.dim() != 2 or mask.shape[0] != T \
+                or mask.shape[1] == 0 or not mask.is_contiguous():
             raise ValueError("mask must be a contiguous int64 tensor [tokens, words] on %s" % dev)
-        words = mask.shape[1]
+        mask_ptr, words = mask.data_ptr(), mask.shape[1]
     if max_q is None:
         max_q = T if qstart is not None or B == 0 else -(-T // B)
     if max_ctx is None:
         max_ctx = min(cols * cache.page_size, (1 << 31) - 65)
-    return AttnStruct(q.data_ptr(), None, q.stride(0), 0, T, B, table.data_ptr(), cols,
-                      ctx.data_ptr() if ctx is not None else None, qstart.data_ptr() if qstart is not None else None,
-                      mask.data_ptr() if words else None, words, max_q, max_ctx, None, 0, H, code, 1.0, 0)
+    return AttnStruct(q.data_ptr(), None, stride, H * D, T, B, table.data_ptr(), cols, ctx_ptr, start_ptr, mask_ptr,
+                      words, max_q, max_ctx, None, 0, H, code, 1.0, 0)
 
 
 def attention_workspace(cache, q, table, max_q=None, max_ctx=None, qstart=None):
     """A workspace tensor for attention() calls of these sizes (one call at a
     time may use it)."""
-    a = _attn_struct(cache, q, table, None, qstart, None, max_q, max_ctx)
+    a = _sizes(cache, q, table, None, qstart, None, max_q, max_ctx)
     with torch.cuda.device(cache.device):
         n = lib.qkv_attn_workspace(cache.ptr, ctypes.addressof(a))
     if n < 0:
         raise ValueError("no attention of these sizes: q %s, table %s, max_q %s, max_ctx %s"
                          % (tuple(q.shape), tuple(table.shape), max_q, max_ctx))
-    return torch.empty(n, dtype=torch.uint8, device=cache.device)
+    return torch.empty(n, dtype=_U8, device=cache.device)
 
 
 def attention(cache, q, table, ctx, qstart=None, mask=None, scale=None, max_q=None, max_ctx=None, out=None,
@@ -288,20 +307,23 @@ def attention(cache, q, table, ctx, qstart=None, mask=None, scale=None, max_q=No
     those up to themselves; int64 [tokens, words]: bit j of a row's words lets it
     see new token j.  scale None: head_dim ** -0.5.  max_q / max_ctx bound the
     new and all tokens of a sequence (defaults: what q and the table hold)."""
-    a = _attn_struct(cache, q, table, ctx, qstart, mask, max_q, max_ctx)
-    if mask is not None and a.mask_words == 0:
-        raise ValueError("mask must have at least one word per row")
+    a = _sizes(cache, q, table, ctx, qstart, mask, max_q, max_ctx)
     dev = cache.device
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    elif _rows(out, "out", *q.shape) != a.dtype or out.device != dev:
-        raise ValueError("out must have the type and device of q")
-    a.out, a.out_stride = out.data_ptr(), out.stride(0)
-    a.scale = scale if scale is not None else 1.0 / math.sqrt(cache.head_dim)
+        out = torch.empty_like(q) if q.is_contiguous() else torch.empty(q.shape, dtype=q.dtype, device=dev)
+    else:
+        got = _rows(out, "out")
+        if out.shape != q.shape or got[0] != a.dtype or out.device != dev:
+            raise ValueError("out must have the type, shape and device of q")
+        a.out_stride = got[4]
+    a.out = out.data_ptr()
+    a.scale = scale if scale is not None else cache.scale
     if workspace is None:
         workspace = attention_workspace(cache, q, table, max_q=max_q, max_ctx=max_ctx, qstart=qstart)
-    elif workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
+    elif workspace.dtype is not _U8 or workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on %s" % dev)
     a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
-    _call(lib.qkv_attention(cache.ptr, ctypes.addressof(a), _stream(dev)), "qkv_attention")
+    status = lib.qkv_attention(cache.ptr, ctypes.addressof(a), _raw_stream(dev.index))
+    if status:
+        _call(status, "qkv_attention")
     return out
