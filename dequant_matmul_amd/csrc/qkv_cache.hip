@@ -193,6 +193,10 @@ rope_kernel(const I *x, int64_t stride, int64_t tokens, int heads, int dim, cons
     }
 }
 
+// Items of one launch (gridDim.y ends at 65535); longer calls take several, since a
+// loop in the kernel costs the single token 0.7 us.
+constexpr int64_t GRID_MOST = 65535;
+
 // ------------------------------------------------------------------ append --
 
 __device__ __forceinline__ float swap_f(float v) { return dpp_f(v, 0xB1); }   // with the neighbouring lane
@@ -201,44 +205,15 @@ __device__ __forceinline__ uint32_t swap_u(uint32_t v)
     return __builtin_bit_cast(uint32_t, dpp_f(__builtin_bit_cast(float, v), 0xB1));
 }
 
-// A thread takes 16 values of a row (half a block): blockIdx.x a window of
-// tokens, y the kv head, z 0 for K and 1 for V.  Two neighbouring lanes share
-// a block and exchange its maximum.  K goes out in 8-dim units, V byte by byte
-// (a token is one byte of every 16): a window's tokens are usually neighbours,
-// so that the L2 gathers whole lines.
-template <int NB, int KT, typename I>
-__global__ void __launch_bounds__(256)
-append_kernel(KvView c, const I *__restrict__ kin, int64_t k_stride, const I *__restrict__ vin, int64_t v_stride,
-              int64_t tokens, const int32_t *__restrict__ slots, const float *__restrict__ cs, int pairs, int inter)
+// Half a block (dims 16 hb ..) of one row: quantize and store.  Two neighbouring
+// lanes share a block and exchange its maximum.  K goes out in 8-dim units, V byte
+// by byte (a token is one byte of every 16): a window's tokens are usually
+// neighbours, so that the L2 gathers whole lines.
+template <int NB, int KT>
+__device__ __forceinline__ void store_half(const KvView &c, bool is_v, int64_t tile, int key, int hb, float (&x)[16])
 {
 #pragma clang fp contract(off)
     using L = KvLay<NB, KT>;
-    constexpr int HB = 2 * NB, WIN = 256 / HB;
-    const bool is_v = blockIdx.z != 0;
-    const int head = blockIdx.y, dim = c.head_dim;
-    const int tt = threadIdx.x / HB, hb = threadIdx.x % HB;
-    const int64_t t = (int64_t)blockIdx.x * WIN + tt;
-    int64_t tile;
-    int key;
-    if (tt >= WIN || t >= tokens || !slot_at<L>(c, slots[t], head, tile, key))
-        return;
-
-    const I *row = is_v ? vin + t * v_stride + (int64_t)head * dim : kin + t * k_stride + (int64_t)head * dim;
-    float x[16];
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-        const int d0 = 16 * hb + 8 * g;
-        float *y = x + 8 * g;
-        if (d0 < dim) {
-            load8(row + d0, y);
-            if (!is_v && pairs > 0)
-                rotate8(y, d0, row, cs + t * 2 * pairs, pairs, inter);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                y[i] = 0.f;
-        }
-    }
 #pragma unroll
     for (int i = 0; i < 16; ++i)
         x[i] = x[i] == x[i] ? fminf(fmaxf(x[i], -65504.f), 65504.f) : 0.f;
@@ -332,138 +307,268 @@ append_kernel(KvView c, const I *__restrict__ kin, int64_t k_stride, const I *__
     }
 }
 
+// A thread takes 16 values of a row: blockIdx.x a window of tokens, y the kv head,
+// z 0 for K and 1 for V.  Where whole heads of whole blocks are rotated in the half
+// layout (TWIN), a thread of K takes both halves of its 16 pairs instead, of twice
+// as many tokens: neither is loaded twice (8185 tokens of 8 x 128, Q4_0: 21 us with
+// each half loading the other's values too).
+template <int NB, int KT, typename I, bool TWIN>
+__global__ void __launch_bounds__(256)
+append_kernel(KvView c, const I *__restrict__ kin, int64_t k_stride, const I *__restrict__ vin, int64_t v_stride,
+              int64_t tokens, const int32_t *__restrict__ slots, const float *__restrict__ cs, int pairs, int inter)
+{
+#pragma clang fp contract(off)
+    using L = KvLay<NB, KT>;
+    constexpr int HB = 2 * NB, WIN = 256 / HB;
+    const bool is_v = blockIdx.z != 0;
+    const int head = blockIdx.y, dim = c.head_dim;
+    int64_t tile;
+    int key;
+    if (TWIN && !is_v) {
+        const int tt = threadIdx.x / NB, hb = threadIdx.x % NB;
+        const int64_t t = (int64_t)blockIdx.x * (2 * WIN) + tt;
+        if (tt >= 2 * WIN || t >= tokens || !slot_at<L>(c, slots[t], head, tile, key))
+            return;
+        const I *row = kin + t * k_stride + (int64_t)head * dim + 16 * hb;
+        const float *ct = cs + t * (32 * NB) + 32 * hb;
+        float a[16], b[16];
+        load8(row, a);
+        load8(row + 8, a + 8);
+        load8(row + 16 * NB, b);
+        load8(row + 16 * NB + 8, b + 8);
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            float co[4], si[4];
+            load_cs4(ct + 8 * g, co, si);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float x = a[4 * g + i], y = b[4 * g + i];
+                a[4 * g + i] = x * co[i] - y * si[i];
+                b[4 * g + i] = y * co[i] + x * si[i];
+            }
+        }
+        store_half<NB, KT>(c, false, tile, key, hb, a);
+        store_half<NB, KT>(c, false, tile, key, hb + NB, b);
+        return;
+    }
+    const int tt = threadIdx.x / HB, hb = threadIdx.x % HB;
+    const int64_t t = (int64_t)blockIdx.x * WIN + tt;
+    if (tt >= WIN || t >= tokens || !slot_at<L>(c, slots[t], head, tile, key))
+        return;
+    const I *row = is_v ? vin + t * v_stride + (int64_t)head * dim : kin + t * k_stride + (int64_t)head * dim;
+    float x[16];
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        const int d0 = 16 * hb + 8 * g;
+        float *y = x + 8 * g;
+        if (d0 < dim) {
+            load8(row + d0, y);
+            if (!TWIN && !is_v && pairs > 0)
+                rotate8(y, d0, row, cs + t * 2 * pairs, pairs, inter);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                y[i] = 0.f;
+        }
+    }
+    store_half<NB, KT>(c, is_v, tile, key, hb, x);
+}
+
 // -------------------------------------------------------------------- read --
 
-// A thread decodes 8 dims of a row; blockIdx.y the kv head, z 0 for K, 1 for V.
+// A workgroup takes READ_ROWS rows: blockIdx.x the kv head, y which rows, z 0 for K
+// and 1 for V.  Head first: with 8 kv heads each XCD (workgroup id modulo 8) works
+// on one head, whose pages stay in its L2 (8185 tokens in any order from an F16
+// cache: 32 us numbered rows first, 21 so).
+//   K: a thread decodes a unit of 8 dims.
+//   V: a wave takes whole rows, lane l the codes at dim (Q4: byte) l + 64 k: 16
+//      neighbouring lanes then read 16 neighbouring 16-byte runs (a token is one
+//      byte of each), two lines; eight dims to a thread as for K would touch a line
+//      per lane (8185 tokens of 8 x 128, Q4_0, in any order: 25 us both buffers).
+constexpr int READ_ROWS = 16;
+
+template <int NB, int KT, typename O>
+__device__ __forceinline__ void read_k(const KvView &c, int head, int dim, const int32_t *slots, int64_t i0, int64_t n,
+                                       O *k_out)
+{
+    using L = KvLay<NB, KT>;
+    constexpr int U = 4 * NB;
+            for (int it = threadIdx.x; it < READ_ROWS * U; it += 256) {
+                const int64_t i = i0 + it / U;
+                const int u = it % U, b = u >> 2;
+                if (i >= n || 8 * u >= dim)
+                    continue;
+                float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                int64_t tile;
+                int key;
+                if (slot_at<L>(c, slots[i], head, tile, key)) {
+                    const uint8_t *unit = c.k + tile + L::k_unit(key, b, u & 3);
+                    if constexpr (KT == KV_F16) {
+                        load8((const _Float16 *)unit, x);
+                    } else {
+                        const float d = h2f(*(const uint16_t *)(c.k + tile + L::k_scale(key, b)));
+                        if constexpr (KT == KV_Q8) {
+                            const uint2 w = *(const uint2 *)unit;
+    #pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                x[j] = d * (float)((int)(((j < 4 ? w.x : w.y) >> (8 * (j & 3))) & 255u) - 128);
+                        } else {
+                            const uint32_t w = *(const uint32_t *)unit;
+    #pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                x[j] = d * (float)((int)((w >> (4 * j)) & 15u) - 8);
+                        }
+                    }
+                }
+                store8(k_out + (i * c.kv_heads + head) * dim + 8 * u, x);
+            }
+}
+
+template <int NB, int KT, typename O>
+__device__ __forceinline__ void read_v(const KvView &c, int head, int dim, const int32_t *slots, int64_t i0, int64_t n,
+                                       O *v_out)
+{
+    using L = KvLay<NB, KT>;
+    constexpr int RPW = READ_ROWS / 4;                              // rows of a wave, loaded together
+    constexpr int CODES = KT == KV_Q4 ? L::DP / 2 : L::DP, KS = (CODES + 63) / 64;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    uint32_t code[RPW][KS], scale[RPW][KS];
+#pragma unroll
+    for (int r = 0; r < RPW; ++r) {
+        const int64_t i = i0 + wave * RPW + r;
+        int64_t tile = 0;
+        int key = 0;
+        const bool live = i < n && slot_at<L>(c, slots[i], head, tile, key);
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+            const int at = lane + 64 * k;
+            // code of dim `at`, or the byte of dims 32 b + m and 32 b + 16 + m
+            const int t = KT == KV_Q4 ? 2 * (at >> 4) : at >> 4, b = t >> 1;
+            code[r][k] = KT == KV_Q8 ? 128 : KT == KV_Q4 ? 0x88 : 0;
+            scale[r][k] = 0;
+            if (live && (CODES % 64 == 0 || at < CODES)) {
+                const uint8_t *p = c.v + tile + L::v_code(key, t, at & 15);
+                code[r][k] = KT == KV_F16 ? *(const uint16_t *)p : *p;
+                if constexpr (KT != KV_F16)
+                    scale[r][k] = *(const uint16_t *)(c.v + tile + L::v_scale(key, b));
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < RPW; ++r) {
+        const int64_t i = i0 + wave * RPW + r;
+        if (i >= n)
+            return;
+        O *out = v_out + (i * c.kv_heads + head) * dim;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+            const int at = lane + 64 * k;
+            const float d = h2f(scale[r][k]);
+            if constexpr (KT == KV_Q4) {
+                const int d0 = 32 * (at >> 4) + (at & 15);
+                if (d0 < dim)
+                    out[d0] = (O)(d * (float)((int)(code[r][k] & 15u) - 8));
+                if (d0 + 16 < dim)
+                    out[d0 + 16] = (O)(d * (float)((int)(code[r][k] >> 4) - 8));
+            } else if (at < dim) {
+                out[at] = (O)(KT == KV_F16 ? h2f(code[r][k]) : d * (float)((int)code[r][k] - 128));
+            }
+        }
+    }
+}
+
 template <int NB, int KT, typename O>
 __global__ void __launch_bounds__(256)
 read_kernel(KvView c, const int32_t *__restrict__ slots, int64_t n, O *__restrict__ k_out, O *__restrict__ v_out)
 {
-    using L = KvLay<NB, KT>;
-    constexpr int U = 4 * NB, ROWS = 256 / U;
-    const bool is_v = blockIdx.z != 0;
-    O *out = is_v ? v_out : k_out;
-    const int r = threadIdx.x / U, u = threadIdx.x % U, head = blockIdx.y;
-    const int64_t i = (int64_t)blockIdx.x * ROWS + r;
-    if (out == nullptr || r >= ROWS || i >= n || 8 * u >= c.head_dim)
-        return;
-    float x[8];
-    int64_t tile;
-    int key;
-    if (!slot_at<L>(c, slots[i], head, tile, key)) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            x[j] = 0.f;
-    } else {
-        const uint8_t *base = (is_v ? c.v : c.k) + tile;
-        const int b = u >> 2, t = u >> 1, m0 = 8 * (u & 1);
-        if constexpr (KT == KV_F16) {
-            if (!is_v) {
-                load8((const _Float16 *)(base + L::k_unit(key, b, u & 3)), x);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    x[j] = h2f(*(const uint16_t *)(base + L::v_code(key, t, m0 + j)));
-            }
-        } else {
-            const float d = h2f(*(const uint16_t *)(base + (is_v ? L::v_scale(key, b) : L::k_scale(key, b))));
-            int q[8];
-            if constexpr (KT == KV_Q8) {
-                if (!is_v) {
-                    const uint2 w = *(const uint2 *)(base + L::k_unit(key, b, u & 3));
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        q[j] = (int)(((j < 4 ? w.x : w.y) >> (8 * (j & 3))) & 255u) - 128;
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        q[j] = (int)base[L::v_code(key, t, m0 + j)] - 128;
-                }
-            } else {
-                if (!is_v) {
-                    const uint32_t w = *(const uint32_t *)(base + L::k_unit(key, b, u & 3));
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        q[j] = (int)((w >> (4 * j)) & 15u) - 8;
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        q[j] = (int)((base[L::v_code(key, t, m0 + j)] >> (4 * (t & 1))) & 15u) - 8;
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                x[j] = d * (float)q[j];
-        }
-    }
-    store8(out + ((int64_t)i * c.kv_heads + head) * c.head_dim + 8 * u, x);
+    const int64_t i0 = (int64_t)blockIdx.y * READ_ROWS;
+    if (blockIdx.z == 0 && k_out != nullptr)
+        read_k<NB, KT>(c, blockIdx.x, c.head_dim, slots, i0, n, k_out);
+    if (blockIdx.z != 0 && v_out != nullptr)
+        read_v<NB, KT>(c, blockIdx.x, c.head_dim, slots, i0, n, v_out);
 }
 
 // -------------------------------------------------------------------- move --
 
-// One workgroup moves the rows of one group, kv head and buffer: every source
-// piece into LDS, then every piece out.  K pieces are 8-dim units, V pieces
+// All pieces of type P of n rows between the cache and LDS (or back): piece p of
+// row i lies at at(i, p) in the buffer and at loc[i * per + p].  Four to a thread
+// are on their way together.
+template <typename P, class F>
+__device__ __forceinline__ void move_pieces(bool out, int n, int per, P *loc, uint8_t *buf, F at)
+{
+    constexpr int TOGETHER = 4;
+    const int all = n * per;
+    for (int it = threadIdx.x; it < all; it += 256 * TOGETHER) {
+        P x[TOGETHER];
+        int64_t off[TOGETHER];
+#pragma unroll
+        for (int k = 0; k < TOGETHER; ++k) {
+            const int j = it + 256 * k;
+            off[k] = j < all ? at(j / per, j % per) : -1;
+            if (off[k] >= 0)
+                x[k] = out ? loc[j] : *(const P *)(buf + off[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < TOGETHER; ++k)
+            if (off[k] >= 0) {
+                if (out)
+                    *(P *)(buf + off[k]) = x[k];
+                else
+                    loc[it + 256 * k] = x[k];
+            }
+    }
+}
+
+// A workgroup moves the rows of one group, kv head and buffer: every source piece
+// into LDS, then every piece out.  K pieces are dwords of 8-dim units, V pieces
 // single codes (16 tokens share a 16-byte run), scales fp16 in both.
 template <int NB, int KT>
 __global__ void __launch_bounds__(256)
 move_kernel(KvView c, const int32_t *__restrict__ src, const int32_t *__restrict__ dst, int n)
 {
     using L = KvLay<NB, KT>;
-    constexpr int KU = 4 * NB;                                   // K units of a row
-    constexpr int VB = KT == KV_F16 ? 2 : 1;                     // bytes of a V piece
-    constexpr int VU = KT == KV_Q4 ? L::DP / 2 : L::DP;          // V pieces of a row
-    constexpr int SC = KT == KV_F16 ? 0 : NB;
-    __shared__ __align__(16) uint8_t rows[KV_MOVE_MAX * 64 * NB];
+    constexpr int UD = L::UNIT / 4, KP = 4 * NB * UD;            // dwords of a unit, of a K row
+    constexpr int VP = KT == KV_Q4 ? L::DP / 2 : L::DP;          // codes (bytes) of a V row
+    typedef typename std::conditional<KT == KV_F16, uint16_t, uint8_t>::type vcode;
+    __shared__ __align__(16) uint8_t codes[KV_MOVE_MAX * 64 * NB];
+    __shared__ uint16_t scales[KV_MOVE_MAX * NB];
+    __shared__ int64_t tiles[2][KV_MOVE_MAX];
+    __shared__ int keys[2][KV_MOVE_MAX];                         // -1: the pair is skipped
     const bool is_v = blockIdx.z != 0;
-    const int head = blockIdx.y;
-    src += (int64_t)blockIdx.x * n;
-    dst += (int64_t)blockIdx.x * n;
+    const int head = blockIdx.x;
     uint8_t *buf = is_v ? c.v : c.k;
-    const int pieces = (is_v ? VU : KU) + SC;
+    src += (int64_t)blockIdx.y * n;
+    dst += (int64_t)blockIdx.y * n;
+    if ((int)threadIdx.x < n) {
+        const int i = threadIdx.x;
+        int64_t ts = 0, td = 0;
+        int ks, kd;
+        if (!slot_at<L>(c, src[i], head, ts, ks) || !slot_at<L>(c, dst[i], head, td, kd))
+            ks = kd = -1;
+        tiles[0][i] = ts;
+        tiles[1][i] = td;
+        keys[0][i] = ks;
+        keys[1][i] = kd;
+    }
+    __syncthreads();
 #pragma unroll
     for (int phase = 0; phase < 2; ++phase) {
-        for (int it = threadIdx.x; it < n * pieces; it += 256) {
-            const int i = it / pieces, p = it - i * pieces;
-            int64_t ts, td;
-            int ks, kd;
-            if (!slot_at<L>(c, src[i], head, ts, ks) || !slot_at<L>(c, dst[i], head, td, kd))
-                continue;
-            const int key = phase ? kd : ks;
-            uint8_t *base = buf + (phase ? td : ts), *loc = rows + i * (64 * NB);
-            if (p < SC) {
-                uint8_t *g = base + (is_v ? L::v_scale(key, p) : L::k_scale(key, p));
-                uint16_t *l = (uint16_t *)(loc + L::ROW_BYTES - 2 * NB) + p;
-                if (phase)
-                    *(uint16_t *)g = *l;
-                else
-                    *l = *(const uint16_t *)g;
-            } else if (!is_v) {
-                const int u = p - SC;
-                uint8_t *g = base + L::k_unit(key, u >> 2, u & 3);
-                uint32_t *l = (uint32_t *)(loc + u * L::UNIT);
-#pragma unroll
-                for (int w = 0; w < L::UNIT / 4; ++w) {
-                    if (phase)
-                        ((uint32_t *)g)[w] = l[w];
-                    else
-                        l[w] = ((const uint32_t *)g)[w];
-                }
-            } else {
-                const int u = p - SC, m = u & 15, t = KT == KV_Q4 ? 2 * (u >> 4) : u >> 4;
-                uint8_t *g = base + L::v_code(key, t, m), *l = loc + u * VB;
-                if constexpr (VB == 2) {
-                    if (phase)
-                        *(uint16_t *)g = *(const uint16_t *)l;
-                    else
-                        *(uint16_t *)l = *(const uint16_t *)g;
-                } else {
-                    if (phase)
-                        *g = *l;
-                    else
-                        *l = *g;
-                }
-            }
-        }
+        const bool out = phase == 1;
+        if (is_v)
+            move_pieces(out, n, VP, (vcode *)codes, buf, [&](int i, int p) -> int64_t {
+                const int key = keys[phase][i];
+                return key < 0 ? -1 : tiles[phase][i] + L::v_code(key, KT == KV_Q4 ? 2 * (p >> 4) : p >> 4, p & 15);
+            });
+        else
+            move_pieces(out, n, KP, (uint32_t *)codes, buf, [&](int i, int p) -> int64_t {
+                const int key = keys[phase][i], u = p / UD;
+                return key < 0 ? -1 : tiles[phase][i] + L::k_unit(key, u >> 2, u & 3) + 4 * (p % UD);
+            });
+        if constexpr (KT != KV_F16)
+            move_pieces(out, n, NB, scales, buf, [&](int i, int b) -> int64_t {
+                const int key = keys[phase][i];
+                return key < 0 ? -1 : tiles[phase][i] + (is_v ? L::v_scale(key, b) : L::k_scale(key, b));
+            });
         __syncthreads();
     }
 }
@@ -529,8 +634,14 @@ static hipError_t append_of(const KvView &c, const void *k, int64_t ks, const vo
 {
     constexpr int WIN = 256 / (2 * NB);
     const dim3 grid((unsigned)((tokens + WIN - 1) / WIN), (unsigned)c.kv_heads, 2);
-    hipLaunchKernelGGL((append_kernel<NB, KT, I>), grid, dim3(256), 0, s, c, (const I *)k, ks, (const I *)v, vs, tokens,
-                       slots, cs, pairs, inter);
+    if constexpr (NB % 2 == 0)
+        if (!inter && pairs == 16 * NB) {
+            hipLaunchKernelGGL((append_kernel<NB, KT, I, true>), grid, dim3(256), 0, s, c, (const I *)k, ks, (const I *)v,
+                               vs, tokens, slots, cs, pairs, inter);
+            return hipGetLastError();
+        }
+    hipLaunchKernelGGL((append_kernel<NB, KT, I, false>), grid, dim3(256), 0, s, c, (const I *)k, ks, (const I *)v, vs,
+                       tokens, slots, cs, pairs, inter);
     return hipGetLastError();
 }
 
@@ -546,20 +657,30 @@ hipError_t launch_append(int kt, int half, const KvView &c, const void *k, int64
     });
 }
 
+template <int NB, int KT, typename O>
+static hipError_t read_of(const KvView &c, const int32_t *slots, int64_t n, O *k_out, O *v_out, hipStream_t s)
+{
+    for (int64_t i = 0; i < n; i += GRID_MOST * READ_ROWS) {
+        const int64_t m = n - i < GRID_MOST * READ_ROWS ? n - i : GRID_MOST * READ_ROWS;
+        const int64_t skip = i * c.kv_heads * c.head_dim;
+        hipLaunchKernelGGL((read_kernel<NB, KT, O>),
+                           dim3((unsigned)c.kv_heads, (unsigned)((m + READ_ROWS - 1) / READ_ROWS), 2), dim3(256), 0, s, c,
+                           slots + i, m, k_out ? k_out + skip : nullptr, v_out ? v_out + skip : nullptr);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
+}
+
 hipError_t launch_read(int kt, int half, const KvView &c, const int32_t *slots, int64_t n, void *k_out, void *v_out,
                        hipStream_t s)
 {
     return by_type(kt, [&](auto T) {
         return by_blocks(c.nb, [&](auto N) {
-            constexpr int KT = decltype(T)::value, NB = decltype(N)::value, ROWS = 256 / (4 * NB);
-            const dim3 grid((unsigned)((n + ROWS - 1) / ROWS), (unsigned)c.kv_heads, 2);
-            if (half)
-                hipLaunchKernelGGL((read_kernel<NB, KT, _Float16>), grid, dim3(256), 0, s, c, slots, n,
-                                   (_Float16 *)k_out, (_Float16 *)v_out);
-            else
-                hipLaunchKernelGGL((read_kernel<NB, KT, float>), grid, dim3(256), 0, s, c, slots, n, (float *)k_out,
-                                   (float *)v_out);
-            return hipGetLastError();
+            constexpr int KT = decltype(T)::value, NB = decltype(N)::value;
+            return half ? read_of<NB, KT>(c, slots, n, (_Float16 *)k_out, (_Float16 *)v_out, s)
+                        : read_of<NB, KT>(c, slots, n, (float *)k_out, (float *)v_out, s);
         });
     });
 }
@@ -570,9 +691,15 @@ hipError_t launch_move(int kt, const KvView &c, const int32_t *src, const int32_
     return by_type(kt, [&](auto T) {
         return by_blocks(c.nb, [&](auto N) {
             constexpr int KT = decltype(T)::value, NB = decltype(N)::value;
-            hipLaunchKernelGGL((move_kernel<NB, KT>), dim3((unsigned)groups, (unsigned)c.kv_heads, 2), dim3(256), 0, s,
-                               c, src, dst, n);
-            return hipGetLastError();
+            for (int64_t g = 0; g < groups; g += GRID_MOST) {
+                const int64_t m = groups - g < GRID_MOST ? groups - g : GRID_MOST;
+                hipLaunchKernelGGL((move_kernel<NB, KT>), dim3((unsigned)c.kv_heads, (unsigned)m, 2), dim3(256), 0, s, c,
+                                   src + g * n, dst + g * n, n);
+                const hipError_t e = hipGetLastError();
+                if (e != hipSuccess)
+                    return e;
+            }
+            return hipSuccess;
         });
     });
 }
