@@ -376,7 +376,7 @@ append_kernel(KvView c, const I *__restrict__ kin, int64_t k_stride, const I *__
 
 // -------------------------------------------------------------------- read --
 
-// A workgroup takes READ_ROWS rows: blockIdx.x the kv head, y which rows, z 0 for K
+// A workgroup takes ROWS rows (4, one a wave, where there are few): blockIdx.x the kv head, y which rows, z 0 for K
 // and 1 for V.  Head first: with 8 kv heads each XCD (workgroup id modulo 8) works
 // on one head, whose pages stay in its L2 (8185 tokens in any order from an F16
 // cache: 32 us numbered rows first, 21 so).
@@ -385,15 +385,13 @@ append_kernel(KvView c, const I *__restrict__ kin, int64_t k_stride, const I *__
 //      neighbouring lanes then read 16 neighbouring 16-byte runs (a token is one
 //      byte of each), two lines; eight dims to a thread as for K would touch a line
 //      per lane (8185 tokens of 8 x 128, Q4_0, in any order: 25 us both buffers).
-constexpr int READ_ROWS = 16;
-
-template <int NB, int KT, typename O>
+template <int NB, int KT, int ROWS, typename O>
 __device__ __forceinline__ void read_k(const KvView &c, int head, int dim, const int32_t *slots, int64_t i0, int64_t n,
                                        O *k_out)
 {
     using L = KvLay<NB, KT>;
     constexpr int U = 4 * NB;
-            for (int it = threadIdx.x; it < READ_ROWS * U; it += 256) {
+            for (int it = threadIdx.x; it < ROWS * U; it += 256) {
                 const int64_t i = i0 + it / U;
                 const int u = it % U, b = u >> 2;
                 if (i >= n || 8 * u >= dim)
@@ -424,12 +422,12 @@ __device__ __forceinline__ void read_k(const KvView &c, int head, int dim, const
             }
 }
 
-template <int NB, int KT, typename O>
+template <int NB, int KT, int ROWS, typename O>
 __device__ __forceinline__ void read_v(const KvView &c, int head, int dim, const int32_t *slots, int64_t i0, int64_t n,
                                        O *v_out)
 {
     using L = KvLay<NB, KT>;
-    constexpr int RPW = READ_ROWS / 4;                              // rows of a wave, loaded together
+    constexpr int RPW = ROWS / 4;                              // rows of a wave, loaded together
     constexpr int CODES = KT == KV_Q4 ? L::DP / 2 : L::DP, KS = (CODES + 63) / 64;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     uint32_t code[RPW][KS], scale[RPW][KS];
@@ -477,15 +475,15 @@ __device__ __forceinline__ void read_v(const KvView &c, int head, int dim, const
     }
 }
 
-template <int NB, int KT, typename O>
+template <int NB, int KT, int ROWS, typename O>
 __global__ void __launch_bounds__(256)
 read_kernel(KvView c, const int32_t *__restrict__ slots, int64_t n, O *__restrict__ k_out, O *__restrict__ v_out)
 {
-    const int64_t i0 = (int64_t)blockIdx.y * READ_ROWS;
+    const int64_t i0 = (int64_t)blockIdx.y * ROWS;
     if (blockIdx.z == 0 && k_out != nullptr)
-        read_k<NB, KT>(c, blockIdx.x, c.head_dim, slots, i0, n, k_out);
+        read_k<NB, KT, ROWS>(c, blockIdx.x, c.head_dim, slots, i0, n, k_out);
     if (blockIdx.z != 0 && v_out != nullptr)
-        read_v<NB, KT>(c, blockIdx.x, c.head_dim, slots, i0, n, v_out);
+        read_v<NB, KT, ROWS>(c, blockIdx.x, c.head_dim, slots, i0, n, v_out);
 }
 
 // -------------------------------------------------------------------- move --
@@ -657,20 +655,28 @@ hipError_t launch_append(int kt, int half, const KvView &c, const void *k, int64
     });
 }
 
-template <int NB, int KT, typename O>
-static hipError_t read_of(const KvView &c, const int32_t *slots, int64_t n, O *k_out, O *v_out, hipStream_t s)
+template <int NB, int KT, int ROWS, typename O>
+static hipError_t read_rows(const KvView &c, const int32_t *slots, int64_t n, O *k_out, O *v_out, hipStream_t s)
 {
-    for (int64_t i = 0; i < n; i += GRID_MOST * READ_ROWS) {
-        const int64_t m = n - i < GRID_MOST * READ_ROWS ? n - i : GRID_MOST * READ_ROWS;
-        const int64_t skip = i * c.kv_heads * c.head_dim;
-        hipLaunchKernelGGL((read_kernel<NB, KT, O>),
-                           dim3((unsigned)c.kv_heads, (unsigned)((m + READ_ROWS - 1) / READ_ROWS), 2), dim3(256), 0, s, c,
-                           slots + i, m, k_out ? k_out + skip : nullptr, v_out ? v_out + skip : nullptr);
+    for (int64_t i = 0; i < n; i += GRID_MOST * ROWS) {
+        const int64_t m = n - i < GRID_MOST * ROWS ? n - i : GRID_MOST * ROWS, skip = i * c.kv_heads * c.head_dim;
+        hipLaunchKernelGGL((read_kernel<NB, KT, ROWS, O>), dim3((unsigned)c.kv_heads, (unsigned)((m + ROWS - 1) / ROWS), 2),
+                           dim3(256), 0, s, c, slots + i, m, k_out ? k_out + skip : nullptr,
+                           v_out ? v_out + skip : nullptr);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess)
             return e;
     }
     return hipSuccess;
+}
+
+// A wave of four rows pays from a few hundred rows on (5 rows of Q8_0: 4.1 us, one
+// row a wave 2.7; 8185 rows 15 against 23).
+template <int NB, int KT, typename O>
+static hipError_t read_of(const KvView &c, const int32_t *slots, int64_t n, O *k_out, O *v_out, hipStream_t s)
+{
+    return n <= 256 ? read_rows<NB, KT, 4>(c, slots, n, k_out, v_out, s)
+                    : read_rows<NB, KT, 16>(c, slots, n, k_out, v_out, s);
 }
 
 hipError_t launch_read(int kt, int half, const KvView &c, const int32_t *slots, int64_t n, void *k_out, void *v_out,
