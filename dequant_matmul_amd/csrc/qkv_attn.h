@@ -287,6 +287,15 @@ __device__ __forceinline__ uint32_t keep_pair(int left, int i, int j)
     return (i < left ? 0xffffu : 0u) | (j < left ? 0xffff0000u : 0u);
 }
 
+// Of two fp16, those that are finite; else 0.  A new token that was not appended
+// (a padded batch) leaves any bits within the sequence; a row that does not see it
+// gives it weight 0, which only a finite number turns into 0.
+__device__ __forceinline__ uint32_t finite_pair(uint32_t x)
+{
+    const uint32_t bad = ((x & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
+    return x & ~((bad >> 15) * 0xffffu);
+}
+
 // One row of q (r, a row of kv head `head`'s; nothing if r >= rows) as operand B:
 // this lane's eighth of every block, in PARTS fp16 parts.  Returns what the
 // products have to be multiplied by to be scores in base 2.  Two parts: the row
@@ -382,6 +391,28 @@ __device__ __forceinline__ float lane_max(const f32x4 (&sc)[4])
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             mx = fmaxf(mx, sc[c][i]);
+    return mx;
+}
+
+// What lane_max is to rows that do not see every token: the largest score plus the
+// exponent of that token's own V scales (vs: fp16 in LDS, the lane's 16 tokens of
+// block 0; blocks are 32 dwords apart), so that the scale of a token that a row
+// does not see has no part in the row's reference.
+template <int NB>
+__device__ __forceinline__ float masked_top(const f32x4 (&sc)[4], float rs, const uint32_t *vs)
+{
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    float mx = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        u16x2 big = {0x0400, 0x0400};       // the smallest normal number
+#pragma unroll
+        for (int bl = 0; bl < NB; ++bl)
+            big = __builtin_elementwise_max(big, __builtin_bit_cast(u16x2, vs[32 * bl + i] & 0x7fff7fffu));
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            mx = fmaxf(mx, fmaf(sc[i >> 1][2 * (i & 1) + j], rs, (float)((int)(big[j] >> 10) - 14)));
+    }
     return mx;
 }
 
@@ -563,6 +594,7 @@ attn_kernel(AttnArgs a)
     }
     for (; tile < t_end; tile += 4) {
         const int64_t k0 = (int64_t)tile * KV_TILE, seen_to = hidden ? k0 : nseen;
+        const bool tail = k0 + KV_TILE > (s.ctx < seen_to ? s.ctx : seen_to);   // some row may not see all of it
         float ev = 0.f;
         if constexpr (SCALED) {
             const int left = (int)(seen_to - k0 < KV_TILE ? seen_to - k0 : KV_TILE);
@@ -573,12 +605,12 @@ attn_kernel(AttnArgs a)
                 if (16 * NB % 64 == 0 || j < 16 * NB) {
                     if (j >= 8 * NB) {
                         // tokens 8 (j % 8) .. of block j / 8; what lies behind the last
-                        // token may be any bits
-                        if (left < KV_TILE) {
+                        // token, and at new ones never appended, may be any bits
+                        if (tail) {
                             const int room = left - 8 * (int)opaque(j & 7);
 #pragma unroll
                             for (int w = 0; w < 4; ++w)
-                                sd[i][w] &= keep_pair(room, 2 * w, 2 * w + 1);
+                                sd[i][w] = finite_pair(sd[i][w] & keep_pair(room, 2 * w, 2 * w + 1));
                         }
 #pragma unroll
                         for (int w = 0; w < 4; ++w)
@@ -651,9 +683,8 @@ attn_kernel(AttnArgs a)
         }
 
         __builtin_amdgcn_sched_barrier(0);
-        // ---- what a row does not see; an F16 cache may hold any bits behind the
-        // last token
-        if (k0 + KV_TILE > s.ctx || hidden) {
+        // ---- what a row does not see; an F16 cache may hold any bits there
+        if (tail) {
             // (opaque: kept from becoming induction variables, a register pair each)
             const uint32_t bits = seen16(a, s, tok, k0 + 16 * (int)opaque(h), seen_to);
 #pragma unroll
@@ -663,16 +694,20 @@ attn_kernel(AttnArgs a)
                     sc[c][i] = (bits >> (4 * c + i)) & 1u ? sc[c][i] : -INFINITY;
         }
         if constexpr (!SCALED) {
-            if (k0 + KV_TILE > seen_to) {
+            if (tail) {
                 const int left = (int)(seen_to - k0) - 16 * (int)opaque(h);
 #pragma unroll
                 for (int w = 0; w < 8; ++w)
 #pragma unroll
                     for (int t = 0; t < VN; ++t)
-                        vr[t][w] &= keep_pair(left, 2 * w, 2 * w + 1);
+                        vr[t][w] = finite_pair(vr[t][w] & keep_pair(left, 2 * w, 2 * w + 1));
             }
         }
-        const float top = fmaf(lane_max(sc), rs, ev);
+        float top;
+        if (SCALED && tail)
+            top = masked_top<NB>(sc, rs, &scales[wave][32 * NB + 8 * h]);
+        else
+            top = fmaf(lane_max(sc), rs, ev);
         if (__any(top > m + P_SLACK))
             raise<NB>(top, m, shift, l, o);
         soften(sc, rs, shift);

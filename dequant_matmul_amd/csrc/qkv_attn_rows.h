@@ -119,11 +119,12 @@ attn_rows_kernel(AttnArgs a)
         return true;
     };
 
-    // what lies behind the last token may be any bits: V (or its scale) becomes 0
+    // what lies behind the last token, and at new ones never appended, may be any
+    // bits: V (or its scale) becomes 0, or at least finite
     auto store_tile = [&](int buf, int tile) {
         const int64_t rest = nseen - (int64_t)tile * KV_TILE;
         const int left = (int)(rest < KV_TILE ? rest : KV_TILE) - 16 * h;
-        const bool tail = rest < KV_TILE;
+        const bool tail = rest < KV_TILE || (int64_t)(tile + 1) * KV_TILE > s.ctx;
 #pragma unroll
         for (int i = 0; i < KI; ++i) {
             const int j = wave + W * i;
@@ -164,7 +165,7 @@ attn_rows_kernel(AttnArgs a)
                         const int first = 8 * (KT == KV_F16 ? j & 1 : st);
 #pragma unroll
                         for (int p = 0; p < 4; ++p)
-                            y[p] &= keep_pair(left, first + C::v_ord(2 * p), first + C::v_ord(2 * p + 1));
+                            y[p] = finite_pair(y[p] & keep_pair(left, first + C::v_ord(2 * p), first + C::v_ord(2 * p + 1)));
                         x = __builtin_bit_cast(h16x8, y);
                     }
                     // [dim tile][step]
@@ -184,7 +185,7 @@ attn_rows_kernel(AttnArgs a)
                 const int j = t - 8 * NB, room = (int)(rest < KV_TILE ? rest : KV_TILE) - 8 * (j & 7);
 #pragma unroll
                 for (int w = 0; w < 4; ++w)
-                    big[w] = sd[w] & keep_pair(room, 2 * w, 2 * w + 1);
+                    big[w] = tail ? finite_pair(sd[w] & keep_pair(room, 2 * w, 2 * w + 1)) : sd[w];
                 *(u32x4 *)&vscale[buf][4 * j] = (u32x4){big[0], big[1], big[2], big[3]};
             }
             if (wave == 8 * NB / 64) {
@@ -250,7 +251,8 @@ attn_rows_kernel(AttnArgs a)
                 }
             __builtin_amdgcn_sched_barrier(0);
         }
-        if (k0 + KV_TILE > s.ctx) {
+        const bool tail = k0 + KV_TILE > (s.ctx < nseen ? s.ctx : nseen);
+        if (tail) {
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
                 const uint32_t bits = seen16(a, s, tok[rt], k0 + 16 * h, nseen);
@@ -278,7 +280,10 @@ attn_rows_kernel(AttnArgs a)
         bool more = false;
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-            top[rt] = fmaf(lane_max(sc[rt]), rs[rt], ev);
+            if (SCALED && tail)
+                top[rt] = masked_top<NB>(sc[rt], rs[rt], &vscale[buf][8 * h]);
+            else
+                top[rt] = fmaf(lane_max(sc[rt]), rs[rt], ev);
             more |= top[rt] > m[rt] + P_SLACK;
         }
         if (__any(more)) {

@@ -182,6 +182,8 @@ QMM_API int qkv_move(const qkv_cache *cache, const int32_t *src, const int32_t *
  * out[row][h] = sum_j softmax_j(scale q[row][h] . k_j) v_j over what the row
  * sees, heads h sharing kv head h / (heads / kv_heads); a row that sees
  * nothing gives 0.  Rows of q that belong to no sequence are left as they are.
+ * A new token whose rows were not appended (padding) has no effect on rows that
+ * do not see it, whatever bits its slot holds; those that do see it are undefined.
  *
  * max_q and max_ctx bound the new tokens of any sequence and the tokens
  * (committed and new) of any sequence; they size the launch and the workspace,

@@ -223,6 +223,40 @@ def test_rows_of_no_sequence_are_left(dt):
 
 
 @pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("pad", [6, 40])
+@pytest.mark.parametrize("bits", [0xffff, 0x7c00, 0x7bff])
+def test_padded_tokens_never_appended(kind, dt, tree, pad, bits):
+    """Equal shares of which the last rows are padding whose K and V were never
+    written: NaN, infinity or the largest number lie there, and the rows before
+    them (which do not see them) are what they are without."""
+    c = Case(kind, [5, 64, 100], [4, 1, 5], 2, 4, 128, page=256, seed=pad, tree=tree, vscale=2.0 ** -6)
+    clean = q.KVCache(R.TYPES[kind], 2, 128, c.pages, page_size=256)
+    fill = up(np.full(c.cache.k.numel() // 2, bits, np.uint16).view(np.int16)).view(torch.uint8)
+    clean.k.copy_(fill.view_as(clean.k))
+    clean.v.copy_(fill.view_as(clean.v))
+    for b, (ctx, t) in enumerate(zip(c.ctx, c.tq)):
+        p = np.arange(ctx + t)
+        slots = up((c.table[b, p // 256] * 256 + p % 256).astype(np.int32))
+        rows = q.kv_read(c.cache, slots)
+        q.kv_append(clean, *rows, slots)
+        # the values of a quantized cache need not be its fixed points
+        c.k[b], c.v[b] = (x.cpu().numpy().astype(np.float64) for x in q.kv_read(clean, slots))
+    c.cache = clean
+    at = np.concatenate([b * pad + np.arange(t) for b, t in enumerate(c.tq)])
+    rows = np.zeros((3 * pad,) + c.q.shape[1:], np.float32)
+    rows[at] = c.q
+    mask = None
+    if tree:
+        words = np.zeros((3 * pad, 1), np.int64)
+        words[at] = c.mask
+        mask = up(words)
+    got = q.attention(clean, up(rows).to(dt), up(c.table), up(np.array(c.ctx, np.int32)), mask=mask)
+    c.check(got[up(at)], dt)
+
+
+@pytest.mark.parametrize("dt", DTS)
 def test_bad_indices_stay_inside(dt):
     """Page ids outside the cache hide their tokens; lengths past the table end
     there; negative ones are empty."""
