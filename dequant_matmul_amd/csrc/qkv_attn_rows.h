@@ -18,6 +18,8 @@
 
 namespace qmm {
 
+constexpr int MODE_FP16_OVFL = 1 | 23 << 6;     // one bit, 23, of hardware register 1
+
 template <int NB, int KT, int RT, int W, int PARTS, typename IO>
 __global__ void __launch_bounds__(64 * W, NB > 4 && W == 4 ? 1 : 2)
 attn_rows_kernel(AttnArgs a)
@@ -53,6 +55,12 @@ attn_rows_kernel(AttnArgs a)
     // tiles that this wave's rows see something of
     const int my_last = ((rows < r0 + 16 * RT ? rows : r0 + 16 * RT) - 1) / a.group;
     const int my_end = r0 >= rows ? 0 : (int)((seen(a, s, my_last) + KV_TILE - 1) / KV_TILE);
+
+    // 127 times the largest scale of a Q8_0 block (516) is past the fp16 range: a
+    // decoded value saturates at 65504 (MODE.FP16_OVFL) until the output is written
+    constexpr bool SATURATE = FOLDED && KT == KV_Q8;
+    if constexpr (SATURATE)
+        __builtin_amdgcn_s_setreg(MODE_FP16_OVFL, 1);
 
     h16x8 qf[RT][PARTS][NB];
     float rs[RT], m[RT], shift[RT], l[RT];
@@ -346,6 +354,9 @@ attn_rows_kernel(AttnArgs a)
         live = next;
         __syncthreads();
     }
+
+    if constexpr (SATURATE)
+        __builtin_amdgcn_s_setreg(MODE_FP16_OVFL, 0);
 
     // ---- this wave's rows
     const int64_t wrows = (int64_t)a.tokens * a.heads;

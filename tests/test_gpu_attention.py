@@ -257,6 +257,32 @@ def test_padded_tokens_never_appended(kind, dt, tree, pad, bits):
 
 
 @pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("tq", [1, 50])
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_the_largest_stored_values(kind, dt, tq, which):
+    """A stored 65504 (an infinity, clamped) in one token: it stays finite, also
+    decoded (127 times the fp16 scale of a Q8_0 block is 65532), and rows that do
+    not see its token do not feel it."""
+    c = Case(kind, [70, 40], [tq, tq], 2, 4, 64, seed=20)
+    slots, k, v = [], [], []
+    for b in range(2):
+        p = 30 + 45 * (tq > 1) + b            # the second sequence's is a new token if there are many
+        k1, v1 = R.stored(c.k[b][p:p + 1], kind).copy(), R.stored(c.v[b][p:p + 1], kind).copy()
+        (k1 if which == "k" else v1)[0, :, 3] = np.inf
+        (k1 if which == "k" else v1)[0, 1, 40] = -np.inf
+        k.append(k1)
+        v.append(v1)
+        slots.append(int(c.table[b, p // 64] * 64 + p % 64))
+        at = torch.tensor([slots[-1]], dtype=torch.int32, device=DEV)
+        q.kv_append(c.cache, up(k1.astype(np.float32)), up(v1.astype(np.float32)), at)
+        for mine, got in zip((c.k, c.v), q.kv_read(c.cache, at)):
+            mine[b][p] = got[0].cpu().numpy()
+            assert np.isfinite(mine[b][p]).all() and (which == "kv"[mine is c.v]) == (np.abs(mine[b][p]).max() > 65000)
+    c.check(c.run(dt), dt)
+
+
+@pytest.mark.parametrize("dt", DTS)
 def test_bad_indices_stay_inside(dt):
     """Page ids outside the cache hide their tokens; lengths past the table end
     there; negative ones are empty."""
