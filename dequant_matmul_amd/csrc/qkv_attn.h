@@ -199,6 +199,14 @@ __device__ __forceinline__ int64_t seen(const AttnArgs &a, const Seq &s, int las
     return n < cap ? (n < most ? n : most) : (cap < most ? cap : most);
 }
 
+// Tiles, from the first on, of which rows from new token `first` on all see every
+// token: they need no mask.
+__device__ __forceinline__ int clear_tiles(const AttnArgs &a, const Seq &s, int first, int64_t nseen)
+{
+    const int64_t all = a.mask ? s.ctx : s.ctx + first + 1;
+    return (int)((all < nseen ? all : nseen) / KV_TILE);
+}
+
 // The page ids of a wave's tiles, 64 at a time, one a lane: a tile's page is a
 // v_readlane instead of a load in front of its loads.
 struct PageIds {
@@ -287,13 +295,13 @@ __device__ __forceinline__ uint32_t keep_pair(int left, int i, int j)
     return (i < left ? 0xffffu : 0u) | (j < left ? 0xffff0000u : 0u);
 }
 
-// Of two fp16, those that are finite; else 0.  A new token that was not appended
-// (a padded batch) leaves any bits within the sequence; a row that does not see it
-// gives it weight 0, which only a finite number turns into 0.
+// Two fp16 made finite (within the range; NaN to one of its ends).  A new token that
+// was not appended (a padded batch) leaves any bits within the sequence; a row that
+// does not see it gives it weight 0, which only a finite number turns into 0.
 __device__ __forceinline__ uint32_t finite_pair(uint32_t x)
 {
-    const uint32_t bad = ((x & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
-    return x & ~((bad >> 15) * 0xffffu);
+    const h16x2 most = {(_Float16)65504.f, (_Float16)65504.f};
+    return as_u(__builtin_elementwise_min(__builtin_elementwise_max(as_h2(x), -most), most));
 }
 
 // One row of q (r, a row of kv head `head`'s; nothing if r >= rows) as operand B:
@@ -513,6 +521,7 @@ attn_kernel(AttnArgs a)
     const int last = ((rows < r0 + 16 ? rows : r0 + 16) - 1) / a.group;
     const int64_t nseen = seen(a, s, last);
     const int ntiles = (int)((nseen + KV_TILE - 1) / KV_TILE);
+    const int clear = clear_tiles(a, s, r0 / a.group, nseen);
     const int per = (ntiles + a.splits - 1) / a.splits;
     const int t_begin = split * per;
     const int t_end = a.pages == 0 ? 0 : t_begin + per < ntiles ? t_begin + per : ntiles;
@@ -594,7 +603,7 @@ attn_kernel(AttnArgs a)
     }
     for (; tile < t_end; tile += 4) {
         const int64_t k0 = (int64_t)tile * KV_TILE, seen_to = hidden ? k0 : nseen;
-        const bool tail = k0 + KV_TILE > (s.ctx < seen_to ? s.ctx : seen_to);   // some row may not see all of it
+        const bool tail = hidden || tile >= clear;       // some row does not see all of it
         float ev = 0.f;
         if constexpr (SCALED) {
             const int left = (int)(seen_to - k0 < KV_TILE ? seen_to - k0 : KV_TILE);

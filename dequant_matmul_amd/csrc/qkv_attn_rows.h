@@ -52,6 +52,7 @@ attn_rows_kernel(AttnArgs a)
     const int ntiles = (int)((nseen + KV_TILE - 1) / KV_TILE);
     const int per = (ntiles + a.splits - 1) / a.splits;
     const int t_begin = split * per, t_end = t_begin + per < ntiles ? t_begin + per : ntiles;
+    const int clear = clear_tiles(a, s, g0 / a.group, nseen), my_clear = clear_tiles(a, s, r0 / a.group, nseen);
     // tiles that this wave's rows see something of
     const int my_last = ((rows < r0 + 16 * RT ? rows : r0 + 16 * RT) - 1) / a.group;
     const int my_end = r0 >= rows ? 0 : (int)((seen(a, s, my_last) + KV_TILE - 1) / KV_TILE);
@@ -132,7 +133,7 @@ attn_rows_kernel(AttnArgs a)
     auto store_tile = [&](int buf, int tile) {
         const int64_t rest = nseen - (int64_t)tile * KV_TILE;
         const int left = (int)(rest < KV_TILE ? rest : KV_TILE) - 16 * h;
-        const bool tail = rest < KV_TILE || (int64_t)(tile + 1) * KV_TILE > s.ctx;
+        const bool tail = tile >= clear;
 #pragma unroll
         for (int i = 0; i < KI; ++i) {
             const int j = wave + W * i;
@@ -259,7 +260,7 @@ attn_rows_kernel(AttnArgs a)
                 }
             __builtin_amdgcn_sched_barrier(0);
         }
-        const bool tail = k0 + KV_TILE > (s.ctx < nseen ? s.ctx : nseen);
+        const bool tail = tile >= my_clear;
         if (tail) {
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
