@@ -74,6 +74,11 @@ __device__ __forceinline__ uint32_t rest_h2(float a, float b, uint32_t h)
 {
     return as_u((h16x2){(_Float16)(a - (float)as_h2(h)[0]), (_Float16)(b - (float)as_h2(h)[1])});
 }
+__device__ __forceinline__ float opaque_f(float v)
+{
+    asm volatile("" : "+v"(v));
+    return v;
+}
 // half i (compile time) of an array of dwords, as fp32
 __device__ __forceinline__ float half_of(const uint32_t *w, int i) { return (float)as_h2(w[i >> 1])[i & 1]; }
 
@@ -673,6 +678,11 @@ attn_kernel(AttnArgs a)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         sc[c][i] = fmaf(acc[bl][i], half_of(ks, i * NB + bl), sc[c][i]);
+                // (opaque: else the compiler puts all of these behind the next loads,
+                // where the products of the whole tile are live: 80 registers)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sc[c][i] = opaque_f(sc[c][i]);
             }
             if constexpr (SCALED && NB >= 4)
                 __builtin_amdgcn_sched_barrier(0);
