@@ -230,6 +230,9 @@ struct PageIds {
         first = col;
         const int i = col + (int)(threadIdx.x & 63);
         held = i < columns ? ids[i] : -1;
+        // (opaque: waits here, not at the readlane, which would wait for all loads
+        // on their way, also where nothing was fetched)
+        held = (int)opaque((uint32_t)held);
     }
     // tiles may only go up; every lane of the wave calls
     __device__ __forceinline__ int page(int tile)
@@ -535,7 +538,7 @@ attn_kernel(AttnArgs a)
     const float rs = load_row<NB, KT, PARTS, IO>(a, s, head, r0 + n, rows, h, qf);
     // the low parts wait in LDS, where the wave's output goes at the end: with them
     // the registers of a tile do not fit two waves a SIMD
-    constexpr bool QLDS = PARTS == 2 && SCALED && NB >= 4;
+    constexpr bool QLDS = PARTS == 2 && (SCALED ? NB >= 4 : NB > 4);
     h16x8(*qlow)[64] = (h16x8(*)[64])joined[wave];
     if constexpr (QLDS) {
 #pragma unroll
@@ -551,8 +554,8 @@ attn_kernel(AttnArgs a)
     for (int t = 0; t < 2 * NB; ++t)
         o[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
 
-    // ---- loads.  K of the next tile is loaded as soon as the scores are done, V
-    // when the output is: either runs under the other half of a tile.  The scales
+    // ---- loads.  A piece of the next tile is loaded as soon as the one in its
+    // registers has gone into the products: it has most of a tile to arrive.  The scales
     // of a tile (one 16-byte piece a lane) pass through LDS, from where each lane
     // takes those of its 16 tokens: loaded by every lane they would be two thirds
     // of all loads.
@@ -562,15 +565,19 @@ attn_kernel(AttnArgs a)
         return ((((int64_t)page * a.kv_heads + head) << pages.shift) + (tile & ((1 << pages.shift) - 1))) *
                (int64_t)L::TILE_BYTES;
     };
-    auto load_k = [&](int64_t at) {
-        const uint8_t *kp = a.k + at, *vp = a.v + at;
-        const uint32_t lane = opaque(threadIdx.x & 63);     // an offset to a uniform base, not an address of its own
+    // No branch around them: the wait for a load has to hold on either side of a
+    // branch behind it, and so would wait for what the taken side has loaded since.
+    // Behind a wave's last tile every lane loads what lane 0 does, from the same tile.
+    auto load_k = [&](int64_t at, uint32_t lane, int c) {       // tokens 4 c .. of every 16
+        lane = opaque(lane);        // an offset to a uniform base, not an address of its own
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int g = 0; g < NB / L::G; ++g)
-                load_dw<CDW>(kp + ((c * (NB / L::G) + g) * 64 + lane) * (L::G * L::UNIT), &kr[c][g * CDW]);
+        for (int g = 0; g < NB / L::G; ++g)
+            load_dw<CDW>(a.k + at + ((c * (NB / L::G) + g) * 64 + lane) * (L::G * L::UNIT), &kr[c][g * CDW]);
+    };
+    auto load_scales = [&](int64_t at, uint32_t lane) {
         if constexpr (SCALED) {
+            const uint8_t *kp = a.k + at, *vp = a.v + at;
+            lane = opaque(lane);
 #pragma unroll
             for (int i = 0; i < SP; ++i) {
                 const int j = 64 * i + (int)lane;       // K scales, then V scales
@@ -579,16 +586,16 @@ attn_kernel(AttnArgs a)
             }
         }
     };
-    auto load_v = [&](int64_t at) {
-        const uint8_t *vp = a.v + at;
-        const uint32_t lane = opaque(threadIdx.x & 63);
+    auto load_v = [&](int64_t at, uint32_t lane, int bl) {      // dims of block bl
+        lane = opaque(lane);
 #pragma unroll
-        for (int t = 0; t < VN; ++t) {
+        for (int u = 0; u < VN / NB; ++u) {
+            const int t = VN / NB * bl + u;
             if constexpr (KT == KV_F16) {
-                load_dw<4>(vp + ((t * 2) * 64 + lane) * 16, &vr[t][0]);
-                load_dw<4>(vp + ((t * 2 + 1) * 64 + lane) * 16, &vr[t][4]);
+                load_dw<4>(a.v + at + ((t * 2) * 64 + lane) * 16, &vr[t][0]);
+                load_dw<4>(a.v + at + ((t * 2 + 1) * 64 + lane) * 16, &vr[t][4]);
             } else {
-                load_dw<4>(vp + (t * 64 + lane) * 16, &vr[t][0]);
+                load_dw<4>(a.v + at + (t * 64 + lane) * 16, &vr[t][0]);
             }
         }
     };
@@ -603,8 +610,13 @@ attn_kernel(AttnArgs a)
         const int page = pages.page(tile);
         hidden = page < 0 || page >= a.pages;
         at = tile_base(hidden ? 0 : page, tile);
-        load_k(at);
-        load_v(at);
+        load_scales(at, lane);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            load_k(at, lane, c);
+#pragma unroll
+        for (int bl = 0; bl < NB; ++bl)
+            load_v(at, lane, bl);
     }
     for (; tile < t_end; tile += 4) {
         const int64_t k0 = (int64_t)tile * KV_TILE, seen_to = hidden ? k0 : nseen;
@@ -637,8 +649,42 @@ attn_kernel(AttnArgs a)
             ev = scale_exponent(big);
         }
 
+        // ---- the next tile.  (Scheduling fences around the phases: moved into one
+        // another they need twice the registers.)
+        const int next = tile + 4;
+        const bool more = next < t_end;
+        bool next_hidden = true;
+        if (more) {
+            const int page = pages.page(next);
+            next_hidden = page < 0 || page >= a.pages;
+            at = tile_base(next_hidden ? 0 : page, next);
+        }
+        const uint32_t next_lane = more ? lane : 0;
+        load_scales(at, next_lane);
+        __builtin_amdgcn_sched_barrier(0);
+
         // ---- scores
-        f32x4 sc[4];
+        f32x4 sc[4], acc[SCALED ? 2 : 1][SCALED ? NB : 1];
+        // those of tokens 4 c .. of every 16 from their blocks' products.  (opaque: else
+        // the compiler puts all of these behind the tile's loads, where the products of
+        // the whole tile are live: 80 registers)
+        auto scale_scores = [&](int c) {
+            uint32_t ks[2 * NB];
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                const u32x2 y = *(const u32x2 *)&scales[wave][8 * NB * h + 2 * NB * c + 2 * i];
+                ks[2 * i] = y[0];
+                ks[2 * i + 1] = y[1];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float y = 0.f;
+#pragma unroll
+                for (int bl = 0; bl < NB; ++bl)
+                    y = fmaf(acc[c & 1][bl][i], half_of(ks, i * NB + bl), y);
+                sc[c][i] = opaque_f(y);
+            }
+        };
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             sc[c] = (f32x4){0.f, 0.f, 0.f, 0.f};
@@ -649,17 +695,7 @@ attn_kernel(AttnArgs a)
                 for (int w = 0; w < KDW; ++w)
                     kr[c][w] = opaque(kr[c][w]);
             }
-            uint32_t ks[SCALED ? 2 * NB : 1];           // of the lane's tokens 4 c .. 4 c + 3
-            if constexpr (SCALED) {
-#pragma unroll
-                for (int i = 0; i < NB; ++i) {
-                    const u32x2 y = *(const u32x2 *)&scales[wave][8 * NB * h + 2 * NB * c + 2 * i];
-                    ks[2 * i] = y[0];
-                    ks[2 * i + 1] = y[1];
-                }
-            }
             // products that do not depend on one another in a row
-            f32x4 acc[SCALED ? NB : 1];
 #pragma unroll
             for (int part = 0; part < PARTS; ++part)
 #pragma unroll
@@ -668,38 +704,20 @@ attn_kernel(AttnArgs a)
                     const h16x8 y = QLDS && part == 1 ? qlow[bl][lane] : qf[part][bl];
                     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
                     if constexpr (SCALED)
-                        acc[bl] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, y, part ? acc[bl] : zero, 0, 0, 0);
+                        acc[c & 1][bl] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, y, part ? acc[c & 1][bl] : zero, 0, 0, 0);
                     else
                         sc[c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, y, sc[c], 0, 0, 0);
                 }
+            load_k(at, next_lane, c);
+            // (the ones before: the matrix cores have finished them)
             if constexpr (SCALED) {
-#pragma unroll
-                for (int bl = 0; bl < NB; ++bl)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        sc[c][i] = fmaf(acc[bl][i], half_of(ks, i * NB + bl), sc[c][i]);
-                // (opaque: else the compiler puts all of these behind the next loads,
-                // where the products of the whole tile are live: 80 registers)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    sc[c][i] = opaque_f(sc[c][i]);
+                if (c > 0)
+                    scale_scores(c - 1);
             }
-            if constexpr (SCALED && NB >= 4)
-                __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_sched_barrier(0);
         }
-
-        // ---- the next tile's K.  (Scheduling fences around the phases: moved into
-        // one another they need twice the registers.)
-        __builtin_amdgcn_sched_barrier(0);
-        const int next = tile + 4;
-        int64_t next_at = 0;
-        bool next_hidden = true;
-        if (next < t_end) {
-            const int page = pages.page(next);
-            next_hidden = page < 0 || page >= a.pages;
-            next_at = tile_base(next_hidden ? 0 : page, next);
-            load_k(next_at);
-        }
+        if constexpr (SCALED)
+            scale_scores(3);
 
         __builtin_amdgcn_sched_barrier(0);
         // ---- what a row does not see; an F16 cache may hold any bits there
@@ -770,12 +788,9 @@ attn_kernel(AttnArgs a)
                     if constexpr (PARTS == 2)
                         o[2 * bl + u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, lo[st], o[2 * bl + u], 0, 0, 0);
                 }
-            if constexpr (SCALED && NB >= 4)
-                __builtin_amdgcn_sched_barrier(0);
+            load_v(at, next_lane, bl);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        __builtin_amdgcn_sched_barrier(0);
-        if (next < t_end)
-            load_v(next_at);
         hidden = next_hidden;
     }
 
