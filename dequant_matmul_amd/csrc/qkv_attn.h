@@ -90,16 +90,19 @@ __device__ __forceinline__ uint32_t q8_pair(uint32_t x, int j)
     return as_u(as_h2(__builtin_amdgcn_perm(0x64646464u, x, j ? 0x04030402u : 0x04010400u)) - off);
 }
 // Nibbles at bits 0 and 16 (HI: 4 and 20) of x, code + 8: the high nibble reads
-// as 1024 + 16 n.
+// as 1024 + 16 n.  1024 is held in a vector register: v_and_or_b32 takes only one of
+// its two constants from elsewhere.
 template <bool HI>
 __device__ __forceinline__ uint32_t q4_pair(uint32_t x)
 {
+    uint32_t magic = 0x64006400u;
+    asm("" : "+v"(magic));
     if constexpr (HI) {
         const h16x2 f = {(_Float16)0.0625f, (_Float16)0.0625f}, off = {(_Float16)-72.f, (_Float16)-72.f};
-        return as_u(as_h2((x & 0x00f000f0u) | 0x64006400u) * f + off);
+        return as_u(as_h2((x & 0x00f000f0u) | magic) * f + off);
     } else {
         const h16x2 off = {(_Float16)1032.f, (_Float16)1032.f};
-        return as_u(as_h2((x & 0x000f000fu) | 0x64006400u) - off);
+        return as_u(as_h2((x & 0x000f000fu) | magic) - off);
     }
 }
 
@@ -484,14 +487,21 @@ __device__ __forceinline__ void weights(const f32x4 (&sc)[4], const uint32_t *vs
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
         const int i = 8 * st + C::v_ord(2 * p), j = 8 * st + C::v_ord(2 * p + 1);
-        float y = sc[i >> 2][i & 3], z = sc[j >> 2][j & 3];
+        const float y = sc[i >> 2][i & 3], z = sc[j >> 2][j & 3];
         if constexpr (SCALED) {
-            y *= half_of(vs, i);
-            z *= half_of(vs, j);
+            // one instruction each: the product, less the first part, rounded to fp16
+            const float u = half_of(vs, i), v = half_of(vs, j);
+            const h16x2 a = {(_Float16)fmaf(y, u, 0.f), (_Float16)fmaf(z, v, 0.f)};
+            w[p] = opaque(as_u(a));
+            if constexpr (PARTS == 2) {
+                const h16x2 b = {(_Float16)fmaf(y, u, -(float)as_h2(w[p])[0]), (_Float16)fmaf(z, v, -(float)as_h2(w[p])[1])};
+                r[p] = as_u(b);
+            }
+        } else {
+            w[p] = to_h2(y, z);
+            if constexpr (PARTS == 2)
+                r[p] = rest_h2(y, z, w[p]);
         }
-        w[p] = to_h2(y, z);
-        if constexpr (PARTS == 2)
-            r[p] = rest_h2(y, z, w[p]);
     }
     hi = as_h8(w[0], w[1], w[2], w[3]);
     if constexpr (PARTS == 2)
@@ -500,8 +510,11 @@ __device__ __forceinline__ void weights(const f32x4 (&sc)[4], const uint32_t *vs
 
 // ---------------------------------------------------------------- the kernel --
 
+// Waves of a workgroup: two a SIMD, or the one that fits (256 dims).
+constexpr int attn_waves(int nb) { return nb > 4 ? 4 : 8; }
+
 template <int NB, int KT, int PARTS, typename IO>
-__global__ void __launch_bounds__(256, NB > 4 ? 1 : 2)
+__global__ void __launch_bounds__(64 * attn_waves(NB), NB > 4 ? 1 : 2)
 attn_kernel(AttnArgs a)
 {
     using L = KvLay<NB, KT>;
@@ -512,10 +525,11 @@ attn_kernel(AttnArgs a)
     constexpr int VN = KT == KV_Q4 ? NB : 2 * NB;      // V pieces
     constexpr bool SCALED = KT != KV_F16;
 
+    constexpr int W = attn_waves(NB);
     constexpr int SP = (16 * NB + 63) / 64;            // 16-byte pieces of a tile's scales per lane
-    __shared__ __align__(16) f32x4 joined[4][2 * NB][64];
-    __shared__ float join_m[4][16], join_l[4][16];
-    __shared__ __align__(16) uint32_t scales[4][SCALED ? 64 * NB : 4];
+    __shared__ __align__(16) f32x4 joined[W][2 * NB][64];
+    __shared__ float join_m[W][16], join_l[W][16];
+    __shared__ __align__(16) uint32_t scales[W][SCALED ? 64 * NB : 4];
 
     const int lane = threadIdx.x & 63, n = lane & 15, h = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);     // the same in every lane, for the compiler too
@@ -618,7 +632,7 @@ attn_kernel(AttnArgs a)
         for (int bl = 0; bl < NB; ++bl)
             load_v(at, lane, bl);
     }
-    for (; tile < t_end; tile += 4) {
+    for (; tile < t_end; tile += W) {
         const int64_t k0 = (int64_t)tile * KV_TILE, seen_to = hidden ? k0 : nseen;
         const bool tail = hidden || tile >= clear;       // some row does not see all of it
         float ev = 0.f;
@@ -651,7 +665,7 @@ attn_kernel(AttnArgs a)
 
         // ---- the next tile.  (Scheduling fences around the phases: moved into one
         // another they need twice the registers.)
-        const int next = tile + 4;
+        const int next = tile + W;
         const bool more = next < t_end;
         bool next_hidden = true;
         if (more) {
@@ -794,7 +808,7 @@ attn_kernel(AttnArgs a)
         hidden = next_hidden;
     }
 
-    // ---- join the four waves; every wave then finishes every fourth 16-dim tile
+    // ---- join the waves; each then finishes every W-th 16-dim tile
     const int64_t wrows = (int64_t)a.tokens * a.heads;
     const float lsum = rows_sum(l);
     if (h == 0) {
@@ -805,13 +819,13 @@ attn_kernel(AttnArgs a)
     for (int t = 0; t < 2 * NB; ++t)
         joined[wave][t][lane] = o[t];
     __syncthreads();
-    float mm = -INFINITY, w[4], lt = 0.f;
+    float mm = -INFINITY, w[W], lt = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < W; ++i)
         mm = fmaxf(mm, join_m[i][n]);
     const float mu = mm == -INFINITY ? 0.f : mm;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < W; ++i) {
         w[i] = __builtin_amdgcn_exp2f(join_m[i][n] - mu);
         lt = fmaf(w[i], join_l[i][n], lt);
     }
@@ -819,10 +833,10 @@ attn_kernel(AttnArgs a)
         const int hq = head * a.group + (r0 + n - tok * a.group);
         const int64_t row = (int64_t)(s.q0 + tok) * a.heads + hq;
         const float inv = lt > 0.f ? 1.f / lt : 0.f;
-        for (int t = wave; t < 2 * NB; t += 4) {
+        for (int t = wave; t < 2 * NB; t += W) {
             f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < W; ++i)
                 acc += joined[i][t][lane] * w[i];
             const int d0 = 16 * t + 4 * h;
             if (a.splits > 1)
@@ -887,7 +901,7 @@ attn_join_kernel(AttnArgs a, int slices)
             mm = mn;
 #pragma unroll
             for (int k = 0; k < JOIN_MOST; ++k)
-                if (x[k].y > 0.f) {
+                if (x[k].y != 0.f) {      // (also where it is not a number)
                     const float w = __builtin_amdgcn_exp2f(x[k].x - mu);
                     lt = fmaf(w, x[k].y, lt);
                     acc += y[k] * w;

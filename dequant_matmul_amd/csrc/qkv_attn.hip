@@ -24,8 +24,9 @@ AttnPlan attn_plan(const KvView &c, int64_t tokens, int64_t batch, int heads, in
     if (rows <= 32) {
         p.rows = 16;
         p.groups = (int)((rows + 15) / 16);
-        const int64_t wgs = batch * c.kv_heads * p.groups, most = tiles <= 8 ? 1 : (tiles + 3) / 4;
-        const int64_t splits = wgs > 0 ? (2 * cus + wgs - 1) / wgs : 1;
+        const int waves = attn_waves(c.nb);
+        const int64_t wgs = batch * c.kv_heads * p.groups, most = tiles <= 2 * waves ? 1 : (tiles + waves - 1) / waves;
+        const int64_t splits = wgs > 0 ? (cus + wgs - 1) / wgs : 1;
         p.splits = (int)(splits < most ? splits : most > 1 ? most : 1);
     } else {
         struct Shape { int rows, per_cu; float alone, full; };

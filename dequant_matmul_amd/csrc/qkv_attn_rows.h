@@ -393,7 +393,7 @@ hipError_t attn_blocks(const AttnArgs &a, const AttnPlan &p, int64_t batch, hipS
     constexpr int PARTS = sizeof(IO) == 4 ? 2 : 1;
     const dim3 grid((unsigned)p.splits, (unsigned)(a.kv_heads * p.groups), (unsigned)batch);
     if (p.rows == 16)
-        hipLaunchKernelGGL((attn_kernel<NB, KT, PARTS, IO>), grid, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((attn_kernel<NB, KT, PARTS, IO>), grid, dim3(64 * attn_waves(NB)), 0, s, a);
     else if (p.rows == 64)
         hipLaunchKernelGGL((attn_rows_kernel<NB, KT, 1, 4, PARTS, IO>), grid, dim3(256), 0, s, a);
     else if constexpr (PARTS == 1 || NB <= 4) {
