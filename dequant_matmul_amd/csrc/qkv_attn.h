@@ -510,11 +510,12 @@ __device__ __forceinline__ void weights(const f32x4 (&sc)[4], const uint32_t *vs
 
 // ---------------------------------------------------------------- the kernel --
 
-// Waves of a workgroup: two a SIMD, or the one that fits (256 dims).
-constexpr int attn_waves(int nb) { return nb > 4 ? 4 : 8; }
+// Waves of a workgroup.  (Eight, one workgroup a CU: 8.9 us instead of 9.3 for a token
+// at 500, Q8_0, fp32, but 35.9 instead of 32.6 for 16 of ragged lengths to 8190, Q4_0.)
+constexpr int ATTN_WAVES = 4;
 
 template <int NB, int KT, int PARTS, typename IO>
-__global__ void __launch_bounds__(64 * attn_waves(NB), NB > 4 ? 1 : 2)
+__global__ void __launch_bounds__(64 * ATTN_WAVES, NB > 4 ? 1 : 2)
 attn_kernel(AttnArgs a)
 {
     using L = KvLay<NB, KT>;
@@ -525,7 +526,7 @@ attn_kernel(AttnArgs a)
     constexpr int VN = KT == KV_Q4 ? NB : 2 * NB;      // V pieces
     constexpr bool SCALED = KT != KV_F16;
 
-    constexpr int W = attn_waves(NB);
+    constexpr int W = ATTN_WAVES;
     constexpr int SP = (16 * NB + 63) / 64;            // 16-byte pieces of a tile's scales per lane
     __shared__ __align__(16) f32x4 joined[W][2 * NB][64];
     __shared__ float join_m[W][16], join_l[W][16];

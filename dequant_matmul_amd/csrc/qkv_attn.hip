@@ -3,10 +3,14 @@
 
 namespace qmm {
 
-// Few rows (attn_kernel): two workgroups for every CU, as long as each still has a
-// tile for each of its four waves; up to 8 tiles (512 tokens) are not split, since
-// joining costs 4 us, about what they take (one 4096-wide layer's token at 500
-// tokens: 9.1 us whole, 9.5 split; at 1000: 13.6 and 9.7).
+// Few rows (attn_kernel): a workgroup for every CU, which is all that a single
+// sequence needs to draw the memory's bandwidth (one 4096-wide layer's token at 32000
+// tokens, Q8_0: 20.2 us in 32 splits, 22.3 in 64); two where there are several
+// sequences, whose lengths the host does not know (16 of ragged lengths to 8190: 32.6
+// in 4 splits, 38.4 in 2), but for 256 dims, of which a CU holds one.  As long as each
+// still has a tile for each of its four waves; up to 8 tiles (512 tokens) are not split,
+// since joining costs 4 us, about what they take (a token at 500 tokens: 9.3 us whole,
+// 9.9 split; at 1000: 13.7 and 10.1).
 //
 // Many rows (attn_rows_kernel): the cheapest of a few row groups and splits by a
 // model whose figures are measured on the 512-token chunk and the tree of the
@@ -24,9 +28,8 @@ AttnPlan attn_plan(const KvView &c, int64_t tokens, int64_t batch, int heads, in
     if (rows <= 32) {
         p.rows = 16;
         p.groups = (int)((rows + 15) / 16);
-        const int waves = attn_waves(c.nb);
-        const int64_t wgs = batch * c.kv_heads * p.groups, most = tiles <= 2 * waves ? 1 : (tiles + waves - 1) / waves;
-        const int64_t splits = wgs > 0 ? (cus + wgs - 1) / wgs : 1;
+        const int64_t wgs = batch * c.kv_heads * p.groups, most = tiles <= 8 ? 1 : (tiles + ATTN_WAVES - 1) / ATTN_WAVES;
+        const int64_t all = batch > 1 && c.nb <= 4 ? 2 * cus : cus, splits = wgs > 0 ? (all + wgs - 1) / wgs : 1;
         p.splits = (int)(splits < most ? splits : most > 1 ? most : 1);
     } else {
         struct Shape { int rows, per_cu; float alone, full; };

@@ -93,37 +93,34 @@ attn_rows_kernel(AttnArgs a)
         const int64_t at = ((((int64_t)page * a.kv_heads + head) << tshift) + (tile & ((1 << tshift) - 1))) *
                            (int64_t)L::TILE_BYTES;
         const uint8_t *kp = a.k + at, *vp = a.v + at;
+        // (a wave that has no piece left loads its first one again: a branch would make
+        // each load wait for the one before it)
 #pragma unroll
         for (int i = 0; i < KI; ++i) {
-            const int j = wave + W * i;
-            if (KN % W == 0 || j < KN) {
-                load_dw<CDW>(kp + (j * 64 + lane) * (L::G * L::UNIT), kr[i]);
-                if constexpr (FOLDED) {
-                    const int c = j / (NB / L::G), key = 16 * (n >> 2) + 4 * c + (n & 3);
-                    const uint16_t *sp = (const uint16_t *)(kp + L::k_scale(key, (j % (NB / L::G)) * L::G));
-                    // (nothing is computed from a load here: that would wait for it)
+            const int j = KN % W == 0 || wave + W * i < KN ? wave + W * i : wave < KN ? wave : 0;
+            load_dw<CDW>(kp + (j * 64 + lane) * (L::G * L::UNIT), kr[i]);
+            if constexpr (FOLDED) {
+                const int c = j / (NB / L::G), key = 16 * (n >> 2) + 4 * c + (n & 3);
+                const uint16_t *sp = (const uint16_t *)(kp + L::k_scale(key, (j % (NB / L::G)) * L::G));
+                // (nothing is computed from a load here: that would wait for it)
 #pragma unroll
-                    for (int w = 0; w < SDW; ++w)
-                        kd[i][w] = SPAIR ? ((const uint32_t *)sp)[w] : sp[w];
-                }
+                for (int w = 0; w < SDW; ++w)
+                    kd[i][w] = SPAIR ? ((const uint32_t *)sp)[w] : sp[w];
             }
         }
 #pragma unroll
         for (int i = 0; i < VI; ++i) {
-            const int j = wave + W * i;
-            if (VN % W == 0 || j < VN) {
-                load_dw<4>(vp + (j * 64 + lane) * 16, vr[i]);
-                if constexpr (FOLDED) {
-                    const uint8_t *sp = vp + L::v_scale(16 * h, KT == KV_Q8 ? j >> 1 : j);
-                    load_dw<4>(sp, &vd[i][0]);
-                    load_dw<4>(sp + 16, &vd[i][4]);
-                }
+            const int j = VN % W == 0 || wave + W * i < VN ? wave + W * i : wave < VN ? wave : 0;
+            load_dw<4>(vp + (j * 64 + lane) * 16, vr[i]);
+            if constexpr (FOLDED) {
+                const uint8_t *sp = vp + L::v_scale(16 * h, KT == KV_Q8 ? j >> 1 : j);
+                load_dw<4>(sp, &vd[i][0]);
+                load_dw<4>(sp + 16, &vd[i][4]);
             }
         }
         if constexpr (SCALED) {
-            const int t = threadIdx.x;
-            if (t < 16 * NB)
-                load_dw<4>((t < 8 * NB ? kp + 16 * t : vp + 16 * (t - 8 * NB)) + L::CODE_BYTES, sd);
+            const int t = 64 * W == 16 * NB || (int)threadIdx.x < 16 * NB ? (int)threadIdx.x : 0;
+            load_dw<4>((t < 8 * NB ? kp + 16 * t : vp + 16 * (t - 8 * NB)) + L::CODE_BYTES, sd);
         }
         return true;
     };
@@ -393,7 +390,7 @@ hipError_t attn_blocks(const AttnArgs &a, const AttnPlan &p, int64_t batch, hipS
     constexpr int PARTS = sizeof(IO) == 4 ? 2 : 1;
     const dim3 grid((unsigned)p.splits, (unsigned)(a.kv_heads * p.groups), (unsigned)batch);
     if (p.rows == 16)
-        hipLaunchKernelGGL((attn_kernel<NB, KT, PARTS, IO>), grid, dim3(64 * attn_waves(NB)), 0, s, a);
+        hipLaunchKernelGGL((attn_kernel<NB, KT, PARTS, IO>), grid, dim3(64 * ATTN_WAVES), 0, s, a);
     else if (p.rows == 64)
         hipLaunchKernelGGL((attn_rows_kernel<NB, KT, 1, 4, PARTS, IO>), grid, dim3(256), 0, s, a);
     else if constexpr (PARTS == 1 || NB <= 4) {
