@@ -218,6 +218,16 @@ attn_rows_kernel(AttnArgs a)
                 ks[4 * i] = y[0]; ks[4 * i + 1] = y[1]; ks[4 * i + 2] = y[2]; ks[4 * i + 3] = y[3];
             }
         }
+        f32x4 acc[SCALED ? 2 : 1][RT][4];
+        auto scale_block = [&](int bl) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        sc[rt][c][i] = fmaf(acc[bl & 1][rt][c][i], half_of(ks, SCALED ? (4 * c + i) * NB + bl : 0), sc[rt][c][i]);
+        };
         // block by block: 4 RT products in a row that do not depend on one another
         // (the matrix cores' latency is several times their rate); the fragments of
         // the next block are read meanwhile
@@ -232,7 +242,8 @@ attn_rows_kernel(AttnArgs a)
                 for (int c = 0; c < 4; ++c)
                     kf[(bl + 1) & 1][c] = kb[buf][c * NB + bl + 1][lane];
             }
-            f32x4 acc[RT][4];
+            // (the scales of a block's sums follow behind the next block's products, by
+            // when they are there)
 #pragma unroll
             for (int part = 0; part < PARTS; ++part)
 #pragma unroll
@@ -240,23 +251,16 @@ attn_rows_kernel(AttnArgs a)
 #pragma unroll
                     for (int rt = 0; rt < RT; ++rt) {
                         const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-                        acc[rt][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                            kf[bl & 1][c], qf[rt][part][bl], part > 0 ? acc[rt][c] : SCALED ? zero : sc[rt][c], 0, 0, 0);
+                        f32x4 &y = SCALED ? acc[bl & 1][rt][c] : sc[rt][c];
+                        y = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[bl & 1][c], qf[rt][part][bl],
+                                                                   SCALED && part == 0 ? zero : y, 0, 0, 0);
                     }
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    if constexpr (SCALED) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            sc[rt][c][i] = fmaf(acc[rt][c][i], half_of(ks, (4 * c + i) * NB + bl), sc[rt][c][i]);
-                    } else {
-                        sc[rt][c] = acc[rt][c];
-                    }
-                }
+            if (SCALED && bl > 0)
+                scale_block(bl - 1);
             __builtin_amdgcn_sched_barrier(0);
         }
+        if (SCALED)
+            scale_block(NB - 1);
         const bool tail = tile >= my_clear;
         if (tail) {
 #pragma unroll
@@ -303,37 +307,37 @@ attn_rows_kernel(AttnArgs a)
             if constexpr (PARTS == 2)
                 l[rt] += sum16(sc[rt]);
         }
+        // the fragments of the next block are read under the products of this one
+        h16x8 vf[2][2], hi[RT], lo[RT];
 #pragma unroll
-        for (int st = 0; st < 2; ++st) {
-            h16x8 hi[RT], lo[RT];
-            if constexpr (!SCALED) {
+        for (int u = 0; u < 2; ++u)
+            vf[0][u] = vb[buf][2 * u][lane];
+#pragma unroll
+        for (int step = 0; step < 2 * NB; ++step) {
+            const int st = step / NB, bl = step % NB;
+            if (step + 1 < 2 * NB) {
+                const int st1 = (step + 1) / NB, bl1 = (step + 1) % NB;
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    vf[(step + 1) & 1][u] = vb[buf][2 * (2 * bl1 + u) + st1][lane];
+            }
+            if (SCALED || bl == 0) {
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
-                    weights<KT, PARTS, false>(sc[rt], vs, st, hi[rt], lo[rt]);
+                    weights<KT, PARTS, SCALED>(sc[rt], &vs[SCALED ? 8 * bl : 0], st, hi[rt], lo[rt]);
                     if constexpr (PARTS == 1)
                         l[rt] = sum8(hi[rt], l[rt]);
                 }
             }
 #pragma unroll
-            for (int bl = 0; bl < NB; ++bl) {
-                if constexpr (SCALED) {
-#pragma unroll
-                    for (int rt = 0; rt < RT; ++rt)
-                        weights<KT, PARTS, true>(sc[rt], &vs[8 * bl], st, hi[rt], lo[rt]);
-                }
-                h16x8 vf[2];
+            for (int part = 0; part < PARTS; ++part)
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
-                    vf[u] = vb[buf][2 * (2 * bl + u) + st][lane];
 #pragma unroll
-                for (int part = 0; part < PARTS; ++part)
-#pragma unroll
-                    for (int u = 0; u < 2; ++u)
-#pragma unroll
-                        for (int rt = 0; rt < RT; ++rt)
-                            o[rt][2 * bl + u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                                vf[u], part ? lo[rt] : hi[rt], o[rt][2 * bl + u], 0, 0, 0);
-            }
+                    for (int rt = 0; rt < RT; ++rt)
+                        o[rt][2 * bl + u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                            vf[step & 1][u], part ? lo[rt] : hi[rt], o[rt][2 * bl + u], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
         }
     };
 
