@@ -63,23 +63,6 @@ attn_rows_kernel(AttnArgs a)
     if constexpr (SATURATE)
         __builtin_amdgcn_s_setreg(MODE_FP16_OVFL, 1);
 
-    h16x8 qf[RT][PARTS][NB];
-    float rs[RT], m[RT], shift[RT], l[RT];
-    int tok[RT];
-    f32x4 o[RT][2 * NB];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        const int r = r0 + 16 * rt + n;
-        rs[rt] = load_row<NB, KT, PARTS, IO>(a, s, head, r, rows, h, qf[rt]);
-        tok[rt] = r < rows ? r / a.group : -1;
-        m[rt] = -INFINITY;
-        shift[rt] = P_TOP;
-        l[rt] = 0.f;
-#pragma unroll
-        for (int t = 0; t < 2 * NB; ++t)
-            o[rt][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
-    }
-
     // ---- staging: a tile's pieces, dealt to the waves
     uint32_t kr[KI][CDW], kd[FOLDED ? KI : 1][SDW], vr[VI][4], vd[FOLDED ? VI : 1][8], sd[4];
     PageIds pages;
@@ -201,6 +184,26 @@ attn_rows_kernel(AttnArgs a)
             }
         }
     };
+
+    // ---- the first tile is loaded, then this wave's rows; `live` is the same in every
+    // wave
+    bool live = t_begin < t_end && load_tile(t_begin);
+    h16x8 qf[RT][PARTS][NB];
+    float rs[RT], m[RT], shift[RT], l[RT];
+    int tok[RT];
+    f32x4 o[RT][2 * NB];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        const int r = r0 + 16 * rt + n;
+        rs[rt] = load_row<NB, KT, PARTS, IO>(a, s, head, r, rows, h, qf[rt]);
+        tok[rt] = r < rows ? r / a.group : -1;
+        m[rt] = -INFINITY;
+        shift[rt] = P_TOP;
+        l[rt] = 0.f;
+#pragma unroll
+        for (int t = 0; t < 2 * NB; ++t)
+            o[rt][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    }
 
     auto compute = [&](int buf, int tile) {
         const int64_t k0 = (int64_t)tile * KV_TILE;
@@ -341,8 +344,7 @@ attn_rows_kernel(AttnArgs a)
         }
     };
 
-    // ---- the tiles; `live` is the same in every wave
-    bool live = t_begin < t_end && load_tile(t_begin);
+    // ---- the tiles
     if (live)
         store_tile(0, t_begin);
     __syncthreads();
