@@ -1,6 +1,5 @@
 // qkv_attn_rows.h -- attention of many query rows over the paged cache: trees
-// and prompt chunks whose rows (new tokens times heads of a kv head) exceed one
-// 16-row tile.
+// and prompt chunks with more than 32 rows (new tokens times heads) a kv head.
 //
 // As attn_kernel, but the W waves of a workgroup hold different rows (RT tiles of
 // 16 each) and walk the same tiles of 64 tokens: a tile is decoded once
@@ -12,6 +11,14 @@
 //     VALU more than the whole softmax.
 //   PARTS 2 (fp32 rows): LDS holds the exact codes, the scales beside them; scores
 //     and weights are scaled in fp32 as in attn_kernel.
+//
+// Bound: the VALU's part (softmax, scales, decoding) and the matrix cores' in turn:
+// instructions of two waves of a SIMD hardly overlap.  Whole calls, replayed, 32/8
+// heads of 128:
+//   512 tokens at 7680: fp16 84 us from Q4_0 (790 TFLOP/s), 84 to 89 from Q8_0 and
+//     F16; fp32 from Q8_0 185
+//   8192 tokens at 0, F16 cache, fp16: 600 us (916 TFLOP/s)
+//   trees of 29 in 4 sequences at 4000, Q8_0: fp32 37 us, fp16 26
 #pragma once
 
 #include "qkv_attn.h"
@@ -56,12 +63,6 @@ attn_rows_kernel(AttnArgs a)
     // tiles that this wave's rows see something of
     const int my_last = ((rows < r0 + 16 * RT ? rows : r0 + 16 * RT) - 1) / a.group;
     const int my_end = r0 >= rows ? 0 : (int)((seen(a, s, my_last) + KV_TILE - 1) / KV_TILE);
-
-    // 127 times the largest scale of a Q8_0 block (516) is past the fp16 range: a
-    // decoded value saturates at 65504 (MODE.FP16_OVFL) until the output is written
-    constexpr bool SATURATE = FOLDED && KT == KV_Q8;
-    if constexpr (SATURATE)
-        __builtin_amdgcn_s_setreg(MODE_FP16_OVFL, 1);
 
     // ---- staging: a tile's pieces, dealt to the waves
     uint32_t kr[KI][CDW], kd[FOLDED ? KI : 1][SDW], vr[VI][4], vd[FOLDED ? VI : 1][8], sd[4];
@@ -111,6 +112,12 @@ attn_rows_kernel(AttnArgs a)
     // what lies behind the last token, and at new ones never appended, may be any
     // bits: V (or its scale) becomes 0, or at least finite
     auto store_tile = [&](int buf, int tile) {
+        // 127 times the largest scale of a Q8_0 block (516) is past the fp16 range:
+        // decoded values saturate at 65504.  (For these alone: in this mode a weight that
+        // is not a number would become one.)
+        constexpr bool SATURATE = FOLDED && KT == KV_Q8;
+        if constexpr (SATURATE)
+            __builtin_amdgcn_s_setreg(MODE_FP16_OVFL, 1);
         const int64_t rest = nseen - (int64_t)tile * KV_TILE;
         const int left = (int)(rest < KV_TILE ? rest : KV_TILE) - 16 * h;
         const bool tail = tile >= clear;
@@ -163,6 +170,8 @@ attn_rows_kernel(AttnArgs a)
                 }
             }
         }
+        if constexpr (SATURATE)
+            __builtin_amdgcn_s_setreg(MODE_FP16_OVFL, 0);
         if constexpr (SCALED) {
             // threads of one wave hold the V scales of a tile
             const int t = threadIdx.x;
@@ -358,9 +367,6 @@ attn_rows_kernel(AttnArgs a)
         live = next;
         __syncthreads();
     }
-
-    if constexpr (SATURATE)
-        __builtin_amdgcn_s_setreg(MODE_FP16_OVFL, 0);
 
     // ---- this wave's rows
     const int64_t wrows = (int64_t)a.tokens * a.heads;

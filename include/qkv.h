@@ -194,7 +194,8 @@ QMM_API int qkv_move(const qkv_cache *cache, const int32_t *src, const int32_t *
  * Arithmetic: dot products, softmax and sums in fp32.  QKV_F32: q and the
  * softmax weights enter the matrix cores as two fp16 parts each (about 22
  * bits) against the exact codes.  QKV_HALF: the weights (times the V scale)
- * enter as one fp16; rows of many tokens (chunks) take K and V rounded to fp16.
+ * enter as one fp16; a call with more than 32 rows a kv head (max_q * heads /
+ * kv_heads) takes K and V as code * scale rounded to fp16.
  * No atomics: the same call gives the same bits.
  */
 typedef struct qkv_attn {

@@ -315,6 +315,21 @@ def test_non_finite_queries_stay_in_their_row(kind, dt):
 
 
 @pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("tq", [2, 40])
+def test_a_query_that_is_not_a_number_stays_one(kind, dt, tq):
+    """Also where a sequence is taken in several splits; its neighbours are as without it."""
+    c = Case(kind, [3000], [tq], 1, 4, 64, seed=12)
+    clean = c.run(dt)
+    c.q[1, 2, 5] = np.nan
+    got = c.run(dt)
+    assert torch.isnan(got[1, 2]).all()
+    hit = torch.zeros(got.shape[:2], dtype=torch.bool, device=DEV)
+    hit[1, 2] = True
+    assert torch.equal(got[~hit], clean[~hit])
+
+
+@pytest.mark.parametrize("dt", DTS)
 def test_strided_rows_and_uniform_sequences(dt):
     c = Case("q4_0", [90, 91, 92], [2, 2, 2], 2, 4, 128, seed=12)
     H, D = c.q.shape[1:]
