@@ -226,10 +226,10 @@ def test_rows_of_no_sequence_are_left(dt):
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("tree", [False, True])
 @pytest.mark.parametrize("pad", [6, 40])
-@pytest.mark.parametrize("bits", [0xffff, 0x7c00, 0x7bff])
+@pytest.mark.parametrize("bits", [0xffff, 0x7d55, 0x7c00, 0x7bff])
 def test_padded_tokens_never_appended(kind, dt, tree, pad, bits):
     """Equal shares of which the last rows are padding whose K and V were never
-    written: NaN, infinity or the largest number lie there, and the rows before
+    written: NaN (quiet or signalling), infinity or the largest number lie there, and the rows before
     them (which do not see them) are what they are without."""
     c = Case(kind, [5, 64, 100], [4, 1, 5], 2, 4, 128, page=256, seed=pad, tree=tree, vscale=2.0 ** -6)
     clean = q.KVCache(R.TYPES[kind], 2, 128, c.pages, page_size=256)
