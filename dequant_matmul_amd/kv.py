@@ -306,7 +306,9 @@ def attention(cache, q, table, ctx, qstart=None, mask=None, scale=None, max_q=No
     [batch + 1] first rows of q (None: equal shares).  mask None: new tokens see
     those up to themselves; int64 [tokens, words]: bit j of a row's words lets it
     see new token j.  scale None: head_dim ** -0.5.  max_q / max_ctx bound the
-    new and all tokens of a sequence (defaults: what q and the table hold)."""
+    new and all tokens of a sequence (defaults: what q and the table hold); they
+    choose the kernel and its splits, so close bounds are faster.  Rows of q that
+    belong to no sequence are not written."""
     a = _sizes(cache, q, table, ctx, qstart, mask, max_q, max_ctx)
     dev = cache.device
     if out is None:
