@@ -278,7 +278,7 @@ constexpr float LOG2E = 1.44269504088896341f;
 // The softmax weights of a row are taken relative to a reference M, exp2(z + e -
 // M + P_TOP - e) for score z and e the exponent of the tile's V scales: weight
 // times V scale, the number that is rounded to fp16 parts, is near 2^P_TOP for the
-// largest, whatever the size of V, and a normal fp16 down to 2^-24 of it.  (F16
+// largest, whatever the size of V (but see SCALES_ALIKE), and a normal fp16 down to 2^-24 of it.  (F16
 // has no scale: e = 0.)  M need not be the maximum: it is raised only when a
 // product would pass 2^(P_TOP + P_SLACK) (fp16 ends at 2^16), which after a row's
 // first tile is rare; the exchange between lanes, the new reference and the
@@ -301,6 +301,28 @@ __device__ __forceinline__ float scale_exponent(const uint32_t (&w)[4])
     f = fmaxf(f, dpp_f(f, 0x141));
     f = fmaxf(f, dpp_f(f, 0x140));
     return rows_max(f);
+}
+
+// One exponent for a tile is right while its V scales lie near one another.  A product
+// of the fp16 range's top 2^P_TOP with the largest scale, and of a token whose scale is
+// 2^d below it, lies 2^d below the top: two parts keep 22 bits down to 2^-3 (d = 13), one
+// keeps 11 down to 2^-14 (d = 24).  Beyond SCALES_ALIKE, which leaves room for weights
+// that are smaller as well, the reference is taken token by token (masked_top): a token
+// without weight, but with large values, else takes the bits of all its neighbours.
+template <int PARTS>
+constexpr float SCALES_ALIKE = PARTS == 2 ? 8.f : 16.f;
+
+// Whether the exponent of some V scale lies more than `alike` below ev, the largest
+// one's; `counts`: this lane holds eight of them (w), of dims that exist.
+__device__ __forceinline__ bool scales_unlike(const uint32_t (&w)[4], bool counts, float ev, float alike)
+{
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    u16x2 m = {0x7fff, 0x7fff};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        m = __builtin_elementwise_min(m, __builtin_bit_cast(u16x2, w[i] & 0x7fff7fffu));
+    const int e = (m[0] < m[1] ? m[0] : m[1]) >> 10;
+    return __any(counts && (float)((e > 1 ? e : 1) - 14) < ev - alike);
 }
 
 // A dword of two fp16 (tokens i and j of which `left` exist): what is past the
@@ -417,10 +439,10 @@ __device__ __forceinline__ float lane_max(const f32x4 (&sc)[4])
     return mx;
 }
 
-// What lane_max is to rows that do not see every token: the largest score plus the
-// exponent of that token's own V scales (vs: fp16 in LDS, the lane's 16 tokens of
-// block 0; blocks are 32 dwords apart), so that the scale of a token that a row
-// does not see has no part in the row's reference.
+// What lane_max is to rows that do not see every token, and to tiles of unlike V scales:
+// the largest score plus the exponent of that token's own V scales (vs: fp16 in LDS, the
+// lane's 16 tokens of block 0; blocks are 32 dwords apart), so that the scale of a token
+// that a row does not see, or gives no weight, has no part in the row's reference.
 template <int NB>
 __device__ __forceinline__ float masked_top(const f32x4 (&sc)[4], float rs, const uint32_t *vs)
 {
@@ -621,6 +643,9 @@ attn_kernel(AttnArgs a)
 
     // A page id outside the cache: its tile is walked with nothing seen (and page
     // 0 loaded in its place), so that every tile is the same straight line.
+    // whether this lane's last piece of scales is V's, of dims that exist
+    const int vpiece = 64 * (SP - 1) + lane - 8 * NB;
+    const bool counts = vpiece >= 0 && vpiece < 8 * NB && 32 * (vpiece >> 3) < a.dim;
     int tile = t_begin + wave;
     bool hidden = true;
     int64_t at = 0;
@@ -640,6 +665,7 @@ attn_kernel(AttnArgs a)
     for (; tile < t_end; tile += W) {
         const int64_t k0 = (int64_t)tile * KV_TILE, seen_to = hidden ? k0 : nseen;
         const bool tail = hidden || tile >= clear;       // some row does not see all of it
+        bool unlike = false;
         float ev = 0.f;
         if constexpr (SCALED) {
             const int left = (int)(seen_to - k0 < KV_TILE ? seen_to - k0 : KV_TILE);
@@ -666,6 +692,7 @@ attn_kernel(AttnArgs a)
             }
             wave_lds_sync();
             ev = scale_exponent(big);
+            unlike = scales_unlike(big, counts, ev, SCALES_ALIKE<PARTS>);
         }
 
         // ---- the next tile.  (Scheduling fences around the phases: moved into one
@@ -760,7 +787,7 @@ attn_kernel(AttnArgs a)
             }
         }
         float top;
-        if (SCALED && tail)
+        if (SCALED && (tail || unlike))
             top = masked_top<NB>(sc, rs, &scales[wave][32 * NB + 8 * h]);
         else
             top = fmaf(lane_max(sc), rs, ev);

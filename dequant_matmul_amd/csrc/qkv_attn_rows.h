@@ -44,6 +44,7 @@ attn_rows_kernel(AttnArgs a)
     __shared__ __align__(16) h16x8 kb[2][4 * NB][64], vb[2][4 * NB][64];
     __shared__ __align__(16) uint32_t kscale[2][SCALED ? 32 * NB : 4], vscale[2][SCALED ? 32 * NB : 4];
     __shared__ float exponent[2];
+    __shared__ int unlike[2];
 
     const int lane = threadIdx.x & 63, n = lane & 15, h = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);     // the same in every lane, for the compiler too
@@ -188,8 +189,12 @@ attn_rows_kernel(AttnArgs a)
             }
             if (wave == 8 * NB / 64) {
                 const float e = scale_exponent(big);
-                if (lane == 0)
+                const bool counts = t >= 8 * NB && t < 16 * NB && 32 * ((t - 8 * NB) >> 3) < a.dim;
+                const bool far = scales_unlike(big, counts, e, SCALES_ALIKE<PARTS>);
+                if (lane == 0) {
                     exponent[buf] = e;
+                    unlike[buf] = far;
+                }
             }
         }
     };
@@ -287,6 +292,7 @@ attn_rows_kernel(AttnArgs a)
         }
         uint32_t vs[SCALED ? 8 * NB : 1];
         float ev = 0.f;
+        bool apart = false;     // token by token: masked, or unlike V scales
         if constexpr (SCALED) {
 #pragma unroll
             for (int bl = 0; bl < NB; ++bl)
@@ -297,12 +303,13 @@ attn_rows_kernel(AttnArgs a)
                     vs[8 * bl + 4 * i + 2] = y[2]; vs[8 * bl + 4 * i + 3] = y[3];
                 }
             ev = exponent[buf];
+            apart = tail || __builtin_amdgcn_readfirstlane(unlike[buf]) != 0;
         }
         float top[RT];
         bool more = false;
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-            if (SCALED && tail)
+            if (SCALED && apart)
                 top[rt] = masked_top<NB>(sc[rt], rs[rt], &vscale[buf][8 * h]);
             else
                 top[rt] = fmaf(lane_max(sc[rt]), rs[rt], ev);

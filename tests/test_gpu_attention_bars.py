@@ -1,0 +1,97 @@
+"""GPU tests of attention where the usual bars would hide a loss of accuracy:
+score errors counted with the weight of their token, losses at the bottom of the
+fp16 range with the largest product instead of the largest |v|.
+
+p are the softmax weights of the reference, A = sum_j p_j |v_j|, e_j = sum_d |scale
+q_d k_jd| the size of a score.  A score error of r e_j moves weight j by that factor,
+and the sum of the weights with it, so the output by r S, S = sum_j p_j e_j (|v_j| + A).
+  float32: q and the weights (times the V scale) in two fp16 parts, 2^-22 each, fp32
+    sums of at most 2^8 products with half steps of 2^-24 a block and a tree over
+    tiles and splits: 2^-19 S + 2^-18 A.
+  float16, few rows: q exact; the weight (times the V scale) rounded once to fp16 and
+    the output once, half a step of 2^-11 each: 2^-10 A on top.
+  float16, many rows: K and V rounded to fp16 too: 2^-11 S, and 2^-11 A on top of that.
+Below 2^-14 a half of a product has steps of 2^-24, an error of 2^-25 against a
+reference of 2^10.  The reference lies at most 2^5 below the row's largest product p_j
+s_j (s_j the largest V scale of token j, at least 2^-14), and at most 2^w above it, w
+the spread of V scales up to which a tile is taken at one exponent (8 in float32, 16 in
+float16), and another 2 for exponents rounded up: n 2^(w - 33) max_j p_j max(vmax_j,
+2^-7) for n tokens, vmax_j the largest stored |v| of token j (a Q8_0 code reaches 127).
+A float16 result below 2^-14 has an error of 2^-25.
+"""
+import numpy as np
+import pytest
+
+import kv_ref as R
+import test_gpu_attention as A
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+
+import dequant_matmul_amd as q  # noqa: E402
+
+up, DEV = A.up, A.DEV
+
+
+def put(c, b, k, v):
+    """The K and V rows of sequence b written anew."""
+    p = np.arange(len(k))
+    slots = c.table[b, p // c.page] * c.page + p % c.page
+    q.kv_append(c.cache, up(k.astype(np.float32)), up(v.astype(np.float32)), up(slots.astype(np.int32)))
+    c.k[b], c.v[b] = R.stored(k, c.kind), R.stored(v, c.kind)
+
+
+def judge(c, got, dt, b=0, rows=None, heads=None):
+    """Rows (of sequence b) and heads of got within the bar; every bar must also
+    refuse a result of zeros."""
+    rows = np.arange(c.tq[b]) if rows is None else np.asarray(rows)
+    at = c.starts[b] + rows
+    heads = range(c.q.shape[1]) if heads is None else heads
+    group = c.q.shape[1] // c.k[b].shape[1]
+    few = max(c.tq) * group <= 32
+    x = up(c.q[at]).to(dt).cpu().numpy().astype(np.float64)
+    got = got[up(at)].cpu().numpy().astype(np.float64)
+    worst, told = 0.0, False
+    for h in heads:
+        k, v = c.k[b][:, h // group], c.v[b][:, h // group]
+        s = np.where(c.see[b][rows], x[:, h] @ k.T * c.D ** -0.5, -np.inf)
+        m = s.max(-1, keepdims=True)
+        p = np.exp(s - np.where(np.isfinite(m), m, 0))
+        p /= np.maximum(p.sum(-1, keepdims=True), 1e-300)
+        out, size = p @ v, p @ np.abs(v)
+        pe = p * (np.abs(x[:, h]) @ np.abs(k).T * c.D ** -0.5)
+        moved = pe @ np.abs(v) + size * pe.sum(-1, keepdims=True)
+        w = 8 if dt == torch.float32 else 16
+        low = len(k) * 2.0 ** (w - 33) * (p * np.maximum(np.abs(v).max(-1), 2.0 ** -7)).max(-1)[:, None]
+        tol = 2.0 ** -19 * moved + 2.0 ** -18 * size + low
+        if dt == torch.float16:
+            tol += 2.0 ** -10 * size + 2.0 ** -25
+            if not few:
+                tol += 2.0 ** -11 * (moved + size) + 2.0 ** -25
+        off = np.abs(got[:, h] - out)
+        assert not np.isnan(off).any()
+        worst, told = max(worst, (off / tol).max()), told or (np.abs(out) > tol).any()
+    assert worst <= 1, "%.3g of the bar" % worst
+    assert told or not np.concatenate([c.see[b][rows]]).any()
+
+
+@pytest.mark.parametrize("dt", A.DTS)
+@pytest.mark.parametrize("kind", A.KINDS)
+@pytest.mark.parametrize("tq", [1, 40])
+@pytest.mark.parametrize("D", [64, 80, 128, 256])
+def test_unlike_scales_of_v_in_one_tile(kind, dt, tq, D):
+    """A token with values 2^27 times those of its 63 neighbours and no weight has no
+    part in the result, and costs it no accuracy either."""
+    c = A.Case(kind, [64], [tq], 2, 4, D, seed=50 + D)
+    rng = np.random.default_rng(51)
+    k, v = rng.standard_normal((2, 64 + tq, 2, D))
+    k *= 0.05
+    v *= 2.0 ** -12
+    k[10], v[10] = 0, 60000.0
+    k[10, :, :8] = -6.0 * D ** 0.5         # a score near -48 * 2
+    c.q[..., :8] = 2.0
+    put(c, 0, k, v)
+    judge(c, c.run(dt), dt)
