@@ -24,6 +24,8 @@ from __future__ import annotations
 import ctypes
 import os
 
+import torch
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libqmm.so")
 
@@ -102,9 +104,15 @@ def _torch():
     return torch
 
 
-def _stream_ptr(device) -> int:
-    torch = _torch()
-    return torch.cuda.current_stream(device).cuda_stream
+def _launch(f, device, *args) -> int:
+    """Status of f(*args, torch's current stream of the device), called with that
+    device current: the default stream is NULL on every device, and means the
+    current one's to the library."""
+    i = device.index
+    if i == torch._C._cuda_getDevice():
+        return f(*args, torch._C._cuda_getCurrentRawStream(i))
+    with torch.cuda.device(i):
+        return f(*args, torch._C._cuda_getCurrentRawStream(i))
 
 
 def _check_w(w, qtype: int, n: int, k: int):
@@ -141,7 +149,7 @@ def dequant(w, qtype: int, n: int, k: int, out=None):
     torch = _torch()
     _check_w(w, qtype, n, k)
     out = _out(out, (n, k), torch.float32, w.device)
-    _call(lib.qmm_dequant(qtype, w.data_ptr(), n, k, out.data_ptr(), _stream_ptr(w.device)), "qmm_dequant")
+    _call(_launch(lib.qmm_dequant, w.device, qtype, w.data_ptr(), n, k, out.data_ptr()), "qmm_dequant")
     return out
 
 
@@ -150,8 +158,7 @@ def dequant_f16(w, qtype: int, n: int, k: int, out=None):
     torch = _torch()
     _check_w(w, qtype, n, k)
     out = _out(out, (n, k), torch.float16, w.device)
-    _call(lib.qmm_dequant_f16(qtype, w.data_ptr(), n, k, out.data_ptr(), _stream_ptr(w.device)),
-          "qmm_dequant_f16")
+    _call(_launch(lib.qmm_dequant_f16, w.device, qtype, w.data_ptr(), n, k, out.data_ptr()), "qmm_dequant_f16")
     return out
 
 
@@ -171,7 +178,7 @@ def embed(table, qtype: int, vocab: int, k: int, ids, dtype=None, out=None):
         raise ValueError("ids and the table must be on the same device")
     out = _out(out, (seq, k), dtype, table.device)
     f = lib.qmm_embed if dtype == torch.float32 else lib.qmm_embed_f16
-    _call(f(qtype, table.data_ptr(), vocab, k, ids.data_ptr(), seq, out.data_ptr(), _stream_ptr(table.device)),
+    _call(_launch(f, table.device, qtype, table.data_ptr(), vocab, k, ids.data_ptr(), seq, out.data_ptr()),
           "qmm_embed")
     return out
 
@@ -195,7 +202,7 @@ def quantize(x, qtype: int, out=None):
         f = lib.qmm_quantize_f16
     else:
         raise ValueError("x must be float32 or float16")
-    _call(f(qtype, x.data_ptr(), n, k, out.data_ptr(), _stream_ptr(x.device)), "qmm_quantize")
+    _call(_launch(f, x.device, qtype, x.data_ptr(), n, k, out.data_ptr()), "qmm_quantize")
     return out
 
 
@@ -212,8 +219,7 @@ def gemv(w, qtype: int, n: int, k: int, x, out=None):
     if x.device != w.device:
         raise ValueError("x and the weights must be on the same device")
     out = _out(out, (B, n), torch.float32, w.device)
-    _call(lib.qmm_gemv(qtype, w.data_ptr(), n, k, x.data_ptr(), B, out.data_ptr(), _stream_ptr(w.device)),
-          "qmm_gemv")
+    _call(_launch(lib.qmm_gemv, w.device, qtype, w.data_ptr(), n, k, x.data_ptr(), B, out.data_ptr()), "qmm_gemv")
     return out[0] if squeeze else out
 
 
@@ -239,8 +245,8 @@ def gemv_multi(ws, qtype: int, ns, k: int, xs, outs=None):
     xp = (ctypes.c_void_p * max(np_, 1))(*[x.data_ptr() for x in xs])
     yp = (ctypes.c_void_p * max(np_, 1))(*[o.data_ptr() for o in outs])
     nn = (ctypes.c_int64 * max(np_, 1))(*ns)
-    dev = ws[0].device if np_ else None
-    _call(lib.qmm_gemv_multi(qtype, np_, wp, nn, k, xp, B, yp, _stream_ptr(dev) if np_ else None),
+    args = (qtype, np_, wp, nn, k, xp, B, yp)
+    _call(_launch(lib.qmm_gemv_multi, ws[0].device, *args) if np_ else lib.qmm_gemv_multi(*args, None),
           "qmm_gemv_multi")
     return outs
 
@@ -272,8 +278,15 @@ def gemv_pass(problems, table=None, stream=None):
     if table is None:
         table = pass_table(problems)
     n = len(problems)
-    st = stream if stream is not None else (_stream_ptr(problems[0][0].device) if n else None)
-    _call(lib.qmm_gemv_pass(n, ctypes.cast(table, ctypes.c_void_p), st), "qmm_gemv_pass")
+    tab = ctypes.cast(table, ctypes.c_void_p)
+    if n == 0:
+        status = lib.qmm_gemv_pass(n, tab, stream)
+    elif stream is None:
+        status = _launch(lib.qmm_gemv_pass, problems[0][0].device, n, tab)
+    else:
+        with torch.cuda.device(problems[0][0].device):
+            status = lib.qmm_gemv_pass(n, tab, stream)
+    _call(status, "qmm_gemv_pass")
 
 
 def gemm_prefill(w, qtype: int, n: int, k: int, x, out=None):
@@ -286,8 +299,8 @@ def gemm_prefill(w, qtype: int, n: int, k: int, x, out=None):
     if x.device != w.device:
         raise ValueError("X and the weights must be on the same device")
     out = _out(out, (m, n), torch.float32, w.device)
-    _call(lib.qmm_gemm_prefill(qtype, w.data_ptr(), n, k, x.data_ptr(), m, out.data_ptr(),
-                               _stream_ptr(w.device)), "qmm_gemm_prefill")
+    _call(_launch(lib.qmm_gemm_prefill, w.device, qtype, w.data_ptr(), n, k, x.data_ptr(), m, out.data_ptr()),
+          "qmm_gemm_prefill")
     return out
 
 

@@ -20,7 +20,7 @@ import math
 
 import torch
 
-from . import _call, _I, _I64, _P, _SZ, lib
+from . import _call, _I, _I64, _launch, _P, _SZ, lib
 
 F16 = 16   # cache type: plain fp16 (Q8_0 and Q4_0 are the block types)
 
@@ -68,7 +68,6 @@ class AttnStruct(ctypes.Structure):
 
 _DTYPES = {torch.float32: 0, torch.float16: 1}
 _F32, _I32, _I64T, _U8 = torch.float32, torch.int32, torch.int64, torch.uint8
-_raw_stream = torch._C._cuda_getCurrentRawStream
 
 # The checks below stand on the path of every decoded token, where a call costs
 # the host about as much as its kernel: one condition each, the message only
@@ -139,8 +138,7 @@ def rope_angles(pos, freqs, magnitude=1.0, out=None):
         out = torch.empty((T, P, 2), dtype=_F32, device=dev)
     elif _angles(out, T, dev) != P:
         raise ValueError("out must be [tokens, pairs, 2]")
-    status = lib.qkv_rope_angles(pos.data_ptr(), T, freqs.data_ptr(), P, magnitude, out.data_ptr(),
-                                 _raw_stream(dev.index))
+    status = _launch(lib.qkv_rope_angles, dev, pos.data_ptr(), T, freqs.data_ptr(), P, magnitude, out.data_ptr())
     if status:
         _call(status, "qkv_rope_angles")
     return out
@@ -160,8 +158,8 @@ def rope(x, cs, interleaved=False, out=None):
         out_stride = got[4]
         if got[:4] != (code, T, H, D) or out.device != dev:
             raise ValueError("out must have the type, shape and device of x")
-    status = lib.qkv_rope(code, x.data_ptr(), stride, T, H, D, cs.data_ptr(), pairs, 1 if interleaved else 0,
-                          out.data_ptr(), out_stride, _raw_stream(dev.index))
+    status = _launch(lib.qkv_rope, dev, code, x.data_ptr(), stride, T, H, D, cs.data_ptr(), pairs, 1 if interleaved else 0,
+                     out.data_ptr(), out_stride)
     if status:
         _call(status, "qkv_rope")
     return out
@@ -207,9 +205,8 @@ def kv_append(cache, k, v, slots, cs=None, interleaved=False):
     if slots.shape[0] != T:
         raise ValueError("slots must have one entry per token")
     pairs = _angles(cs, T, dev) if cs is not None else 0
-    status = lib.qkv_append(cache.ptr, code, k.data_ptr(), k_stride, v.data_ptr(), got[4], T, slots.data_ptr(),
-                            cs.data_ptr() if cs is not None else None, pairs, 1 if interleaved else 0,
-                            _raw_stream(dev.index))
+    status = _launch(lib.qkv_append, dev, cache.ptr, code, k.data_ptr(), k_stride, v.data_ptr(), got[4], T, slots.data_ptr(),
+                     cs.data_ptr() if cs is not None else None, pairs, 1 if interleaved else 0)
     if status:
         _call(status, "qkv_append")
 
@@ -233,8 +230,7 @@ def kv_read(cache, slots, dtype=torch.float32, k_out=None, v_out=None):
             if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != dev:
                 raise ValueError("outputs must be contiguous %s tensors of shape %s on %s" % (dtype, shape, dev))
         k_out, v_out = outs
-    status = lib.qkv_read(cache.ptr, code, slots.data_ptr(), n, k_out.data_ptr(), v_out.data_ptr(),
-                          _raw_stream(dev.index))
+    status = _launch(lib.qkv_read, dev, cache.ptr, code, slots.data_ptr(), n, k_out.data_ptr(), v_out.data_ptr())
     if status:
         _call(status, "qkv_read")
     return k_out, v_out
@@ -249,7 +245,7 @@ def kv_move(cache, src, dst):
     groups, n = src.shape
     if dst.shape != src.shape:
         raise ValueError("src and dst must have the same shape")
-    status = lib.qkv_move(cache.ptr, src.data_ptr(), dst.data_ptr(), groups, n, _raw_stream(dev.index))
+    status = _launch(lib.qkv_move, dev, cache.ptr, src.data_ptr(), dst.data_ptr(), groups, n)
     if status:
         _call(status, "qkv_move")
 
@@ -325,7 +321,7 @@ def attention(cache, q, table, ctx, qstart=None, mask=None, scale=None, max_q=No
     elif workspace.dtype is not _U8 or workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on %s" % dev)
     a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
-    status = lib.qkv_attention(cache.ptr, ctypes.addressof(a), _raw_stream(dev.index))
+    status = _launch(lib.qkv_attention, dev, cache.ptr, ctypes.addressof(a))
     if status:
         _call(status, "qkv_attention")
     return out

@@ -20,7 +20,8 @@
  *     of 16 bytes.  Index arrays (int32) are device memory, 4-byte aligned.
  *   - Index values are device data and are not reported when invalid: the
  *     kernels check them and never access memory outside the given buffers.
- *   - The stream's device is made current for the call and restored after it.
+ *   - A stream's device is made current for the call and restored after it.  The
+ *     NULL stream is the current device's: that must be the pointers' device.
  */
 #ifndef QKV_H
 #define QKV_H

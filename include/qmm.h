@@ -52,7 +52,8 @@
  *     besides device properties it reads once per device (CU count, resident
  *     workgroups per kernel, cached with atomics), and is safe to call from
  *     several host threads.
- *   - stream: a hipStream_t passed as void* (NULL = the default stream).
+ *   - stream: a hipStream_t passed as void* (NULL = the default stream) of the
+ *     current device, which must be the pointers' device.
  *     Every call only enqueues work on that stream and never synchronizes
  *     (dotLLM "GPU Inference", Synchronization Model: one stream, all
  *     launches asynchronous).  Outputs are overwritten, never accumulated.
