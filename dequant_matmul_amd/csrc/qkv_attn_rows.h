@@ -408,18 +408,18 @@ hipError_t attn_blocks(const AttnArgs &a, const AttnPlan &p, int64_t batch, hipS
 {
     constexpr int PARTS = sizeof(IO) == 4 ? 2 : 1;
     const dim3 grid((unsigned)p.splits, (unsigned)(a.kv_heads * p.groups), (unsigned)batch);
+    hipError_t e = hipErrorInvalidValue;
     if (p.rows == 16)
-        hipLaunchKernelGGL((attn_kernel<NB, KT, PARTS, IO>), grid, dim3(64 * ATTN_WAVES), 0, s, a);
+        e = start((attn_kernel<NB, KT, PARTS, IO>), grid, dim3(64 * ATTN_WAVES), s, a);
     else if (p.rows == 64)
-        hipLaunchKernelGGL((attn_rows_kernel<NB, KT, 1, 4, PARTS, IO>), grid, dim3(256), 0, s, a);
+        e = start((attn_rows_kernel<NB, KT, 1, 4, PARTS, IO>), grid, dim3(256), s, a);
     else if constexpr (PARTS == 1 || NB <= 4) {
         if (p.rows == 128) {
-            hipLaunchKernelGGL((attn_rows_kernel<NB, KT, 1, 8, PARTS, IO>), grid, dim3(512), 0, s, a);
+            e = start((attn_rows_kernel<NB, KT, 1, 8, PARTS, IO>), grid, dim3(512), s, a);
         } else if constexpr (PARTS == 1 && NB <= 4) {
-            hipLaunchKernelGGL((attn_rows_kernel<NB, KT, 2, 8, PARTS, IO>), grid, dim3(512), 0, s, a);
+            e = start((attn_rows_kernel<NB, KT, 2, 8, PARTS, IO>), grid, dim3(512), s, a);
         }
     }
-    const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1)
         return e;
     constexpr int PER = 8 * NB, MOST = 256 / PER;
@@ -428,9 +428,8 @@ hipError_t attn_blocks(const AttnArgs &a, const AttnPlan &p, int64_t batch, hipS
         slices *= 2;
     const int here = MOST / slices;
     const int64_t rows = (int64_t)a.max_q * a.heads;
-    hipLaunchKernelGGL((attn_join_kernel<NB, IO>), dim3((unsigned)((rows + here - 1) / here), (unsigned)batch), dim3(256),
-                       0, s, a, slices);
-    return hipGetLastError();
+    return start((attn_join_kernel<NB, IO>), dim3((unsigned)((rows + here - 1) / here), (unsigned)batch), dim3(256),
+                 s, a, slices);
 }
 
 // One translation unit per cache type.

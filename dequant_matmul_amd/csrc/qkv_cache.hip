@@ -600,9 +600,8 @@ hipError_t launch_rope_angles(const int32_t *pos, int64_t tokens, const double *
                               float *cs, hipStream_t s)
 {
     const int64_t total = tokens * pairs, groups = (total + 255) / 256;
-    hipLaunchKernelGGL(angles_kernel, dim3((unsigned)(groups < (1 << 20) ? groups : (1 << 20))), dim3(256), 0, s, pos,
-                       total, freqs, (uint32_t)pairs, mag, (float2 *)cs);
-    return hipGetLastError();
+    return start(angles_kernel, dim3((unsigned)(groups < (1 << 20) ? groups : (1 << 20))), dim3(256), s, pos,
+                 total, freqs, (uint32_t)pairs, mag, (float2 *)cs);
 }
 
 template <typename I>
@@ -613,9 +612,8 @@ static hipError_t rope_of(const I *x, int64_t stride, int64_t tokens, int heads,
     const int units = twin ? dim / 8 - pairs / 8 : inter ? dim / 8 : dim - pairs;
     const int per = heads * units, tpb = per >= 256 ? 1 : 256 / per;
     const int64_t grid = (tokens + tpb - 1) / tpb;
-    hipLaunchKernelGGL(rope_kernel<I>, dim3((unsigned)grid), dim3(256), 0, s, x, stride, tokens, heads, dim, cs, pairs,
-                       inter, out, out_stride, tpb, units);
-    return hipGetLastError();
+    return start(rope_kernel<I>, dim3((unsigned)grid), dim3(256), s, x, stride, tokens, heads, dim, cs, pairs,
+                 inter, out, out_stride, tpb, units);
 }
 
 hipError_t launch_rope(int half, const void *x, int64_t stride, int64_t tokens, int heads, int dim, const float *cs,
@@ -634,13 +632,11 @@ static hipError_t append_of(const KvView &c, const void *k, int64_t ks, const vo
     const dim3 grid((unsigned)((tokens + WIN - 1) / WIN), (unsigned)c.kv_heads, 2);
     if constexpr (NB % 2 == 0)
         if (!inter && pairs == 16 * NB) {
-            hipLaunchKernelGGL((append_kernel<NB, KT, I, true>), grid, dim3(256), 0, s, c, (const I *)k, ks, (const I *)v,
-                               vs, tokens, slots, cs, pairs, inter);
-            return hipGetLastError();
+            return start((append_kernel<NB, KT, I, true>), grid, dim3(256), s, c, (const I *)k, ks, (const I *)v,
+                         vs, tokens, slots, cs, pairs, inter);
         }
-    hipLaunchKernelGGL((append_kernel<NB, KT, I, false>), grid, dim3(256), 0, s, c, (const I *)k, ks, (const I *)v, vs,
-                       tokens, slots, cs, pairs, inter);
-    return hipGetLastError();
+    return start((append_kernel<NB, KT, I, false>), grid, dim3(256), s, c, (const I *)k, ks, (const I *)v, vs,
+                 tokens, slots, cs, pairs, inter);
 }
 
 hipError_t launch_append(int kt, int half, const KvView &c, const void *k, int64_t ks, const void *v, int64_t vs,
@@ -660,10 +656,9 @@ static hipError_t read_rows(const KvView &c, const int32_t *slots, int64_t n, O 
 {
     for (int64_t i = 0; i < n; i += GRID_MOST * ROWS) {
         const int64_t m = n - i < GRID_MOST * ROWS ? n - i : GRID_MOST * ROWS, skip = i * c.kv_heads * c.head_dim;
-        hipLaunchKernelGGL((read_kernel<NB, KT, ROWS, O>), dim3((unsigned)c.kv_heads, (unsigned)((m + ROWS - 1) / ROWS), 2),
-                           dim3(256), 0, s, c, slots + i, m, k_out ? k_out + skip : nullptr,
-                           v_out ? v_out + skip : nullptr);
-        const hipError_t e = hipGetLastError();
+        const hipError_t e = start((read_kernel<NB, KT, ROWS, O>), dim3((unsigned)c.kv_heads, (unsigned)((m + ROWS - 1) / ROWS), 2),
+                                   dim3(256), s, c, slots + i, m, k_out ? k_out + skip : nullptr,
+                                   v_out ? v_out + skip : nullptr);
         if (e != hipSuccess)
             return e;
     }
@@ -699,9 +694,8 @@ hipError_t launch_move(int kt, const KvView &c, const int32_t *src, const int32_
             constexpr int KT = decltype(T)::value, NB = decltype(N)::value;
             for (int64_t g = 0; g < groups; g += GRID_MOST) {
                 const int64_t m = groups - g < GRID_MOST ? groups - g : GRID_MOST;
-                hipLaunchKernelGGL((move_kernel<NB, KT>), dim3((unsigned)c.kv_heads, (unsigned)m, 2), dim3(256), 0, s, c,
-                                   src + g * n, dst + g * n, n);
-                const hipError_t e = hipGetLastError();
+                const hipError_t e = start((move_kernel<NB, KT>), dim3((unsigned)c.kv_heads, (unsigned)m, 2), dim3(256), s, c,
+                                           src + g * n, dst + g * n, n);
                 if (e != hipSuccess)
                     return e;
             }

@@ -5,8 +5,6 @@
 
 #include "qmm_launch.h"
 
-#include <type_traits>
-
 namespace qmm {
 
 struct KvView;

@@ -220,15 +220,14 @@ hipError_t launch_any(int type, const void *w, int64_t n, int64_t k, size_t rb, 
     const uint8_t *wb = (const uint8_t *)w;
     const int64_t r = (int64_t)rb;
     switch (type) {
-    case T_Q4_0: hipLaunchKernelGGL((dequant_kernel<T_Q4_0, O, GATHER>), grid, block, 0, s, wb, n, k, r, ids, vocab, out); break;
-    case T_Q8_0: hipLaunchKernelGGL((dequant_kernel<T_Q8_0, O, GATHER>), grid, block, 0, s, wb, n, k, r, ids, vocab, out); break;
-    case T_Q4_K: hipLaunchKernelGGL((dequant_kernel<T_Q4_K, O, GATHER>), grid, block, 0, s, wb, n, k, r, ids, vocab, out); break;
-    case T_Q6_K: hipLaunchKernelGGL((dequant_kernel<T_Q6_K, O, GATHER>), grid, block, 0, s, wb, n, k, r, ids, vocab, out); break;
-    case T_Q5_0: hipLaunchKernelGGL((dequant_kernel<T_Q5_0, O, GATHER>), grid, block, 0, s, wb, n, k, r, ids, vocab, out); break;
-    case T_Q5_K: hipLaunchKernelGGL((dequant_kernel<T_Q5_K, O, GATHER>), grid, block, 0, s, wb, n, k, r, ids, vocab, out); break;
+    case T_Q4_0: return start((dequant_kernel<T_Q4_0, O, GATHER>), grid, block, s, wb, n, k, r, ids, vocab, out);
+    case T_Q8_0: return start((dequant_kernel<T_Q8_0, O, GATHER>), grid, block, s, wb, n, k, r, ids, vocab, out);
+    case T_Q4_K: return start((dequant_kernel<T_Q4_K, O, GATHER>), grid, block, s, wb, n, k, r, ids, vocab, out);
+    case T_Q6_K: return start((dequant_kernel<T_Q6_K, O, GATHER>), grid, block, s, wb, n, k, r, ids, vocab, out);
+    case T_Q5_0: return start((dequant_kernel<T_Q5_0, O, GATHER>), grid, block, s, wb, n, k, r, ids, vocab, out);
+    case T_Q5_K: return start((dequant_kernel<T_Q5_K, O, GATHER>), grid, block, s, wb, n, k, r, ids, vocab, out);
     default: return hipErrorInvalidValue;
     }
-    return hipGetLastError();
 }
 
 }  // namespace

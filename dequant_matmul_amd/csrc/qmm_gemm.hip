@@ -686,9 +686,8 @@ hipError_t launch_cfg(const uint8_t *w, int64_t n, int64_t k, size_t rb, const u
         if (e != hipSuccess)
             return e;
     }
-    hipLaunchKernelGGL((gemm_kernel<T, FM, FN, WM, WN, XD>), dim3((unsigned)(tiles * ksplit)), dim3(C::NT), 0, s, w,
-                       (int)n, (int)k, (int64_t)rb, x, (int)m, y, nnt, tiles, ksplit, remap);
-    return hipGetLastError();
+    return start((gemm_kernel<T, FM, FN, WM, WN, XD>), dim3((unsigned)(tiles * ksplit)), dim3(C::NT), s, w,
+                 (int)n, (int)k, (int64_t)rb, x, (int)m, y, nnt, tiles, ksplit, remap);
 }
 
 template <int T>
@@ -748,8 +747,7 @@ hipError_t launch_fill_zero(float *p, int64_t count, hipStream_t s)
 {
     if (count <= 0)
         return hipSuccess;
-    hipLaunchKernelGGL(fill_zero_kernel, dim3((unsigned)((count + 255) / 256)), dim3(256), 0, s, p, count);
-    return hipGetLastError();
+    return start(fill_zero_kernel, dim3((unsigned)((count + 255) / 256)), dim3(256), s, p, count);
 }
 
 }  // namespace qmm

@@ -714,10 +714,8 @@ static hipError_t launch_b1_xlds(const uint8_t *w, int64_t n, int64_t k, size_t 
     const int64_t want = ((n + R - 1) / R + NW - 1) / NW;
     const dim3 grid((unsigned)(want < cus ? want : cus)), block(64 * NW);
     if (n * (int64_t)rb >= NT_MIN_BYTES)
-        hipLaunchKernelGGL((gemv3_kernel<T, R, NW, true>), grid, block, 0, s, w, (int)n, (int)k, (int64_t)rb, x, y);
-    else
-        hipLaunchKernelGGL((gemv3_kernel<T, R, NW, false>), grid, block, 0, s, w, (int)n, (int)k, (int64_t)rb, x, y);
-    return hipGetLastError();
+        return start((gemv3_kernel<T, R, NW, true>), grid, block, s, w, (int)n, (int)k, (int64_t)rb, x, y);
+    return start((gemv3_kernel<T, R, NW, false>), grid, block, s, w, (int)n, (int)k, (int64_t)rb, x, y);
 }
 
 template <int T, int R>
@@ -731,8 +729,7 @@ static hipError_t launch_b1_table(const GemvProbs &P, int64_t k, size_t rb, hipS
     if (want == 0)
         return hipSuccess;
     const dim3 grid((unsigned)(want < cap ? want : cap)), block(256);
-    hipLaunchKernelGGL((gemv2m_kernel<T, R>), grid, block, 0, s, P, (int)k, (int64_t)rb);
-    return hipGetLastError();
+    return start((gemv2m_kernel<T, R>), grid, block, s, P, (int)k, (int64_t)rb);
 }
 
 // Shared-x table through gemv3m: at most one workgroup per CU.
@@ -746,8 +743,7 @@ static hipError_t launch_b1_table_xlds(const GemvProbs &P, int64_t k, size_t rb,
     if (want == 0)
         return hipSuccess;
     const dim3 grid((unsigned)(want < cus ? want : cus)), block(64 * NW);
-    hipLaunchKernelGGL((gemv3m_kernel<T, 1, NW>), grid, block, 0, s, P, (int)k, (int64_t)rb);
-    return hipGetLastError();
+    return start((gemv3m_kernel<T, 1, NW>), grid, block, s, P, (int)k, (int64_t)rb);
 }
 
 template <int UEK, int NW>
@@ -794,9 +790,8 @@ static hipError_t launch_stage_t(const StageGroups &G, int ng, const int *type, 
         types |= type[g] << (4 * g);
     for (int g = 1; g < ng; ++g)
         wb[g] = wb[g - 1] + cnt[g - 1];
-    hipLaunchKernelGGL((gemv3s_kernel<UEK, NW>), dim3((unsigned)grid), dim3(64 * NW), 0, s, x, (int)k, grid, wb[1],
-                       wb[2], types, G);
-    return hipGetLastError();
+    return start((gemv3s_kernel<UEK, NW>), dim3((unsigned)grid), dim3(64 * NW), s, x, (int)k, grid, wb[1],
+                 wb[2], types, G);
 }
 
 hipError_t launch_gemv_stage(int ng, const int *type, const int *np, const void *const *w, const int64_t *n,
@@ -849,8 +844,7 @@ static hipError_t launch_b1_lds_nt(const uint8_t *w, int64_t n, int64_t k, size_
         return hipErrorInvalidValue;
     const int64_t want = ((n + R - 1) / R + NW - 1) / NW;
     const dim3 grid((unsigned)(want < cap ? want : cap)), block(64 * NW);
-    hipLaunchKernelGGL((gemv1_kernel<T, R, NW, XK, D, NT>), grid, block, 0, s, w, (int)n, (int)k, (int64_t)rb, x, y);
-    return hipGetLastError();
+    return start((gemv1_kernel<T, R, NW, XK, D, NT>), grid, block, s, w, (int)n, (int)k, (int64_t)rb, x, y);
 }
 
 template <int T, int R, int NW, int XK, int D>
@@ -874,12 +868,10 @@ static hipError_t launch_b1_split(const uint8_t *w, int64_t n, int64_t k, size_t
     rwg = rwg < cap ? rwg : cap;
     const int64_t grid = (n + rwg - 1) / rwg;
     if (n * (int64_t)rb >= NT_MIN_BYTES)
-        hipLaunchKernelGGL((gemv4_kernel<T, NW, true>), dim3((unsigned)grid), dim3(64 * NW), 0, s, w, (int)n,
-                           (int)k, (int64_t)rb, x, y, (int)rwg, nseg);
-    else
-        hipLaunchKernelGGL((gemv4_kernel<T, NW, false>), dim3((unsigned)grid), dim3(64 * NW), 0, s, w, (int)n,
-                           (int)k, (int64_t)rb, x, y, (int)rwg, nseg);
-    return hipGetLastError();
+        return start((gemv4_kernel<T, NW, true>), dim3((unsigned)grid), dim3(64 * NW), s, w, (int)n,
+                     (int)k, (int64_t)rb, x, y, (int)rwg, nseg);
+    return start((gemv4_kernel<T, NW, false>), dim3((unsigned)grid), dim3(64 * NW), s, w, (int)n,
+                 (int)k, (int64_t)rb, x, y, (int)rwg, nseg);
 }
 
 template <int T, int B, int R>
@@ -888,10 +880,8 @@ static hipError_t launch_tbr(const uint8_t *w, int64_t n, int64_t k, size_t rb, 
 {
     const dim3 grid((unsigned)((n + 4 * R - 1) / (4 * R))), block(256);
     if (rb % 16 == 0)
-        hipLaunchKernelGGL((gemv_kernel<T, B, R, true>), grid, block, 0, s, w, (int)n, (int)k, (int64_t)rb, x, y);
-    else
-        hipLaunchKernelGGL((gemv_kernel<T, B, R, false>), grid, block, 0, s, w, (int)n, (int)k, (int64_t)rb, x, y);
-    return hipGetLastError();
+        return start((gemv_kernel<T, B, R, true>), grid, block, s, w, (int)n, (int)k, (int64_t)rb, x, y);
+    return start((gemv_kernel<T, B, R, false>), grid, block, s, w, (int)n, (int)k, (int64_t)rb, x, y);
 }
 
 template <int T>

@@ -850,13 +850,11 @@ hipError_t launch_b(const uint8_t *w, int64_t n, int64_t k, size_t rb, const flo
         P.n[0] = (int)n;
         P.tile0[1] = (int)ntiles;
         P.np = 1;
-        hipLaunchKernelGGL(gemvb1_kernel<T>, dim3(grid), dim3(64 * GB_W), 0, s, x, (int)k, (int64_t)rb, batch,
-                           (int)ntiles, grid, P);
-        return hipGetLastError();
+        return start(gemvb1_kernel<T>, dim3(grid), dim3(64 * GB_W), s, x, (int)k, (int64_t)rb, batch,
+                     (int)ntiles, grid, P);
     }
-    hipLaunchKernelGGL(gemvb_kernel<T>, dim3(grid), dim3(64 * GB_W), 0, s, w, (int)n, (int)k, (int64_t)rb, x,
-                       batch, y);
-    return hipGetLastError();
+    return start(gemvb_kernel<T>, dim3(grid), dim3(64 * GB_W), s, w, (int)n, (int)k, (int64_t)rb, x,
+                 batch, y);
 }
 
 // Problems of one type and k <= 4096 reading one x: one launch over all their
@@ -882,9 +880,8 @@ hipError_t launch_b_multi(int np, const void *const *w, const int64_t *n, int64_
         P.np = c;
         const int ntiles = P.tile0[c];
         const int grid = ntiles < cu_count_cached() ? ntiles : cu_count_cached();
-        hipLaunchKernelGGL(gemvb1_kernel<T>, dim3(grid), dim3(64 * GB_W), 0, s, x, (int)k, (int64_t)rb, batch,
-                           ntiles, grid, P);
-        const hipError_t e = hipGetLastError();
+        const hipError_t e = start(gemvb1_kernel<T>, dim3(grid), dim3(64 * GB_W), s, x, (int)k, (int64_t)rb, batch,
+                                   ntiles, grid, P);
         if (e != hipSuccess)
             return e;
     }

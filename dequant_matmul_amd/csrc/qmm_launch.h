@@ -10,8 +10,21 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <type_traits>
 
 namespace qmm {
+
+// Launch a kernel.  The status is this launch's own: hipGetLastError would report (and
+// clear) what an earlier, unrelated call of the thread has left as well.
+template <class... P>
+inline hipError_t start(void (*kernel)(P...), dim3 grid, dim3 block, hipStream_t s, std::common_type_t<P>... a)
+{
+    void *args[] = {(void *)&a...};
+    const hipError_t e = hipLaunchKernel((const void *)kernel, grid, block, args, 0, s);
+    if (e != hipSuccess)
+        (void)hipGetLastError();    // reported here, and only here
+    return e;
+}
 
 // A positive per-device value (a CU count, resident workgroups of a kernel)
 // computed on first use for the current device and cached in slot[device].

@@ -166,12 +166,10 @@ hipError_t launch_q(int type, const I *x, int64_t n, int64_t k, uint8_t *out, hi
     const int64_t groups = (nblk + QBLK - 1) / QBLK;
     const dim3 grid((unsigned)(groups < (1 << 20) ? groups : (1 << 20))), block(256);
     if (type == T_Q8_0)
-        hipLaunchKernelGGL((quantize_kernel<T_Q8_0, I>), grid, block, 0, s, x, nblk, out);
-    else if (type == T_Q4_0)
-        hipLaunchKernelGGL((quantize_kernel<T_Q4_0, I>), grid, block, 0, s, x, nblk, out);
-    else
-        return hipErrorInvalidValue;
-    return hipGetLastError();
+        return start((quantize_kernel<T_Q8_0, I>), grid, block, s, x, nblk, out);
+    if (type == T_Q4_0)
+        return start((quantize_kernel<T_Q4_0, I>), grid, block, s, x, nblk, out);
+    return hipErrorInvalidValue;
 }
 
 }  // namespace
