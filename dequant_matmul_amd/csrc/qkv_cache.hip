@@ -193,9 +193,10 @@ rope_kernel(const I *x, int64_t stride, int64_t tokens, int heads, int dim, cons
     }
 }
 
-// Items of one launch (gridDim.y ends at 65535); longer calls take several, since a
-// loop in the kernel costs the single token 0.7 us.
-constexpr int64_t GRID_MOST = 65535;
+// Workgroups of one launch in y (gridDim.y ends at 65535) and in x (a dimension ends at
+// 2^32 work-items); longer calls take several launches, since a loop in the kernel costs
+// the single token 0.7 us.
+constexpr int64_t GRID_MOST = 65535, GRID_X_MOST = 1 << 23;
 
 // ------------------------------------------------------------------ append --
 
@@ -611,9 +612,15 @@ static hipError_t rope_of(const I *x, int64_t stride, int64_t tokens, int heads,
     const bool twin = !inter && (pairs & 7) == 0;
     const int units = twin ? dim / 8 - pairs / 8 : inter ? dim / 8 : dim - pairs;
     const int per = heads * units, tpb = per >= 256 ? 1 : 256 / per;
-    const int64_t grid = (tokens + tpb - 1) / tpb;
-    return start(rope_kernel<I>, dim3((unsigned)grid), dim3(256), s, x, stride, tokens, heads, dim, cs, pairs,
-                 inter, out, out_stride, tpb, units);
+    for (int64_t t = 0; t < tokens; t += GRID_X_MOST * tpb) {
+        const int64_t m = tokens - t < GRID_X_MOST * tpb ? tokens - t : GRID_X_MOST * tpb;
+        const hipError_t e = start(rope_kernel<I>, dim3((unsigned)((m + tpb - 1) / tpb)), dim3(256), s, x + t * stride,
+                                   stride, m, heads, dim, cs + t * 2 * pairs, pairs, inter, out + t * out_stride,
+                                   out_stride, tpb, units);
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
 }
 
 hipError_t launch_rope(int half, const void *x, int64_t stride, int64_t tokens, int heads, int dim, const float *cs,
@@ -629,14 +636,19 @@ static hipError_t append_of(const KvView &c, const void *k, int64_t ks, const vo
                             const int32_t *slots, const float *cs, int pairs, int inter, hipStream_t s)
 {
     constexpr int WIN = 256 / (2 * NB);
-    const dim3 grid((unsigned)((tokens + WIN - 1) / WIN), (unsigned)c.kv_heads, 2);
+    auto kernel = append_kernel<NB, KT, I, false>;
     if constexpr (NB % 2 == 0)
-        if (!inter && pairs == 16 * NB) {
-            return start((append_kernel<NB, KT, I, true>), grid, dim3(256), s, c, (const I *)k, ks, (const I *)v,
-                         vs, tokens, slots, cs, pairs, inter);
-        }
-    return start((append_kernel<NB, KT, I, false>), grid, dim3(256), s, c, (const I *)k, ks, (const I *)v, vs,
-                 tokens, slots, cs, pairs, inter);
+        if (!inter && pairs == 16 * NB)
+            kernel = append_kernel<NB, KT, I, true>;
+    for (int64_t t = 0; t < tokens; t += GRID_X_MOST * WIN) {
+        const int64_t m = tokens - t < GRID_X_MOST * WIN ? tokens - t : GRID_X_MOST * WIN;
+        const dim3 grid((unsigned)((m + WIN - 1) / WIN), (unsigned)c.kv_heads, 2);
+        const hipError_t e = start(kernel, grid, dim3(256), s, c, (const I *)k + t * ks, ks, (const I *)v + t * vs, vs, m,
+                                   slots + t, cs ? cs + t * 2 * pairs : nullptr, pairs, inter);
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
 }
 
 hipError_t launch_append(int kt, int half, const KvView &c, const void *k, int64_t ks, const void *v, int64_t vs,

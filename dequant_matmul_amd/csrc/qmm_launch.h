@@ -19,6 +19,10 @@ namespace qmm {
 template <class... P>
 inline hipError_t start(void (*kernel)(P...), dim3 grid, dim3 block, hipStream_t s, std::common_type_t<P>... a)
 {
+    // the runtime takes a dimension of 2^32 work-items and more, and runs what is left of
+    // it modulo 2^32
+    if ((uint64_t)grid.x * block.x > 0xffffffffu)
+        return hipErrorInvalidConfiguration;
     void *args[] = {(void *)&a...};
     const hipError_t e = hipLaunchKernel((const void *)kernel, grid, block, args, 0, s);
     if (e != hipSuccess)
