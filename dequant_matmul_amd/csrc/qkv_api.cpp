@@ -207,7 +207,7 @@ int qkv_rope(int dtype, const void *x, int64_t stride, int64_t tokens, int64_t h
     if (!good_dtype(dtype))
         return QMM_ERR_TYPE;
     if (tokens < 0 || tokens > INT_MOST || heads < 0 || heads > 65536 || head_dim < 0 || head_dim > 65536 ||
-        head_dim % 8 != 0 || pairs < 0 || 2 * pairs > head_dim || heads * head_dim > (1 << 24))
+        head_dim % 8 != 0 || pairs < 0 || pairs > head_dim / 2 || heads * head_dim > (1 << 24))
         return QMM_ERR_SHAPE;
     if (tokens == 0 || heads == 0 || head_dim == 0)
         return QMM_OK;
@@ -246,7 +246,7 @@ int qkv_append(const qkv_cache *cache, int dtype, const void *k, int64_t k_strid
         return st;
     if (!good_dtype(dtype))
         return QMM_ERR_TYPE;
-    if (tokens < 0 || tokens > INT_MOST || pairs < 0 || 2 * pairs > c.head_dim)
+    if (tokens < 0 || tokens > INT_MOST || pairs < 0 || pairs > c.head_dim / 2)
         return QMM_ERR_SHAPE;
     if (tokens == 0 || c.pages == 0)
         return QMM_OK;
