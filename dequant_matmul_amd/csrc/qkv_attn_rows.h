@@ -25,7 +25,29 @@
 
 namespace qmm {
 
-constexpr int MODE_FP16_OVFL = 1 | 23 << 6;     // one bit, 23, of hardware register 1
+// fp16 results past the range saturate at 65504 between saturate<true> and
+// saturate<false> (bit 23 of the MODE register).  The compiler knows nothing of the mode:
+// what stays between them is held there by its data.  `order` comes out of the first, goes
+// with every operand (under) and every result (done), and into the second.
+template <bool ON>
+__device__ __forceinline__ void saturate(uint32_t &order)
+{
+    if constexpr (ON)
+        asm volatile("s_nop 1\n\ts_setreg_imm32_b32 hwreg(HW_REG_MODE, 23, 1), 1" : "+s"(order));
+    else
+        asm volatile("s_nop 1\n\ts_setreg_imm32_b32 hwreg(HW_REG_MODE, 23, 1), 0" : "+s"(order));
+}
+__device__ __forceinline__ uint32_t under(uint32_t x, uint32_t order)
+{
+    asm volatile("" : "+v"(x) : "s"(order));
+    return x;
+}
+__device__ __forceinline__ h16x8 done(h16x8 x, uint32_t &order)
+{
+    u32x4 y = __builtin_bit_cast(u32x4, x);
+    asm volatile("" : "+v"(y), "+s"(order));
+    return __builtin_bit_cast(h16x8, y);
+}
 
 template <int NB, int KT, int RT, int W, int PARTS, typename IO>
 __global__ void __launch_bounds__(64 * W, NB > 4 && W == 4 ? 1 : 2)
@@ -117,8 +139,9 @@ attn_rows_kernel(AttnArgs a)
         // decoded values saturate at 65504.  (For these alone: in this mode a weight that
         // is not a number would become one.)
         constexpr bool SATURATE = FOLDED && KT == KV_Q8;
+        uint32_t order = 0;
         if constexpr (SATURATE)
-            __builtin_amdgcn_s_setreg(MODE_FP16_OVFL, 1);
+            saturate<true>(order);
         const int64_t rest = nseen - (int64_t)tile * KV_TILE;
         const int left = (int)(rest < KV_TILE ? rest : KV_TILE) - 16 * h;
         const bool tail = tile >= clear;
@@ -129,8 +152,14 @@ attn_rows_kernel(AttnArgs a)
 #pragma unroll
                 for (int u = 0; u < L::G; ++u) {
                     h16x8 f = C::k(&kr[i][u * (L::UNIT / 4)]);
-                    if constexpr (FOLDED)
-                        f *= (h16x8)(as_h2(kd[i][SPAIR ? u >> 1 : u])[SPAIR ? u & 1 : 0]);
+                    if constexpr (FOLDED) {
+                        uint32_t d = kd[i][SPAIR ? u >> 1 : u];
+                        if constexpr (SATURATE)
+                            d = under(d, order);
+                        f *= (h16x8)(as_h2(d)[SPAIR ? u & 1 : 0]);
+                        if constexpr (SATURATE)
+                            f = done(f, order);
+                    }
                     kb[buf][j * L::G + u][lane] = f;
                 }
             }
@@ -149,13 +178,15 @@ attn_rows_kernel(AttnArgs a)
                         const uint32_t *d = &vd[i][4 * st];
                         h16x8 dv;
                         if constexpr (KT == KV_Q8)
-                            dv = as_h8(d[0], d[1], d[2], d[3]);
+                            dv = as_h8(under(d[0], order), under(d[1], order), under(d[2], order), under(d[3], order));
                         else
                             dv = as_h8(__builtin_amdgcn_perm(d[1], d[0], 0x05040100u),
                                        __builtin_amdgcn_perm(d[1], d[0], 0x07060302u),
                                        __builtin_amdgcn_perm(d[3], d[2], 0x05040100u),
                                        __builtin_amdgcn_perm(d[3], d[2], 0x07060302u));
                         x *= dv;
+                        if constexpr (SATURATE)
+                            x = done(x, order);
                     }
                     if (!SCALED && tail) {
                         u32x4 y = __builtin_bit_cast(u32x4, x);
@@ -172,7 +203,7 @@ attn_rows_kernel(AttnArgs a)
             }
         }
         if constexpr (SATURATE)
-            __builtin_amdgcn_s_setreg(MODE_FP16_OVFL, 0);
+            saturate<false>(order);
         if constexpr (SCALED) {
             // threads of one wave hold the V scales of a tile
             const int t = threadIdx.x;

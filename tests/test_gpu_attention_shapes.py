@@ -18,7 +18,7 @@ if not torch.cuda.is_available():
 
 import dequant_matmul_amd as q  # noqa: E402
 from graph_nodes import launched  # noqa: E402
-from test_gpu_attention_bars import judge  # noqa: E402
+from test_gpu_attention_bars import judge, put  # noqa: E402
 
 up, DEV = A.up, A.DEV
 F32, F16 = A.DTS
@@ -80,6 +80,33 @@ def test_rows_of_a_workgroup_of_wide_heads(dt, kvh, group, ctx, tq, rows, kind):
     got = run()
     assert shape(c, run, tq * group)[0] == rows
     judge(c, got, dt, 0, *sample(c, 0))
+
+
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("D", [64, 80, 128, 256])
+@pytest.mark.parametrize("rows,dt,kvh,group,ctx,tq", CALLS[:4])
+def test_the_largest_values_saturate(rows, dt, kvh, group, ctx, tq, D, which):
+    """Q8_0, decoded to fp16: 127 times the scale of a block whose largest value is 65504
+    is 65532, past the fp16 range.  As V of a token alike for all dims and of a weight
+    near 1 it comes out as 65504 (no rounding of a weight below 1 takes it higher), and
+    leaves no infinity in any row; as K it does not reach other tokens' scores."""
+    if D == 256 and rows == 256:
+        pytest.skip("no such shape: 128 rows at most")
+    c = A.Case("q8_0", list(ctx), list(tq), kvh, group, D, page=128, seed=7)
+    at = ctx[0] // 2
+    k, v = c.k[0].copy(), c.v[0].copy()
+    (k if which == "k" else v)[at] = np.sign((k if which == "k" else v)[at]) * 65504.0
+    if which == "v":
+        k[at] = 0
+    put(c, 0, k, v)
+    if which == "k":
+        c.q[c.starts[0]:c.starts[1]] *= 2.0 ** -6        # scores within a few thousand
+    run = ready(c, dt)
+    got = run()
+    assert shape(c, run, max(tq) * group)[0] == rows
+    assert torch.isfinite(got).all()
+    for b in range(len(ctx)):
+        judge(c, got, dt, b, *sample(c, b))
 
 
 def shared(kind, B, ctx, tq, kvh, group, D, dt, columns):
