@@ -439,13 +439,21 @@ __device__ __forceinline__ float lane_max(const f32x4 (&sc)[4])
     return mx;
 }
 
-// What lane_max is to rows that do not see every token, and to tiles of unlike V scales:
+// The largest score plus the tile's exponent of V scales.
+__device__ __forceinline__ float tile_top(const f32x4 (&sc)[4], float rs, float ev)
+{
+#pragma clang fp contract(off)      // the product as coarsen rounds it
+    return lane_max(sc) * rs + ev;
+}
+
+// What tile_top is to rows that do not see every token, and to tiles of unlike V scales:
 // the largest score plus the exponent of that token's own V scales (vs: fp16 in LDS, the
 // lane's 16 tokens of block 0; blocks are 32 dwords apart), so that the scale of a token
 // that a row does not see, or gives no weight, has no part in the row's reference.
 template <int NB>
 __device__ __forceinline__ float masked_top(const f32x4 (&sc)[4], float rs, const uint32_t *vs)
 {
+#pragma clang fp contract(off)      // the product as coarsen rounds it
     typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
     float mx = -INFINITY;
 #pragma unroll
@@ -456,24 +464,55 @@ __device__ __forceinline__ float masked_top(const f32x4 (&sc)[4], float rs, cons
             big = __builtin_elementwise_max(big, __builtin_bit_cast(u16x2, vs[32 * bl + i] & 0x7fff7fffu));
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-            mx = fmaxf(mx, fmaf(sc[i >> 1][2 * (i & 1) + j], rs, (float)((int)(big[j] >> 10) - 14)));
+            mx = fmaxf(mx, sc[i >> 1][2 * (i & 1) + j] * rs + (float)((int)(big[j] >> 10) - 14));
     }
     return mx;
 }
 
+// Past this size of score the steps of m and of shift, and the reference's own rounding,
+// come near the range that fp16 leaves above P_TOP (at 2^27 they would pass it:
+// infinities and NaN from finite scores).
+constexpr float SCORES_FINE = 1048576.f;
+__device__ __forceinline__ bool past_fine(float shift) { return fabsf(shift) > SCORES_FINE; }
+
 // Raise a row tile's reference m to its maximum, top (per lane: largest score
-// plus exponent of the V scales); l and o follow.  shift = P_TOP - m.
+// plus exponent of the V scales), where that passes `bar`; l and o follow.  shift =
+// P_TOP - m, bar = m + P_SLACK, or anything at all where every tile has to come here
+// (coarsen).
 template <int NB>
-__device__ __forceinline__ void raise(float top, float &m, float &shift, float &l, f32x4 (&o)[2 * NB])
+__device__ __forceinline__ void raise(float top, float &m, float &shift, float &bar, float &l, f32x4 (&o)[2 * NB])
 {
-    const float mn = fmaxf(m, rows_max(top)), mu = mn == -INFINITY ? 0.f : mn;
+    const float most = rows_max(top), mn = most > bar ? fmaxf(m, most) : m, mu = mn == -INFINITY ? 0.f : mn;
     const float alpha = __builtin_amdgcn_exp2f(m - mu);
     m = mn;
     shift = P_TOP - mu;
+    bar = past_fine(shift) ? -INFINITY : m + P_SLACK;
     l *= alpha;
 #pragma unroll
     for (int t = 0; t < 2 * NB; ++t)
         o[t] *= alpha;
+}
+
+// Rows past SCORES_FINE: the weights' exponents in place of the scores (to be scaled by
+// r = 1 and shifted by t = 0).  The product is rounded as the reference's was (tile_top) and
+// subtracted from it, which is exact near the largest, and what an absorbed exponent of
+// V (ev) adds is cut off.  Other rows of the wave keep theirs: no row's bits depend on
+// another's scores.
+__device__ __forceinline__ void coarsen(f32x4 (&sc)[4], float rs, float m, float shift, float ev, float &r, float &t)
+{
+#pragma clang fp contract(off)
+    const bool here = past_fine(shift);
+    const float most = P_TOP + P_SLACK - ev;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float x = (sc[c][i] * rs - m) + P_TOP;
+            x = x > most ? most : x;                // (not a number stays one)
+            sc[c][i] = here ? x : sc[c][i];
+        }
+    r = here ? 1.f : r;
+    t = here ? 0.f : t;
 }
 
 // Scores to weights, in place.
@@ -590,7 +629,7 @@ attn_kernel(AttnArgs a)
     const int tok = r0 + n < rows ? (r0 + n) / a.group : -1;
 
     f32x4 o[2 * NB];
-    float m = -INFINITY, shift = P_TOP, l = 0.f;
+    float m = -INFINITY, shift = P_TOP, bar = -INFINITY, l = 0.f;
 #pragma unroll
     for (int t = 0; t < 2 * NB; ++t)
         o[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
@@ -790,10 +829,15 @@ attn_kernel(AttnArgs a)
         if (SCALED && (tail || unlike))
             top = masked_top<NB>(sc, rs, &scales[wave][32 * NB + 8 * h]);
         else
-            top = fmaf(lane_max(sc), rs, ev);
-        if (__any(top > m + P_SLACK))
-            raise<NB>(top, m, shift, l, o);
-        soften(sc, rs, shift);
+            top = tile_top(sc, rs, ev);
+        float r = rs, t = shift;
+        if (__any(top > bar)) {
+            raise<NB>(top, m, shift, bar, l, o);
+            t = shift;
+            if (__builtin_expect(__any(past_fine(shift)), 0))
+                coarsen(sc, rs, m, shift, ev, r, t);
+        }
+        soften(sc, r, t);
         l += sum16(sc);
         __builtin_amdgcn_sched_barrier(0);
 

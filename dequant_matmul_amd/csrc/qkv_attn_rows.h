@@ -234,7 +234,7 @@ attn_rows_kernel(AttnArgs a)
     // wave
     bool live = t_begin < t_end && load_tile(t_begin);
     h16x8 qf[RT][PARTS][NB];
-    float rs[RT], m[RT], shift[RT], l[RT];
+    float rs[RT], m[RT], shift[RT], bar[RT], l[RT];
     int tok[RT];
     f32x4 o[RT][2 * NB];
 #pragma unroll
@@ -244,6 +244,7 @@ attn_rows_kernel(AttnArgs a)
         tok[rt] = r < rows ? r / a.group : -1;
         m[rt] = -INFINITY;
         shift[rt] = P_TOP;
+        bar[rt] = -INFINITY;
         l[rt] = 0.f;
 #pragma unroll
         for (int t = 0; t < 2 * NB; ++t)
@@ -336,24 +337,32 @@ attn_rows_kernel(AttnArgs a)
             ev = exponent[buf];
             apart = tail || __builtin_amdgcn_readfirstlane(unlike[buf]) != 0;
         }
-        float top[RT];
+        float top[RT], r[RT], t[RT];
         bool more = false;
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
             if (SCALED && apart)
                 top[rt] = masked_top<NB>(sc[rt], rs[rt], &vscale[buf][8 * h]);
             else
-                top[rt] = fmaf(lane_max(sc[rt]), rs[rt], ev);
-            more |= top[rt] > m[rt] + P_SLACK;
+                top[rt] = tile_top(sc[rt], rs[rt], ev);
+            more |= top[rt] > bar[rt];
+            r[rt] = rs[rt];
+            t[rt] = shift[rt];
         }
         if (__any(more)) {
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt)
-                raise<NB>(top[rt], m[rt], shift[rt], l[rt], o[rt]);
+                raise<NB>(top[rt], m[rt], shift[rt], bar[rt], l[rt], o[rt]);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                t[rt] = shift[rt];
+                if (__builtin_expect(__any(past_fine(shift[rt])), 0))
+                    coarsen(sc[rt], rs[rt], m[rt], shift[rt], ev, r[rt], t[rt]);
+            }
         }
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-            soften(sc[rt], rs[rt], shift[rt]);
+            soften(sc[rt], r[rt], t[rt]);
             if constexpr (PARTS == 2)
                 l[rt] += sum16(sc[rt]);
         }

@@ -127,3 +127,35 @@ def test_sharp_and_flat_softmax(kind, tq, spread, dt):
         pytest.skip("K rounded to fp16 moves scores of 20000 by 10: no bar on the weights")
     c = A.Case(kind, [700], [tq], 2, 4, 128, seed=3, spread=spread, vscale=20.0)
     judge(c, c.run(dt), dt)
+
+
+@pytest.mark.parametrize("dt,lift", [(torch.float32, n) for n in list(range(0, 27)) + [30, 60, 100]] +
+                         [(torch.float16, n) for n in range(0, 25)])
+@pytest.mark.parametrize("kind", A.KINDS)
+@pytest.mark.parametrize("tq", [1, 40])
+def test_scores_past_the_whole_numbers(kind, tq, dt, lift):
+    """Scores of any finite size, whose steps in fp32 are wider than the softmax's unit: one
+    token takes a row, or two of equal keys share it.  Keys are a_j in every dim, a_j whole;
+    the next lower a_j is 2% lower, a score error 2^-19 of it."""
+    D, n = 128, 200 + tq
+    c = A.Case(kind, [200], [tq], 2, 4, D, seed=70)
+    rng = np.random.default_rng(71)
+    a = rng.integers(1, 62, n).astype(np.float64)
+    a[[40, 130, 150]] = 64, 63, 64          # in the first and the third tile
+    a[200:] = 1
+    high = max(0, lift - 15) if dt == torch.float16 else 0       # q ends at 2^15: the rest is K's
+    k = np.repeat(a[:, None, None], 2, 1) * np.ones(D) * 2.0 ** high
+    v = rng.standard_normal((n, 2, D))
+    c.q[:] = 2.0 ** (lift - high)
+    c.q[::2, ::2] *= -1                      # there the lowest keys win
+    put(c, 0, k, v)
+    got = c.run(dt).cpu().numpy().astype(np.float64)
+    for r in range(tq):
+        for h in range(c.q.shape[1]):
+            s = c.k[0][:201 + r, h // 4, 0] * np.sign(c.q[r, h, 0])
+            hit = np.flatnonzero(s > s.max() - 0.2 * 2.0 ** high)
+            if lift == 0 and s.max() < 0:
+                continue                     # scores a few units apart: the usual bars' case
+            x = c.v[0][hit, h // 4]
+            tol = (2.0 ** -9 if dt == torch.float16 else 2.0 ** -18) * np.abs(x).mean(0) + (1e-4 if lift == 0 else 2.0 ** -24)
+            assert np.all(np.abs(got[r, h] - x.mean(0)) <= tol), (r, h, len(hit))
