@@ -13,7 +13,7 @@
  * Conventions are those of qmm.h (device pointers owned by the caller, every
  * call only enqueues on the stream, argument errors return before anything is
  * enqueued, status codes qmm_status, empty problems are QMM_OK), and:
- *   - Activations (x, q, k, v, out) are QKV_F32 or QKV_F16 (IEEE fp16 bits),
+ *   - Activations (x, q, k, v, out) are QKV_F32 or QKV_HALF (IEEE fp16 bits),
  *     [tokens][heads][head_dim]: the heads of a token are contiguous, tokens
  *     are `stride` elements apart (so that q, k and v may be views of one
  *     projection output).  Pointers are 16-byte aligned and strides multiples
