@@ -285,7 +285,8 @@ def _sizes(cache, q, table, ctx, qstart, mask, max_q, max_ctx):
 
 def attention_workspace(cache, q, table, max_q=None, max_ctx=None, qstart=None):
     """A workspace tensor for attention() calls of these sizes (one call at a
-    time may use it)."""
+    time may use it).  Fewer sequences or rows may need more: one kept for several
+    batches is the largest of theirs."""
     a = _sizes(cache, q, table, None, qstart, None, max_q, max_ctx)
     with torch.cuda.device(cache.device):
         n = lib.qkv_attn_workspace(cache.ptr, ctypes.addressof(a))

@@ -186,6 +186,10 @@ QMM_API int qkv_move(const qkv_cache *cache, const int32_t *src, const int32_t *
  * A new token whose rows were not appended (padding) has no effect on rows that
  * do not see it, whatever bits its slot holds; those that do see it are undefined.
  *
+ * Rows are taken in groups of 16 to 256 (max_q * heads / kv_heads of them a kv
+ * head); groups times kv_heads may not pass 65535, which is about 4 million rows of q or
+ * more: QMM_ERR_SHAPE.
+ *
  * max_q and max_ctx bound the new tokens of any sequence and the tokens
  * (committed and new) of any sequence; they size the launch and the workspace,
  * so a captured call serves any lengths below them.  New tokens past max_q get
@@ -225,9 +229,15 @@ typedef struct qkv_attn {
     int32_t reserved;     /* 0 */
 } qkv_attn;
 
-/* Bytes of workspace that a call with these sizes needs (0 possible; pointers,
+/*
+ * Bytes of workspace that a call with these sizes needs (0 possible; pointers,
  * scale and workspace fields are not looked at); -1 for invalid sizes.  It
- * depends on the device's number of compute units. */
+ * depends on the device's number of compute units, and does not grow with every
+ * size: fewer sequences or rows are cut into more parts and may need more (32/8
+ * heads of 128, long contexts, single tokens: 16 sequences 1064960 bytes, 7
+ * 1164800, 64 none).  A workspace kept for calls of several sizes has the largest
+ * of theirs.
+ */
 QMM_API int64_t qkv_attn_workspace(const qkv_cache *cache, const qkv_attn *a);
 
 QMM_API int qkv_attention(const qkv_cache *cache, const qkv_attn *a, void *stream);

@@ -190,3 +190,33 @@ def test_first_rows_outside_q(starts, max_q, dt):
             judge(c, got, dt, b, rows=[0])
     assert (got[up(free)] == 7).all() and not (got[up(~free)] == 7).any()
     assert (memory[:3] == 7).all() and (memory[3 + T:] == 7).all()
+
+
+@pytest.mark.parametrize("dt", A.DTS)
+def test_the_most_sequences(dt):
+    """65535 sequences of one token, all over the same two pages."""
+    B, kvh, group, D = 65535, 1, 2, 64
+    c = A.Case("q8_0", [69], [1], kvh, group, D, seed=80)
+    rows = np.random.default_rng(81).standard_normal((B, kvh * group, D)).astype(np.float32)
+    got = q.attention(c.cache, up(rows).to(dt), up(c.table).expand(B, -1).contiguous(),
+                      torch.full((B,), 69, dtype=torch.int32, device=DEV), max_ctx=70)
+    for b in (0, 1, 32767, 32768, 65534):
+        c.q = rows[b:b + 1]
+        judge(c, got[b:b + 1], dt)
+
+
+@pytest.mark.parametrize("dt", A.DTS)
+def test_the_most_row_groups(dt):
+    """1024 kv heads with so many rows each that the groups of them fill a dimension of
+    the launch; twice as many are refused."""
+    kvh, D = 1024, 8
+    tq = 4032
+    c = A.Case("f16", [0], [tq], kvh, 1, D, seed=82)
+    run = ready(c, dt)
+    got = run()
+    assert launched(run)[0][1][1] > 65535 // 2 or dt == F16
+    rows = np.array([0, 1, 63, 64, 2000, 4031])
+    judge(c, got, dt, rows=rows, heads=[0, 511, 1023])
+    x = torch.zeros(17 * tq, kvh, D, dtype=dt, device=DEV)
+    with pytest.raises((ValueError, q.QmmError)):
+        q.attention(c.cache, x, up(c.table), up(np.array([0], np.int32)), max_ctx=64 * c.cols)
