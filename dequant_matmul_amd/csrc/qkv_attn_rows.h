@@ -27,25 +27,30 @@ namespace qmm {
 
 // fp16 results past the range saturate at 65504 between saturate<true> and
 // saturate<false> (bit 23 of the MODE register).  The compiler knows nothing of the mode:
-// what stays between them is held there by its data.  `order` comes out of the first, goes
-// with every operand (under) and every result (done), and into the second.
-template <bool ON>
-__device__ __forceinline__ void saturate(uint32_t &order)
+// what stays between them is held there by its data, and what stays outside as well.
+// `order` comes out of the first, goes with every operand (under) and every result (done),
+// and into the second; the first waits for x, the second lets x through: one value a row
+// tile that all fp16 work before (after) it leads to (comes from).  (As volatile asm under
+// and done would keep their own order too: 2% of a chunk.)
+template <bool ON, int RT>
+__device__ __forceinline__ void saturate(uint32_t &order, float (&x)[RT])
 {
-    if constexpr (ON)
-        asm volatile("s_nop 1\n\ts_setreg_imm32_b32 hwreg(HW_REG_MODE, 23, 1), 1" : "+s"(order));
-    else
-        asm volatile("s_nop 1\n\ts_setreg_imm32_b32 hwreg(HW_REG_MODE, 23, 1), 0" : "+s"(order));
+    static_assert(RT == 1 || RT == 2, "");
+    if constexpr (RT == 2)
+        asm("" : "+v"(x[0]), "+v"(x[1]));       // x[0] waits for x[1], x[1] comes with x[0]
+    asm volatile("s_nop 1\n\ts_setreg_imm32_b32 hwreg(HW_REG_MODE, 23, 1), %2" : "+s"(order), "+v"(x[0]) : "n"(ON));
+    if constexpr (RT == 2)
+        asm("" : "+v"(x[0]), "+v"(x[1]));
 }
 __device__ __forceinline__ uint32_t under(uint32_t x, uint32_t order)
 {
-    asm volatile("" : "+v"(x) : "s"(order));
+    asm("" : "+v"(x) : "s"(order));
     return x;
 }
 __device__ __forceinline__ h16x8 done(h16x8 x, uint32_t &order)
 {
     u32x4 y = __builtin_bit_cast(u32x4, x);
-    asm volatile("" : "+v"(y), "+s"(order));
+    asm("" : "+v"(y), "+s"(order));
     return __builtin_bit_cast(h16x8, y);
 }
 
@@ -132,6 +137,12 @@ attn_rows_kernel(AttnArgs a)
         return true;
     };
 
+    // ---- this wave's rows
+    h16x8 qf[RT][PARTS][NB];
+    float rs[RT], m[RT], shift[RT], bar[RT], l[RT];
+    int tok[RT];
+    f32x4 o[RT][2 * NB];
+
     // what lies behind the last token, and at new ones never appended, may be any
     // bits: V (or its scale) becomes 0, or at least finite
     auto store_tile = [&](int buf, int tile) {
@@ -141,7 +152,7 @@ attn_rows_kernel(AttnArgs a)
         constexpr bool SATURATE = FOLDED && KT == KV_Q8;
         uint32_t order = 0;
         if constexpr (SATURATE)
-            saturate<true>(order);
+            saturate<true>(order, l);          // sums of the weights as they are rounded
         const int64_t rest = nseen - (int64_t)tile * KV_TILE;
         const int left = (int)(rest < KV_TILE ? rest : KV_TILE) - 16 * h;
         const bool tail = tile >= clear;
@@ -203,7 +214,7 @@ attn_rows_kernel(AttnArgs a)
             }
         }
         if constexpr (SATURATE)
-            saturate<false>(order);
+            saturate<false>(order, shift);     // what every later weight is made with
         if constexpr (SCALED) {
             // threads of one wave hold the V scales of a tile
             const int t = threadIdx.x;
@@ -233,10 +244,6 @@ attn_rows_kernel(AttnArgs a)
     // ---- the first tile is loaded, then this wave's rows; `live` is the same in every
     // wave
     bool live = t_begin < t_end && load_tile(t_begin);
-    h16x8 qf[RT][PARTS][NB];
-    float rs[RT], m[RT], shift[RT], bar[RT], l[RT];
-    int tok[RT];
-    f32x4 o[RT][2 * NB];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
         const int r = r0 + 16 * rt + n;
