@@ -476,29 +476,30 @@ constexpr float SCORES_FINE = 1048576.f;
 __device__ __forceinline__ bool past_fine(float shift) { return fabsf(shift) > SCORES_FINE; }
 
 // Raise a row tile's reference m to its maximum, top (per lane: largest score
-// plus exponent of the V scales), where that passes `bar`; l and o follow.  shift =
-// P_TOP - m, bar = m + P_SLACK, or anything at all where every tile has to come here
-// (coarsen).
+// plus exponent of the V scales), where that passes `bar`; l and o follow.  bar = m +
+// P_SLACK, or anything at all where every tile has to come here (coarsen).  Returns what
+// is added to the scores: P_TOP - m.
 template <int NB>
-__device__ __forceinline__ void raise(float top, float &m, float &shift, float &bar, float &l, f32x4 (&o)[2 * NB])
+__device__ __forceinline__ float raise(float top, float &m, float &bar, float &l, f32x4 (&o)[2 * NB])
 {
     const float most = rows_max(top), mn = most > bar ? fmaxf(m, most) : m, mu = mn == -INFINITY ? 0.f : mn;
     const float alpha = __builtin_amdgcn_exp2f(m - mu);
+    const float shift = P_TOP - mu;
     m = mn;
-    shift = P_TOP - mu;
     bar = past_fine(shift) ? -INFINITY : m + P_SLACK;
     l *= alpha;
 #pragma unroll
     for (int t = 0; t < 2 * NB; ++t)
         o[t] *= alpha;
+    return shift;
 }
 
-// Rows past SCORES_FINE: the weights' exponents in place of the scores (to be scaled by
-// r = 1 and shifted by t = 0).  The product is rounded as the reference's was (tile_top) and
+// Rows past SCORES_FINE: the weights' exponents in place of the scores, to be scaled by 1
+// and shifted by 0 (mul and shift: their own otherwise).  The product is rounded as the reference's was (tile_top) and
 // subtracted from it, which is exact near the largest, and what an absorbed exponent of
 // V (ev) adds is cut off.  Other rows of the wave keep theirs: no row's bits depend on
 // another's scores.
-__device__ __forceinline__ void coarsen(f32x4 (&sc)[4], float rs, float m, float shift, float ev, float &r, float &t)
+__device__ __forceinline__ void coarsen(f32x4 (&sc)[4], float rs, float m, float ev, float &mul, float &shift)
 {
 #pragma clang fp contract(off)
     const bool here = past_fine(shift);
@@ -511,18 +512,18 @@ __device__ __forceinline__ void coarsen(f32x4 (&sc)[4], float rs, float m, float
             x = x > most ? most : x;                // (not a number stays one)
             sc[c][i] = here ? x : sc[c][i];
         }
-    r = here ? 1.f : r;
-    t = here ? 0.f : t;
+    mul = here ? 1.f : mul;
+    shift = here ? 0.f : shift;
 }
 
 // Scores to weights, in place.
-__device__ __forceinline__ void soften(f32x4 (&sc)[4], float rs, float shift)
+__device__ __forceinline__ void soften(f32x4 (&sc)[4], float mul, float shift)
 {
 #pragma unroll
     for (int c = 0; c < 4; ++c)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            sc[c][i] = __builtin_amdgcn_exp2f(fmaf(sc[c][i], rs, shift));
+            sc[c][i] = __builtin_amdgcn_exp2f(fmaf(sc[c][i], mul, shift));
 }
 
 __device__ __forceinline__ float sum16(const f32x4 (&sc)[4])
@@ -629,7 +630,7 @@ attn_kernel(AttnArgs a)
     const int tok = r0 + n < rows ? (r0 + n) / a.group : -1;
 
     f32x4 o[2 * NB];
-    float m = -INFINITY, shift = P_TOP, bar = -INFINITY, l = 0.f;
+    float m = -INFINITY, mul = rs, shift = P_TOP, bar = -INFINITY, l = 0.f;
 #pragma unroll
     for (int t = 0; t < 2 * NB; ++t)
         o[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
@@ -830,14 +831,13 @@ attn_kernel(AttnArgs a)
             top = masked_top<NB>(sc, rs, &scales[wave][32 * NB + 8 * h]);
         else
             top = tile_top(sc, rs, ev);
-        float r = rs, t = shift;
         if (__any(top > bar)) {
-            raise<NB>(top, m, shift, bar, l, o);
-            t = shift;
+            shift = raise<NB>(top, m, bar, l, o);
+            mul = rs;
             if (__builtin_expect(__any(past_fine(shift)), 0))
-                coarsen(sc, rs, m, shift, ev, r, t);
+                coarsen(sc, rs, m, ev, mul, shift);
         }
-        soften(sc, r, t);
+        soften(sc, mul, shift);
         l += sum16(sc);
         __builtin_amdgcn_sched_barrier(0);
 

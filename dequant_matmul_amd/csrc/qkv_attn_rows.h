@@ -139,7 +139,7 @@ attn_rows_kernel(AttnArgs a)
 
     // ---- this wave's rows
     h16x8 qf[RT][PARTS][NB];
-    float rs[RT], m[RT], shift[RT], bar[RT], l[RT];
+    float rs[RT], m[RT], mul[RT], shift[RT], bar[RT], l[RT];
     int tok[RT];
     f32x4 o[RT][2 * NB];
 
@@ -250,6 +250,7 @@ attn_rows_kernel(AttnArgs a)
         rs[rt] = load_row<NB, KT, PARTS, IO>(a, s, head, r, rows, h, qf[rt]);
         tok[rt] = r < rows ? r / a.group : -1;
         m[rt] = -INFINITY;
+        mul[rt] = rs[rt];
         shift[rt] = P_TOP;
         bar[rt] = -INFINITY;
         l[rt] = 0.f;
@@ -344,7 +345,7 @@ attn_rows_kernel(AttnArgs a)
             ev = exponent[buf];
             apart = tail || __builtin_amdgcn_readfirstlane(unlike[buf]) != 0;
         }
-        float top[RT], r[RT], t[RT];
+        float top[RT];
         bool more = false;
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
@@ -353,23 +354,21 @@ attn_rows_kernel(AttnArgs a)
             else
                 top[rt] = tile_top(sc[rt], rs[rt], ev);
             more |= top[rt] > bar[rt];
-            r[rt] = rs[rt];
-            t[rt] = shift[rt];
         }
         if (__any(more)) {
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt)
-                raise<NB>(top[rt], m[rt], shift[rt], bar[rt], l[rt], o[rt]);
+                shift[rt] = raise<NB>(top[rt], m[rt], bar[rt], l[rt], o[rt]);
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
-                t[rt] = shift[rt];
+                mul[rt] = rs[rt];
                 if (__builtin_expect(__any(past_fine(shift[rt])), 0))
-                    coarsen(sc[rt], rs[rt], m[rt], shift[rt], ev, r[rt], t[rt]);
+                    coarsen(sc[rt], rs[rt], m[rt], ev, mul[rt], shift[rt]);
             }
         }
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-            soften(sc[rt], r[rt], t[rt]);
+            soften(sc[rt], mul[rt], shift[rt]);
             if constexpr (PARTS == 2)
                 l[rt] += sum16(sc[rt]);
         }
