@@ -18,11 +18,11 @@
 //
 // Bound: HBM for long or many sequences, a wave's instructions (two per pair of
 // codes, whatever the number of rows) for short ones.  Whole calls, replayed:
-//   1 token at 32000, 32/8 heads of 128: Q8_0 fp32 20.3 us (3.4 TB/s of cache, 4 us
-//     of it the join), Q4_0 fp16 16.8, F16 fp16 27.9 (4.7 TB/s)
-//   16 tokens at 8000, fp16: Q4_0 35 us (4.2 TB/s), Q8_0 58 (4.8), F16 97 (5.4)
-//   64 tokens at 4000, 32 kv heads, Q8_0: 375 us (5.9 TB/s)
-//   1 token at 300, 32/4 heads of 64, F16, fp32: 5.4 us
+//   1 token at 32000, 32/8 heads of 128: Q8_0 fp32 20.7 us (3.4 TB/s of cache, 4 us
+//     of it the join), Q4_0 fp16 17.2, F16 fp16 27.9 (4.7 TB/s)
+//   16 tokens at 8000, fp16: Q4_0 35 us (4.2 TB/s), Q8_0 59 (4.7), F16 98 (5.4)
+//   64 tokens at 4000, 32 kv heads, Q8_0: 385 us (5.8 TB/s)
+//   1 token at 300, 32/4 heads of 64, F16, fp32: 5.5 us
 #pragma once
 
 #include "qkv_layout.h"

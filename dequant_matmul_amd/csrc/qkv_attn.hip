@@ -17,9 +17,12 @@ namespace qmm {
 // layer with 128-wide heads, in us: a tile's time for a workgroup of `rows` rows
 // alone on a CU (it hardly depends on how many rows its waves hold as long as they
 // do not share a CU), and the join's fixed part and traffic.  Chunk of 512 at 7680
-// tokens, fp16: 256 rows in 4 splits 87 us (model 91), 128 in 2 107 (104), 64 in 2 131
-// (128); at an empty cache: 64 rows whole 17 us, 128 18, 256 25; tree of 29 in 4
-// sequences, fp32: 128 rows in 8 splits 37.9, 64 in 8 37.0, 128 in 4 55.
+// tokens, fp16: 256 rows in 4 splits 87 us (model 86), 128 in 2 107 (99), 64 in 2 131
+// (117); at an empty cache: 64 rows whole 17 us, 128 18, 256 25; tree of 29 in 4
+// sequences, fp32: 128 rows in 8 splits 37.9 (34, so taken), 64 in 8 37.0 (38), 128 in
+// 4 55 (54).  Other head widths are scaled by their blocks, and not measured: a
+// workgroup of 64 rows of 256 dims has a CU to itself, not half of one, and two of
+// 128 rows of up to 96 dims would fit a CU.
 AttnPlan attn_plan(const KvView &c, int64_t tokens, int64_t batch, int heads, int half, int64_t max_q, int64_t max_ctx)
 {
     AttnPlan p;

@@ -15,10 +15,10 @@
 // Bound: the VALU's part (softmax, scales, decoding) and the matrix cores' in turn:
 // instructions of two waves of a SIMD hardly overlap.  Whole calls, replayed, 32/8
 // heads of 128:
-//   512 tokens at 7680: fp16 84 us from Q4_0 (790 TFLOP/s), 84 to 89 from Q8_0 and
-//     F16; fp32 from Q8_0 185
-//   8192 tokens at 0, F16 cache, fp16: 600 us (916 TFLOP/s)
-//   trees of 29 in 4 sequences at 4000, Q8_0: fp32 37 us, fp16 26
+//   512 tokens at 7680: fp16 83 us from Q4_0 (805 TFLOP/s), 86 to 90 from Q8_0 and
+//     F16; fp32 from Q8_0 189
+//   8192 tokens at 0, F16 cache, fp16: 610 us (900 TFLOP/s)
+//   trees of 29 in 4 sequences at 4000, Q8_0: fp32 38 us, fp16 26.6
 #pragma once
 
 #include "qkv_attn.h"

@@ -392,35 +392,35 @@ __device__ __forceinline__ void read_k(const KvView &c, int head, int dim, const
 {
     using L = KvLay<NB, KT>;
     constexpr int U = 4 * NB;
-            for (int it = threadIdx.x; it < ROWS * U; it += 256) {
-                const int64_t i = i0 + it / U;
-                const int u = it % U, b = u >> 2;
-                if (i >= n || 8 * u >= dim)
-                    continue;
-                float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                int64_t tile;
-                int key;
-                if (slot_at<L>(c, slots[i], head, tile, key)) {
-                    const uint8_t *unit = c.k + tile + L::k_unit(key, b, u & 3);
-                    if constexpr (KT == KV_F16) {
-                        load8((const _Float16 *)unit, x);
-                    } else {
-                        const float d = h2f(*(const uint16_t *)(c.k + tile + L::k_scale(key, b)));
-                        if constexpr (KT == KV_Q8) {
-                            const uint2 w = *(const uint2 *)unit;
-    #pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                x[j] = d * (float)((int)(((j < 4 ? w.x : w.y) >> (8 * (j & 3))) & 255u) - 128);
-                        } else {
-                            const uint32_t w = *(const uint32_t *)unit;
-    #pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                x[j] = d * (float)((int)((w >> (4 * j)) & 15u) - 8);
-                        }
-                    }
+    for (int it = threadIdx.x; it < ROWS * U; it += 256) {
+        const int64_t i = i0 + it / U;
+        const int u = it % U, b = u >> 2;
+        if (i >= n || 8 * u >= dim)
+            continue;
+        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        int64_t tile;
+        int key;
+        if (slot_at<L>(c, slots[i], head, tile, key)) {
+            const uint8_t *unit = c.k + tile + L::k_unit(key, b, u & 3);
+            if constexpr (KT == KV_F16) {
+                load8((const _Float16 *)unit, x);
+            } else {
+                const float d = h2f(*(const uint16_t *)(c.k + tile + L::k_scale(key, b)));
+                if constexpr (KT == KV_Q8) {
+                    const uint2 w = *(const uint2 *)unit;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        x[j] = d * (float)((int)(((j < 4 ? w.x : w.y) >> (8 * (j & 3))) & 255u) - 128);
+                } else {
+                    const uint32_t w = *(const uint32_t *)unit;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        x[j] = d * (float)((int)((w >> (4 * j)) & 15u) - 8);
                 }
-                store8(k_out + (i * c.kv_heads + head) * dim + 8 * u, x);
             }
+        }
+        store8(k_out + (i * c.kv_heads + head) * dim + 8 * u, x);
+    }
 }
 
 template <int NB, int KT, int ROWS, typename O>
