@@ -51,3 +51,23 @@ def test_append_of_more_tokens_than_a_launch(rotated):
     if rotated:
         rows = torch.cat([-rows[..., 1:2], rows[..., :1], rows[..., 2:]], -1)
     assert torch.equal(k, rows.float())
+
+
+@pytest.mark.parametrize("kind", ["f16", "q8_0"])
+def test_read_and_move_of_more_rows_than_a_launch(kind):
+    """65535 workgroups of 16 rows, of one group: every slot of a cache read in a
+    shuffled order, then moved one by one from its lower to its upper half."""
+    half = 1 << 20
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    cache = q.KVCache(R.TYPES[kind], 1, 8, 2 * half // 256, page_size=256)
+    rows = torch.randint(-100, 100, (half, 1, 8), device=DEV, generator=gen)
+    rows[..., 0] = 127              # the scale of a Q8_0 block is 1
+    every = torch.arange(half, dtype=torch.int32, device=DEV)
+    q.kv_append(cache, rows.half(), -rows.half(), every)
+    order = torch.randperm(half, device=DEV, generator=gen)
+    order = torch.cat([order, order[:70]])
+    k, v = q.kv_read(cache, order.int())
+    assert torch.equal(k, rows[order].float()) and torch.equal(v, -rows[order].float())
+    q.kv_move(cache, every[:, None].contiguous(), (every + half)[:, None].contiguous())
+    k, v = q.kv_read(cache, every + half)
+    assert torch.equal(k, rows.float()) and torch.equal(v, -rows.float())
