@@ -164,8 +164,9 @@ int qkv_rope_freqs(int64_t rot, double base, const qkv_rope_scaling *scaling, co
         auto at = [&](double turns) {
             return (double)rot * std::log(scaling->trained / (turns * TWO_PI)) / (2 * std::log(base));
         };
-        lo = std::fmax(std::floor(at(scaling->beta_fast)), 0.0);
         hi = std::fmin(std::ceil(at(scaling->beta_slow)), (double)(rot - 1));
+        // (hi not above the first pair: every one makes at most beta_slow turns)
+        lo = hi > 0 ? std::fmax(std::floor(at(scaling->beta_fast)), 0.0) : hi - 1;
     }
     for (int64_t i = 0; i < pairs; ++i) {
         double f = std::pow(base, -2.0 * (double)i / (double)rot);

@@ -36,3 +36,14 @@ def test_fewer_sequences_may_need_more_workspace(q):  # noqa: F811
     assert need == {7: 1164800, 16: 1064960, 64: 0}
     a = call(7, workspace_bytes=need[16])
     assert q.lib.qkv_attention(ctypes.addressof(c), ctypes.addressof(a), None) == q.ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("trained,slow,share", [(4.0, 1.0, 1 / 16), (500.0, 100.0, 1 / 16), (1e30, 1.0, 1.0)])
+def test_yarn_where_all_pairs_are_on_one_side(q, trained, slow, share):  # noqa: F811
+    """Every pair below beta_slow turns of the trained context is scaled, the first one
+    too; every pair above beta_fast is not."""
+    f, _ = q.rope_freqs(64, 10000.0, "yarn", factor=16.0, trained=trained, beta_slow=slow, beta_fast=32 * slow)
+    plain, _ = q.rope_freqs(64, 10000.0)
+    turns = trained * plain / (2 * 3.141592653589793)
+    assert (turns < slow).all() or (turns > 32 * slow).all()
+    assert (abs(f / plain - share) < 1e-15).all()
