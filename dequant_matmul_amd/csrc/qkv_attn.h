@@ -268,8 +268,13 @@ __device__ __forceinline__ void read8(const float *p, float v[8])
     }
 }
 __device__ __forceinline__ void write4(float *p, f32x4 v) { *(f32x4 *)p = v; }
+// A mean of values up to 65532 (127 times the largest scale of a Q8_0 block), times what
+// rounded weights add: finite results past the fp16 range are its end.
 __device__ __forceinline__ void write4(_Float16 *p, f32x4 v)
 {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v[i] = fabsf(v[i]) > 65504.f && fabsf(v[i]) < INFINITY ? copysignf(65504.f, v[i]) : v[i];
     *(u32x2 *)p = (u32x2){as_u((h16x2){(_Float16)v[0], (_Float16)v[1]}), as_u((h16x2){(_Float16)v[2], (_Float16)v[3]})};
 }
 

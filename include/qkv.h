@@ -200,10 +200,11 @@ QMM_API int qkv_move(const qkv_cache *cache, const int32_t *src, const int32_t *
  * softmax weights (times the V scale) enter the matrix cores as two fp16 parts
  * each (about 22 bits) against the exact codes.  QKV_HALF: the weights enter as
  * one fp16; a call with more than 32 rows a kv head (max_q * heads / kv_heads)
- * takes K and V as code * scale rounded to fp16, largest value 65504.  The parts
- * are fp16 numbers: such products have all their bits down to 2^-4 (QKV_HALF:
- * 2^-7) of a row's largest one at least, and steps of at most 2^-25 (2^-17) of it
- * below, whatever the scales of V.
+ * takes K and V as code * scale rounded to fp16, largest value 65504; that is the
+ * largest result of any QKV_HALF call, too.  The parts are fp16 numbers: such
+ * products have all their bits down to 2^-4 (QKV_HALF: 2^-7) of a row's largest
+ * one at least, and steps of at most 2^-25 (2^-17) of it below, whatever the
+ * scales of V.
  * No atomics: the same call gives the same bits.
  */
 typedef struct qkv_attn {

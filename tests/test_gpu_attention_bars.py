@@ -159,3 +159,22 @@ def test_scores_past_the_whole_numbers(kind, tq, dt, lift):
             x = c.v[0][hit, h // 4]
             tol = (2.0 ** -9 if dt == torch.float16 else 2.0 ** -18) * np.abs(x).mean(0) + (1e-4 if lift == 0 else 2.0 ** -24)
             assert np.all(np.abs(got[r, h] - x.mean(0)) <= tol), (r, h, len(hit))
+
+
+@pytest.mark.parametrize("kind", A.KINDS)
+@pytest.mark.parametrize("tq", [1, 8, 40])
+@pytest.mark.parametrize("ctx", [200, 3000])
+def test_values_at_the_end_of_fp16(kind, tq, ctx):
+    """Every V at the largest stored value: a mean of them is that value, and no rounding of a
+    weight takes an fp16 result past the range."""
+    c = A.Case(kind, [ctx], [tq], 2, 4, 64, seed=90)
+    v = np.full((ctx + tq, 2, 64), 65504.0)
+    v[..., 1::2] *= -1
+    k = c.k[0].copy()
+    put(c, 0, k, v)
+    got = c.run(torch.float16).cpu().numpy().astype(np.float64)
+    assert np.isfinite(got).all()
+    # K rounded once more than in c.k has no part in it; weights and V by half a step each
+    want = np.minimum(np.abs(c.v[0][0, 0]), 65504.0)
+    assert np.all(np.abs(np.abs(got) - want) <= 2.0 ** -10 * want + 32)
+    assert np.all(np.sign(got) == np.sign(v[0, 0]))
