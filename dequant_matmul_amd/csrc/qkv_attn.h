@@ -383,7 +383,7 @@ __device__ __forceinline__ float load_row(const AttnArgs &a, const Seq &s, int h
         amax = rows_max(amax);
         int e;
         (void)frexpf(amax, &e);
-        e = amax > 0.f && amax < 3.0e38f ? 15 - e : 0;      // maximum to [2^14, 2^15)
+        e = amax > 0.f && amax < INFINITY ? 15 - e : 0;      // maximum to [2^14, 2^15)
         e = e < 120 ? e : 120;
         scale = ldexpf(1.f, -e);
 #pragma unroll

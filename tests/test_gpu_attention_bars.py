@@ -178,3 +178,21 @@ def test_values_at_the_end_of_fp16(kind, tq, ctx):
     want = np.minimum(np.abs(c.v[0][0, 0]), 65504.0)
     assert np.all(np.abs(np.abs(got) - want) <= 2.0 ** -10 * want + 32)
     assert np.all(np.sign(got) == np.sign(v[0, 0]))
+
+
+@pytest.mark.parametrize("kind", ["f16", "q8_0"])
+@pytest.mark.parametrize("tq", [1, 40])
+def test_queries_at_the_end_of_fp32(kind, tq):
+    """Queries whose scaled values lie just below the largest fp32, against keys so small
+    that scores stay below it: the largest key takes the row."""
+    D, n = 128, 100 + tq
+    c = A.Case(kind, [100], [tq], 1, 4, D, seed=95)
+    a = 1.0 + np.arange(n) % 32
+    a[70] = 64
+    k = np.zeros((n, 1, D))
+    k[:, 0, :4] = a[:, None] * 2.0 ** -8        # (in four dims: the sum is 2^-8 of a value)
+    v = np.random.default_rng(96).standard_normal((n, 1, D))
+    put(c, 0, k, v)
+    c.q[:] = 2.2e38
+    got = c.run(torch.float32, scale=1.0).cpu().numpy()
+    assert np.all(np.abs(got - c.v[0][70, 0]) <= 2.0 ** -18 * np.abs(c.v[0][70, 0]) + 2.0 ** -24)
