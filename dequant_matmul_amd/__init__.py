@@ -14,7 +14,8 @@ CPU fallback: if the library is missing, importing this package fails.
     B = qmm.quantize(kv_f16, qmm.Q8_0)                 # fp16 [n, k] -> Q8_0 blocks
 
 Rotary positions, the paged KV cache and attention over it are in kv.py (C ABI
-include/qkv.h) and re-exported here.
+include/qkv.h), block tables, norms, products of Q8_0 activations and adapters in
+step.py (include/qst.h); both are re-exported here.
 
 Block types and layouts follow shimmy "Architecture" (Quantization table) and
 dotLLM "GPU Inference" (Quantization on GPU table); see include/qmm.h.
@@ -306,3 +307,4 @@ def gemm_prefill(w, qtype: int, n: int, k: int, x, out=None):
 
 from .kv import (F16, KVCache, attention, attention_workspace, kv_append, kv_move, kv_read,  # noqa: E402
                  rope, rope_angles, rope_freqs)
+from .step import (gemv_q8, gemv_q8_multi, kv_plan, kv_trim, lora, lora_workspace, rms_norm)  # noqa: E402

@@ -4,41 +4,15 @@
 #include <hip/hip_runtime.h>
 
 #include "../../include/qkv.h"
+#include "qkv_checks.h"
 #include "qkv_launch.h"
 #include "qkv_layout.h"
 
 #include <cmath>
 
+using namespace qmm::host;
+
 namespace {
-
-constexpr int64_t INT_MOST = 0x7fffffff;
-
-bool aligned(const void *p, unsigned n) { return ((uintptr_t)p & (n - 1)) == 0; }
-
-int hip_status(hipError_t e) { return e == hipSuccess ? QMM_OK : QMM_ERR_HIP; }
-
-// The stream's device current for the scope of a call (a launch on another
-// device's stream is refused by the runtime); the NULL stream is the current
-// device's.
-struct OnDevice {
-    int before = -1;
-    explicit OnDevice(void *stream)
-    {
-        if (stream == nullptr)
-            return;
-        int now = 0;
-        hipDevice_t dev = 0;
-        if (hipGetDevice(&now) != hipSuccess || hipStreamGetDevice((hipStream_t)stream, &dev) != hipSuccess)
-            return;
-        if ((int)dev != now && hipSetDevice((int)dev) == hipSuccess)
-            before = now;
-    }
-    ~OnDevice()
-    {
-        if (before >= 0)
-            (void)hipSetDevice(before);
-    }
-};
 
 int kv_type(int type)
 {
@@ -85,21 +59,6 @@ int check_cache(const qkv_cache *c, bool with_buffers, int *kt, qmm::KvView *v)
     v->nb = blocks_of(c->head_dim);
     return QMM_OK;
 }
-
-// An activation tensor of `tokens` rows of `width` elements, `stride` apart.
-int check_rows(int dtype, const void *p, int64_t stride, int64_t tokens, int64_t width)
-{
-    const int64_t es = dtype == QKV_F32 ? 4 : 2;
-    if (tokens > 1 && (stride < width || stride > ((int64_t)1 << 40)))
-        return QMM_ERR_SHAPE;
-    if (p == nullptr)
-        return QMM_ERR_NULL;
-    if (!aligned(p, 16) || (tokens > 1 && stride * es % 16 != 0))
-        return QMM_ERR_ALIGN;
-    return QMM_OK;
-}
-
-bool good_dtype(int dtype) { return dtype == QKV_F32 || dtype == QKV_HALF; }
 
 // The sizes of an attention call; on success *kt, *v and *p describe it.
 int check_attn(const qkv_cache *cache, const qkv_attn *a, bool with_buffers, int *kt, qmm::KvView *v, qmm::AttnPlan *p)
