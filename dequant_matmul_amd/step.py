@@ -207,12 +207,13 @@ def gemv_q8_multi(ws, qtypes, ns, k, x, outs=None):
         outs = [None] * n_probs
     if len(outs) != n_probs:
         raise ValueError("outs must have one tensor per problem")
-    outs = [_out(o, (B, n), _F32, dev) for o, n in zip(outs, ns)]
-    probs = (GemvProblem * max(n_probs, 1))()
-    for i, (w, t, n, o) in enumerate(zip(ws, qtypes, ns, outs)):
+    for w, t, n in zip(ws, qtypes, ns):
         _check_w(w, t, n, k)
         if w.device != dev:
             raise ValueError("x and the weights must be on the same device")
+    outs = [_out(o, (B, n), _F32, dev) for o, n in zip(outs, ns)]
+    probs = (GemvProblem * max(n_probs, 1))()
+    for i, (w, t, n, o) in enumerate(zip(ws, qtypes, ns, outs)):
         probs[i] = GemvProblem(w.data_ptr(), o.data_ptr(), n, t, 0)
     status = _launch(lib.qst_gemv_q8, dev, n_probs, ctypes.addressof(probs), k, x.data_ptr(), B)
     if status:
