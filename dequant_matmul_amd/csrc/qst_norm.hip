@@ -1,7 +1,26 @@
 // qst_norm.hip -- RMS norm of rows with the residual's addition, out in fp32,
 // fp16 or Q8_0 blocks (qst_norm).
+//
+//   s = x + residual,  y = s / sqrt(mean(s^2) + eps) * weight
+//
+// Bound: HBM at length (each value read once, written once), the launch and one
+// round trip for a few rows.  A row is held in registers by the lanes that share
+// it, 8 values a chunk and lane, so nothing is read twice, `sum` may be x or the
+// residual itself, and the only exchange is one sum.  Rows of up to 512 values
+// (heads) are shared by 1 to 64 lanes of a wave, several rows to a wave, so short
+// rows leave no lanes idle; longer ones by a workgroup of up to 16 waves.
+//
+// Q8_0: a block's 32 values are four neighbouring lanes' chunks; its largest
+// value passes by two DPP swaps and the rule is qmm_quantize's on the fp32
+// results, every step rounded once (contraction off there).
+//
+// Measured: 8191 rows of 4096, fp32 + fp16 residual -> fp16, 335 MB, 59 us (5.7
+// TB/s); 2047 x 32 heads of 128, fp32 -> fp16, 50 MB, 9.4 us (5.4 TB/s); one row
+// of 4096 to Q8_0 under 3 us.
 #include "qmm_device.h"
 #include "qst_launch.h"
+
+#include <type_traits>
 
 namespace qmm {
 
@@ -15,69 +34,224 @@ struct NormK {
     int64_t xs, rs, ss, os, rows;
     int heads, dim;
     float eps;
-    int x_half, res_half, out_type;
 };
 
-__device__ __forceinline__ float value(const void *p, int half, int64_t i)
+// 8 values from element i of a row; VEC: 16-byte loads, and dim a multiple of 8.
+template <bool VEC, typename I>
+__device__ __forceinline__ void load8(const I *p, int i, int dim, float v[8])
 {
-    return half ? (float)((const _Float16 *)p)[i] : ((const float *)p)[i];
-}
-
-__device__ __forceinline__ void put(void *p, int half, int64_t i, float v)
-{
-    if (half)
-        ((_Float16 *)p)[i] = (_Float16)v;
-    else
-        ((float *)p)[i] = v;
-}
-
-// One workgroup a row, its sums read twice.
-__global__ void __launch_bounds__(256) norm_kernel(NormK a)
-{
-    __shared__ float part[4];
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        const int64_t tok = row / a.heads, at = (row - tok * a.heads) * a.dim;
-        const int64_t xo = tok * a.xs + at, ro = tok * a.rs + at, so = tok * a.ss + at, oo = tok * a.os + at;
-        float q = 0.f;
-        for (int i = threadIdx.x; i < a.dim; i += 256) {
-            const float v = value(a.x, a.x_half, xo + i) + (a.res ? value(a.res, a.res_half, ro + i) : 0.f);
-            q = __builtin_fmaf(v, v, q);
-        }
-        q = wave_sum(q);
-        if ((threadIdx.x & 63) == 0)
-            part[threadIdx.x >> 6] = q;
-        __syncthreads();
-        q = (part[0] + part[1]) + (part[2] + part[3]);
-        const float r = 1.f / sqrtf(q / (float)a.dim + a.eps);
-        for (int i0 = 0; i0 < a.dim; i0 += 256) {
-            const int i = i0 + (int)threadIdx.x;
-            const bool in = i < a.dim;
-            float v = 0.f, y = 0.f;
-            if (in) {
-                v = value(a.x, a.x_half, xo + i) + (a.res ? value(a.res, a.res_half, ro + i) : 0.f);
-                y = v * r * (a.w ? a.w[i] : 1.f);
-            }
-            if (in && a.sum)
-                put(a.sum, a.res ? a.res_half : a.x_half, so + i, v);
-            if (a.out_type != QST_Q8_0) {
-                if (in)
-                    put(a.out, a.out_type == QST_HALF, oo + i, y);
-                continue;
-            }
-            float m = fabsf(y);
+    if constexpr (VEC && sizeof(I) == 2) {
+        const u32x4 r = *(const u32x4 *)(p + i);
 #pragma unroll
-            for (int d = 16; d > 0; d /= 2)
-                m = fmaxf(m, __shfl_xor(m, d));
-            const float d = m / 127.f, id = d != 0.f ? 1.f / d : 0.f;
-            uint8_t *blk = (uint8_t *)a.out + (row * (a.dim / 32) + i / 32) * 34;
-            if (in) {
-                blk[2 + i % 32] = (uint8_t)(int)roundf(y * id);
-                if (i % 32 == 0)
-                    *(uint16_t *)blk = __builtin_bit_cast(uint16_t, (_Float16)d);
-            }
+        for (int j = 0; j < 4; ++j) {
+            v[2 * j] = h2f(r[j] & 0xffffu);
+            v[2 * j + 1] = h2f(r[j] >> 16);
         }
-        __syncthreads();
+    } else if constexpr (VEC) {
+        const f32x4 a = *(const f32x4 *)(p + i), b = *(const f32x4 *)(p + i + 4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[j] = a[j];
+            v[4 + j] = b[j];
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = i + j < dim ? (float)p[i + j] : 0.f;
     }
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b)
+{
+    return __builtin_bit_cast(uint32_t, (h16x2){(_Float16)a, (_Float16)b});
+}
+
+template <bool VEC, typename O>
+__device__ __forceinline__ void store8(O *p, int i, int dim, const float v[8])
+{
+    if constexpr (VEC && sizeof(O) == 2) {
+        *(u32x4 *)(p + i) = (u32x4){pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7])};
+    } else if constexpr (VEC) {
+        *(f32x4 *)(p + i) = (f32x4){v[0], v[1], v[2], v[3]};
+        *(f32x4 *)(p + i + 4) = (f32x4){v[4], v[5], v[6], v[7]};
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (i + j < dim)
+                p[i + j] = (O)v[j];
+    }
+}
+
+// The chunk's part of a Q8_0 block: 8 codes by lane i / 8 % 4 of the block's four.
+__device__ __forceinline__ void store_q8(uint8_t *row, int i, const float y[8])
+{
+#pragma clang fp contract(off)
+    float m = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        m = fmaxf(m, fabsf(y[j]));
+    m = fmaxf(m, dpp_f(m, 0xB1));
+    m = fmaxf(m, dpp_f(m, 0x4E));
+    const float d = m / 127.f, id = d != 0.f ? 1.f / d : 0.f;
+    uint16_t *b = (uint16_t *)(row + i / 32 * 34);
+    const int c = i / 8 % 4;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t lo = (uint32_t)(int)roundf(y[2 * j] * id) & 0xffu, hi = (uint32_t)(int)roundf(y[2 * j + 1] * id);
+        b[1 + 4 * c + j] = (uint16_t)(lo | hi << 8);
+    }
+    if (c == 0)
+        b[0] = __builtin_bit_cast(uint16_t, (_Float16)d);
+}
+
+struct Q8Out {};   // as an output type
+
+// LPR lanes a row (a power of two up to 64: several rows a wave; more: the
+// workgroup), NC chunks of 8 values a lane, chunk c at lane + c LPR.
+template <typename X, typename R, typename O, int LPR, int NC, bool VEC>
+__global__ void __launch_bounds__(LPR < 256 ? 256 : LPR) norm_kernel(NormK a)
+{
+    constexpr int BLOCK = LPR < 256 ? 256 : LPR, RPB = BLOCK / LPR;
+    constexpr bool Q8 = std::is_same<O, Q8Out>::value;
+    const int l = threadIdx.x % LPR;
+    // lanes past the row's end, and rows past the last, read what the last chunk or row
+    // does (no load stands in a branch) and count as zero
+    int at[NC];
+    bool has[NC];
+    float w[NC][8];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        const int i = 8 * (l + c * LPR);
+        has[c] = i < a.dim;
+        at[c] = VEC && !has[c] ? a.dim - 8 : i;
+    }
+    if (a.w) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+            load8<VEC>(a.w, at[c], a.dim, w[c]);
+    } else {
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                w[c][j] = 1.f;
+    }
+    for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < a.rows; row0 += (int64_t)gridDim.x * RPB) {
+        const int64_t row1 = row0 + threadIdx.x / LPR;
+        const bool live = row1 < a.rows;
+        const int64_t row = live ? row1 : a.rows - 1;
+        const int64_t tok = a.heads == 1 ? row : (int64_t)((uint64_t)row / (uint32_t)a.heads);
+        const int64_t head = (row - tok * a.heads) * a.dim;
+        const X *x = (const X *)a.x + tok * a.xs + head;
+        const R *r = (const R *)a.res + tok * a.rs + head;
+        float s[NC][8];
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+            load8<VEC>(x, at[c], a.dim, s[c]);
+        if (a.res) {
+            float t[NC][8];
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+                load8<VEC>(r, at[c], a.dim, t[c]);
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    s[c][j] += t[c][j];
+        }
+        float q = 0.f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                q = has[c] ? __builtin_fmaf(s[c][j], s[c][j], q) : q;
+        if constexpr (LPR <= 64) {
+#pragma unroll
+            for (int d = 1; d < LPR; d *= 2)
+                q += __shfl_xor(q, d);
+        } else {
+            __shared__ float part[LPR / 64];
+            q = wave_sum(q);
+            __syncthreads();           // the row before has been summed
+            if ((threadIdx.x & 63) == 0)
+                part[threadIdx.x >> 6] = q;
+            __syncthreads();
+            q = 0.f;
+#pragma unroll
+            for (int i = 0; i < LPR / 64; ++i)
+                q += part[i];
+        }
+        const float g = 1.f / sqrtf(q / (float)a.dim + a.eps);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const int i = at[c];
+            if (!live || !has[c])
+                continue;
+            if (a.sum) {
+                if (a.res)
+                    store8<VEC>((R *)a.sum + tok * a.ss + head, i, a.dim, s[c]);
+                else
+                    store8<VEC>((X *)a.sum + tok * a.ss + head, i, a.dim, s[c]);
+            }
+            float y[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                y[j] = s[c][j] * g * w[c][j];
+            if constexpr (Q8)
+                store_q8((uint8_t *)a.out + row * (a.dim / 32 * 34), i, y);
+            else
+                store8<VEC>((O *)a.out + tok * a.os + head, i, a.dim, y);
+        }
+    }
+}
+
+// A workgroup a row (or RPB rows): weights read once by workgroups that go on over
+// rows are no faster (8191 x 4096, fp32 + fp16 -> fp16: 59.0 us; 512, 1024 or 2048
+// such workgroups 60.4, 60.8, 60.4; 16-bit rows 42.1 and 46.6, 42.4, 43.3).
+constexpr int64_t GROUPS = 1 << 20;
+
+template <typename X, typename R, typename O, int LPR, int NC, bool VEC>
+hipError_t launch(const NormK &k, hipStream_t s)
+{
+    constexpr int BLOCK = LPR < 256 ? 256 : LPR, RPB = BLOCK / LPR;
+    const int64_t groups = (k.rows + RPB - 1) / RPB;
+    return start(norm_kernel<X, R, O, LPR, NC, VEC>, dim3((unsigned)(groups < GROUPS ? groups : GROUPS)), dim3(BLOCK), s,
+                 k);
+}
+
+template <typename X, typename R, typename O>
+hipError_t by_length(const NormK &k, bool vec, hipStream_t s)
+{
+    const int chunks = (k.dim + 7) / 8;
+    if (!vec)      // unaligned rows: element by element, of few shapes
+        return chunks <= 64    ? launch<X, R, O, 64, 1, false>(k, s)
+               : chunks <= 512 ? launch<X, R, O, 256, 2, false>(k, s)
+                               : launch<X, R, O, 1024, 8, false>(k, s);
+    return chunks <= 8      ? launch<X, R, O, 8, 1, true>(k, s)
+           : chunks <= 16   ? launch<X, R, O, 16, 1, true>(k, s)
+           : chunks <= 32   ? launch<X, R, O, 32, 1, true>(k, s)
+           : chunks <= 64   ? launch<X, R, O, 64, 1, true>(k, s)
+           : chunks <= 256  ? launch<X, R, O, 256, 1, true>(k, s)
+           : chunks <= 512  ? launch<X, R, O, 256, 2, true>(k, s)
+           : chunks <= 1024 ? launch<X, R, O, 512, 2, true>(k, s)
+           : chunks <= 2048 ? launch<X, R, O, 1024, 2, true>(k, s)
+                            : launch<X, R, O, 1024, 8, true>(k, s);
+}
+
+template <typename X, typename R>
+hipError_t by_out(int out_type, const NormK &k, bool vec, hipStream_t s)
+{
+    switch (out_type) {
+    case QST_F32: return by_length<X, R, float>(k, vec, s);
+    case QST_HALF: return by_length<X, R, _Float16>(k, vec, s);
+    default: return by_length<X, R, Q8Out>(k, vec, s);
+    }
+}
+
+// 8 values of every row start 16-byte aligned
+bool even(const void *p, int64_t stride, int64_t tokens)
+{
+    return p == nullptr || (((uintptr_t)p & 15) == 0 && (tokens == 1 || stride % 8 == 0));
 }
 
 }  // namespace
@@ -85,9 +259,14 @@ __global__ void __launch_bounds__(256) norm_kernel(NormK a)
 hipError_t launch_norm(const qst_norm_args &a, hipStream_t s)
 {
     const NormK k{a.x, a.residual, a.sum, a.weight, a.out, a.x_stride, a.residual_stride, a.sum_stride, a.out_stride,
-                  a.tokens * a.heads, (int)a.heads, (int)a.dim, a.eps, a.x_type == QKV_HALF, a.residual_type == QKV_HALF,
-                  a.out_type};
-    return start(norm_kernel, dim3((unsigned)(k.rows < (1 << 20) ? k.rows : (1 << 20))), dim3(256), s, k);
+                  a.tokens * a.heads, (int)a.heads, (int)a.dim, a.eps};
+    const bool vec = a.dim % 8 == 0 && even(a.x, a.x_stride, a.tokens) && even(a.residual, a.residual_stride, a.tokens) &&
+                     even(a.sum, a.sum_stride, a.tokens) && even(a.weight, 0, 1) &&
+                     (a.out_type == QST_Q8_0 || even(a.out, a.out_stride, a.tokens));
+    const bool xh = a.x_type == QKV_HALF, rh = a.residual ? a.residual_type == QKV_HALF : xh;
+    if (xh)
+        return rh ? by_out<_Float16, _Float16>(a.out_type, k, vec, s) : by_out<_Float16, float>(a.out_type, k, vec, s);
+    return rh ? by_out<float, _Float16>(a.out_type, k, vec, s) : by_out<float, float>(a.out_type, k, vec, s);
 }
 
 }  // namespace qmm
