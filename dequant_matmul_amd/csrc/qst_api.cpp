@@ -153,23 +153,36 @@ int qst_gemv_q8(int nprob, const qst_gemv_problem *probs, int64_t k, const void 
             }
         return QMM_OK;
     }
-    // one launch for the problems of a type, up to Q8_PROBS of them
-    for (int type = 0; qmm_block_elems(type) != 0; ++type) {
-        qmm::Q8Probs t;
-        t.np = 0;
+    // a launch for the 32-element types and one for the others, of up to Q8_PROBS
+    // problems a type
+    static const int types[2][qmm::Q8_TYPES] = {{QMM_Q4_0, QMM_Q8_0, QMM_Q5_0}, {QMM_Q4_K, QMM_Q6_K, QMM_Q5_K}};
+    for (int large = 0; large < 2; ++large) {
+        const auto launch = large ? (batch <= 3 ? qmm::launch_q8_large1 : qmm::launch_q8_large2)
+                                  : (batch <= 3 ? qmm::launch_q8_small1 : qmm::launch_q8_small2);
+        qmm::Q8Probs t[qmm::Q8_TYPES];
+        bool any = false;
+        for (qmm::Q8Probs &p : t)
+            p.np = 0;
         for (int i = 0; i <= nprob; ++i) {
-            if (t.np == qmm::Q8_PROBS || (i == nprob && t.np > 0)) {
-                const int st = hip_status(qmm::launch_gemv_q8(type, t, k, qmm_row_bytes(type, k), (const uint8_t *)x,
-                                                              (int)batch, (hipStream_t)stream));
+            int at = -1;
+            for (int j = 0; i < nprob && j < qmm::Q8_TYPES; ++j)
+                if (probs[i].type == types[large][j] && probs[i].n > 0)
+                    at = j;
+            if (any && (i == nprob || (at >= 0 && t[at].np == qmm::Q8_PROBS))) {
+                const int st = hip_status(launch(t, (int)k, (const uint8_t *)x, (int)batch, (hipStream_t)stream));
                 if (st != QMM_OK)
                     return st;
-                t.np = 0;
+                any = false;
+                for (qmm::Q8Probs &p : t)
+                    p.np = 0;
             }
-            if (i == nprob || probs[i].type != type || probs[i].n == 0)
+            if (at < 0)
                 continue;
-            t.w[t.np] = (const uint8_t *)probs[i].w;
-            t.y[t.np] = probs[i].y;
-            t.n[t.np++] = (int)probs[i].n;
+            qmm::Q8Probs &p = t[at];
+            p.w[p.np] = (const uint8_t *)probs[i].w;
+            p.y[p.np] = probs[i].y;
+            p.n[p.np++] = (int)probs[i].n;
+            any = true;
         }
     }
     return QMM_OK;

@@ -1,4 +1,4 @@
-// qst_gemv_q8.hip -- products of Q8_0 activations with quantized weights, as
+// qst_gemv_q8.h -- products of Q8_0 activations with quantized weights, as
 // integer dot products (qst_gemv_q8).
 //
 //   y[b][j] = sum over blocks of  d_w d_x sum_i q_i x_i      (Q4_0, Q5_0, Q6_K: q less its offset)
@@ -24,11 +24,11 @@
 // formed with the rounding error of dmin m S carried along: where the weights of a
 // sub-block cancel, what is left is right to a rounding of itself, and a row of
 // zero weights gives 0.
+#pragma once
+
 #include "qmm_device.h"
 #include "qmm_gemv_unit.h"
 #include "qst_launch.h"
-
-#include <cstdlib>
 
 namespace qmm {
 
@@ -37,12 +37,20 @@ namespace {
 constexpr int WAVES = 8;     // of a workgroup at most
 constexpr int ITEMS = 8;     // of a block of rows at most
 
-struct Q8K {
+// The problems of a block type.
+struct Q8Type {
     const uint8_t *w[Q8_PROBS];
     float *y[Q8_PROBS];
     int n[Q8_PROBS];
     int blk0[Q8_PROBS + 1];   // first block of each problem; the total behind the last
     int np;
+};
+
+// A launch: up to three block types of one unit size, each with a run of the
+// workgroups, wg0[t] .. wg0[t + 1].
+struct Q8Call {
+    Q8Type t[Q8_TYPES];
+    int wg0[Q8_TYPES + 1];
 };
 
 // x of one lane-unit for B rows: codes in the order in which dot() meets them, the
@@ -58,56 +66,99 @@ template <int T, int B> struct XUnit {
 
 __device__ __forceinline__ int dot4(uint32_t a, int b, int acc) { return __builtin_amdgcn_sdot4((int)a, b, acc, false); }
 
-// The bytes of x are 2-byte aligned (34 bytes a block).
-struct __attribute__((packed, aligned(2))) Four {
-    uint32_t v[4];
+// A block's 32 codes: 2-byte aligned (34 bytes a block).
+struct __attribute__((packed, aligned(2))) Codes {
+    uint32_t v[8];
 };
 
-template <int T, int B>
-__device__ __forceinline__ void load_x(XUnit<T, B> &x, const uint8_t *p, int nblocks, int unit, int batch)
-{
+// x passes through LDS: the workgroup's threads take a block of 32 each (a few, where
+// there are more) and lay its codes 16-byte aligned, unit after unit with 16 bytes
+// between (so that the lanes' reads meet different banks), the scales behind them.
+// (Each wave loading its lanes' codes itself costs the address unit 6 us at batch 8.)
+template <int T> struct XLay {
+    static constexpr int UE = GemvUnit<T>::UE, NB = UE / 32;
+    static constexpr int UNIT = UE / 4 + 4;                    // dwords
+    static constexpr int CODES = 64 * UNIT;                    // of a segment's row
+    static constexpr int ROW = CODES + 64 * NB;                // ... with its scales
+};
+
+// Blocks of `rows` rows of x from row0 on, `segs` segments from unit0's: threads t of nt.
+template <int T, int MOST>
+struct XStage {
+    Codes c[MOST];
+    uint16_t d[MOST];
+    __device__ __forceinline__ void load(const uint8_t *x, int nblocks, int block0, int per_row, int rows, int row0,
+                                         int last, int t, int nt)
+    {
 #pragma unroll
-    for (int b = 0; b < B; ++b) {
-        // rows past the batch repeat its last one and are not stored
-        const uint8_t *row = p + (int64_t)(b < batch ? b : batch - 1) * nblocks * 34;
-        if constexpr (T == T_Q6_K) {
-            // four groups of 16: half a block each
-            const uint8_t *q = row + (8 * (unit >> 2) + 4 * ((unit >> 1) & 1)) * 34;
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const Four f = *(const Four *)(q + 34 * g + 2 + 16 * (unit & 1));
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    x.c[b][4 * g + i] = (int)f.v[i];
-                x.d[b][g] = h2f(*(const uint16_t *)(q + 34 * g));
-            }
-        } else {
-            constexpr int NB = GemvUnit<T>::UE / 32;
-            const uint8_t *q = row + unit * NB * 34;
-#pragma unroll
-            for (int g = 0; g < NB; ++g) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const Four f = *(const Four *)(q + 34 * g + 2 + 16 * h);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        x.c[b][8 * g + 4 * h + i] = (int)f.v[i];
-                }
-                x.d[b][g] = h2f(*(const uint16_t *)(q + 34 * g));
-            }
+        for (int i = 0; i < MOST; ++i) {
+            // past the end: the last block again
+            const int j = min(t + i * nt, per_row * rows - 1), r = j / per_row;
+            const int blk = min(block0 + j - r * per_row, nblocks - 1);
+            const uint8_t *p = x + ((int64_t)min(row0 + r, last) * nblocks + blk) * 34;
+            c[i] = *(const Codes *)(p + 2);
+            d[i] = *(const uint16_t *)p;
         }
+    }
+    __device__ __forceinline__ void store(uint32_t *xs, int per_row, int rows, int t, int nt) const
+    {
+        using L = XLay<T>;
+#pragma unroll
+        for (int i = 0; i < MOST; ++i) {
+            const int j = t + i * nt, r = j / per_row, blk = j - r * per_row;
+            if (j >= per_row * rows)
+                continue;
+            // of the segment: its unit's place, its scale's
+            const int seg = blk / (64 * L::NB), in = blk - seg * 64 * L::NB;
+            uint32_t *row = xs + (r * (per_row / (64 * L::NB)) + seg) * L::ROW;
+            uint32_t *to = row + in / L::NB * L::UNIT + 8 * (in % L::NB);
+            *(u32x4 *)to = (u32x4){c[i].v[0], c[i].v[1], c[i].v[2], c[i].v[3]};
+            *(u32x4 *)(to + 4) = (u32x4){c[i].v[4], c[i].v[5], c[i].v[6], c[i].v[7]};
+            row[L::CODES + in] = __builtin_bit_cast(uint32_t, h2f(d[i]));
+        }
+    }
+};
+
+// Row b of a lane's unit from a staged row of its segment.
+template <int T, int B>
+__device__ __forceinline__ void take_x(XUnit<T, B> &x, int b, const uint32_t *row, int unit)
+{
+    using L = XLay<T>;
+    if constexpr (T == T_Q6_K) {
+        // four groups of 16: half a block each
+        const int blk = 8 * (unit >> 2) + 4 * ((unit >> 1) & 1);
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const u32x4 f = *(const u32x4 *)(row + (blk + g) / 2 * L::UNIT + 8 * ((blk + g) % 2) + 4 * (unit & 1));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                x.c[b][4 * g + i] = (int)f[i];
+        }
+        const f32x4 d = *(const f32x4 *)(row + L::CODES + blk);
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+            x.d[b][g] = d[g];
+    } else {
+#pragma unroll
+        for (int i = 0; i < XUnit<T, B>::NC; i += 4) {
+            const u32x4 f = *(const u32x4 *)(row + unit * L::UNIT + i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                x.c[b][i + j] = (int)f[j];
+        }
+#pragma unroll
+        for (int g = 0; g < L::NB; ++g)
+            x.d[b][g] = __builtin_bit_cast(float, row[L::CODES + unit * L::NB + g]);
     }
     if constexpr (XUnit<T, B>::NS > 0) {
 #pragma unroll
-        for (int b = 0; b < B; ++b)
+        for (int g = 0; g < 2; ++g) {
+            int s = 0;
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                int s = 0;
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    s = dot4(0x01010101u, x.c[b][8 * g + i], s);
-                x.s[b][g] = (float)s;
-            }
+            for (int i = 0; i < 8; ++i)
+                s = dot4(0x01010101u, x.c[b][8 * g + i], s);
+            x.s[b][g] = (float)s;
+        }
     }
 }
 
@@ -275,7 +326,7 @@ template <int D> __device__ __forceinline__ float add_rows(float v)
     return u + v;
 }
 
-// Sums of v[0 .. B) over groups of LP lanes.  Each of the first log2 B steps halves
+// Sums of v[0 .. B), B a power of two, over groups of LP lanes.  Each of the first log2 B steps halves
 // the values a lane carries: lane bits 0, 1 and 3 say which is left (value bits 0, 1
 // and 2).  The tree, over lane bits 0, 1, 3, 2, 4, 5, is the same for every B.
 template <int B, int LP> __device__ __forceinline__ float sum_lanes(float (&v)[B], int lane)
@@ -315,22 +366,32 @@ template <int B, int LP> __device__ __forceinline__ float sum_lanes(float (&v)[B
 
 // An item: RPI = 64 / LP whole rows (LP < 64: k is less than half a segment), or one
 // row's segment.  MULTI: `seg_waves` waves share a row; rounds of that many segments.
+template <int T, int B, int LP, bool MULTI> struct Q8Shape {
+    static constexpr int UE = GemvUnit<T>::UE, SEGB = 64 * UE / Fmt<T>::BE * Fmt<T>::BB;
+    static constexpr bool EVEN = T == T_Q4_K || T == T_Q5_K;     // rows of whole 16-byte chunks
+    static constexpr int BYTES = SEGB + (EVEN ? 0 : 16);
+    static constexpr int STAGE = BYTES / 4 + 4;                  // dwords of a wave (+ 4: reads realign past the end)
+    // x passes through before the first item, XR rows of it at a time
+    static constexpr int XR = MULTI ? 1 : B, XSEGS = MULTI ? WAVES : 1;
+    static constexpr int XDW = XR * XSEGS * XLay<T>::ROW;
+    static constexpr int DW = WAVES * STAGE > XDW ? WAVES * STAGE : XDW;
+};
+
+// wg of wgs: this workgroup among those of its type.
 template <int T, int B, int LP, bool MULTI>
-__global__ void __launch_bounds__(64 * WAVES, B <= 2 ? 4 : 2)
-gemv_q8_kernel(Q8K P, const uint8_t *x, int k, int batch, int items, int seg_waves, int groups)
+__device__ __forceinline__ void gemv_q8_body(const Q8Type &P, const uint8_t *x, int k, int batch, int items,
+                                             int seg_waves, int groups, int wg, int wgs, uint32_t *stage, float *part)
 {
+    using S = Q8Shape<T, B, LP, MULTI>;
     using X = XUnit<T, B>;
-    constexpr int UE = GemvUnit<T>::UE, SEGB = 64 * UE / Fmt<T>::BE * Fmt<T>::BB, RPI = 64 / LP;
-    constexpr bool EVEN = T == T_Q4_K || T == T_Q5_K;            // rows of whole 16-byte chunks
-    constexpr int BYTES = SEGB + (EVEN ? 0 : 16);
-    constexpr int NCH = (BYTES + 1023) / 1024, STAGE = BYTES / 4 + 4;   // (+ 4: reads realign past the end)
-    __shared__ __align__(16) uint32_t stage[WAVES * STAGE];
-    __shared__ float part[MULTI ? 2 * WAVES * ITEMS * B : 1];
+    using XL = XLay<T>;
+    constexpr int UE = S::UE, SEGB = S::SEGB, RPI = 64 / LP, BYTES = S::BYTES, NCH = (BYTES + 1023) / 1024, XR = S::XR;
+    constexpr bool EVEN = S::EVEN;
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    uint32_t *mine = stage + wave * STAGE;
+    uint32_t *mine = stage + wave * S::STAGE;
     const int g = MULTI ? wave / seg_waves : wave, sw = MULTI ? wave - g * seg_waves : 0;
-    const int gw = blockIdx.x * groups + g, tw = gridDim.x * groups;
+    const int gw = wg * groups + g, tw = wgs * groups;
     const int units = k / UE, nblocks = k / 32;
     const int64_t rb = (int64_t)(k / Fmt<T>::BE) * Fmt<T>::BB;
     const int total = P.blk0[P.np];
@@ -370,23 +431,48 @@ gemv_q8_kernel(Q8K P, const uint8_t *x, int k, int batch, int items, int seg_wav
             f[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, 16 * (lane + 64 * i), 0, 2));
     };
 
+    X xu;
+    const int nt = 64 * (MULTI ? seg_waves * groups : WAVES), segs = MULTI ? seg_waves : 1;
+    const int per_row = segs * 64 * XL::NB;
+    constexpr int XM = MULTI ? 2 : (B * 64 * XL::NB + 64 * WAVES - 1) / (64 * WAVES);
+    XStage<T, XM> t;
+    auto load_seg = [&](int round, bool first) __attribute__((always_inline)) {
+        const int unit = (MULTI ? 64 * (round * seg_waves + sw) : 0) + unit0;
+        const int mine_unit = unit < units ? unit0 : 0;
+#pragma unroll
+        for (int r0 = 0; r0 < B; r0 += XR) {
+            if (!first || r0 > 0) {
+                t.load(x, nblocks, round * per_row, per_row, XR, r0, batch - 1, threadIdx.x, nt);
+                lds_barrier();            // what was there has been read
+            }
+            t.store(stage, per_row, XR, threadIdx.x, nt);
+            lds_barrier();
+#pragma unroll
+            for (int r = 0; r < XR; ++r)
+                take_x<T, B>(xu, r0 + r, stage + (r * segs + sw) * XL::ROW, mine_unit);
+        }
+    };
+
     Cur cl{gw, 0, 0, 0};
     while (cl.p + 1 < P.np && cl.blk >= P.blk0[cl.p + 1])
         ++cl.p;
     Cur cc = cl;
+    // x is asked for first, so that the wait for it leaves the items in flight (many
+    // rows of several segments have no registers for both)
+    t.load(x, nblocks, 0, per_row, XR, 0, batch - 1, threadIdx.x, nt);
+    __builtin_amdgcn_sched_barrier(0);
+    if (MULTI && B >= 6)
+        load_seg(0, true);
     load(cl, pf[0]);
     next(cl);
     load(cl, pf[1]);
     next(cl);
+    if (!(MULTI && B >= 6))
+        load_seg(0, true);
+    lds_barrier();                        // the stage belongs to the items now
 
-    X xu;
-    auto load_seg = [&](int round) __attribute__((always_inline)) {
-        const int unit = (MULTI ? 64 * (round * seg_waves + sw) : 0) + unit0;
-        load_x<T, B>(xu, x, nblocks, unit < units ? unit : 0, batch);
-    };
-    load_seg(0);
-
-    float acc[B];
+    constexpr int PB = B == 3 ? 4 : B == 6 ? 8 : B;       // the sums' values: more are zero
+    float acc[PB];
     auto work = [&](const Cur &c, u32x4 *f) __attribute__((always_inline)) {
         const int n = P.n[c.p];
         const int64_t row0 = ((int64_t)(c.blk - P.blk0[c.p]) * items + c.item) * RPI;
@@ -416,26 +502,31 @@ gemv_q8_kernel(Q8K P, const uint8_t *x, int k, int batch, int items, int seg_wav
         const bool in = unit < units && (LP == 64 || row0 + sub < n);
         URaw<T> r;
         read_unit<T>(mine, in ? (LP < 64 ? sub * units + unit0 : lane) : 0, shift, r);
-        dot<T, B>(r, in ? unit0 : 0, xu, acc);
+        float v[B];
+        dot<T, B>(r, in ? unit0 : 0, xu, v);
 #pragma unroll
-        for (int b = 0; b < B; ++b)
-            acc[b] = in ? acc[b] : 0.f;
+        for (int b = 0; b < PB; ++b)
+            acc[b] = b < B && in ? v[b < B ? b : 0] : 0.f;
     };
     // lanes whose sum is a result: bits 0, 1 and 3 as far as B has values
-    constexpr int VBITS = B == 1 ? 0 : B == 2 ? 1 : B == 4 ? 3 : 11;
-    const int vb = (lane & VBITS & 3) | (B == 8 ? (lane & 8) >> 1 : 0);
+    constexpr int VBITS = PB == 1 ? 0 : PB == 2 ? 1 : PB == 4 ? 3 : 11;
+    const int vb = (lane & VBITS & 3) | (PB == 8 ? (lane & 8) >> 1 : 0);
     const bool holds = ((lane & (LP - 1)) & ~VBITS) == 0 && vb < batch;
 
     const int blocks = gw < total ? (total - 1 - gw) / tw + 1 : 0;
     const int most = MULTI ? (total + tw - 1) / tw : blocks;      // the same for every wave of a workgroup
     int steps = most * items * rounds, buf = 0;
+    bool steps_done = false;
     auto step = [&](u32x4 *f) __attribute__((always_inline)) {
-        if (MULTI && rounds > 1 && cc.item == 0)
-            load_seg(cc.round);
+        if (MULTI && rounds > 1 && cc.item == 0 && steps_done) {
+            load_seg(cc.round, false);
+            lds_barrier();
+        }
+        steps_done = true;
         work(cc, f);
         load(cl, f);
         next(cl);
-        const float s = sum_lanes<B, LP>(acc, lane);
+        const float s = sum_lanes<PB, LP>(acc, lane);
         if constexpr (!MULTI) {
             const int n = P.n[cc.p];
             const int64_t row = ((int64_t)(cc.blk - P.blk0[cc.p]) * items + cc.item) * RPI + sub;
@@ -470,69 +561,91 @@ gemv_q8_kernel(Q8K P, const uint8_t *x, int k, int batch, int items, int seg_wav
         step(pf[0]);
 }
 
-template <int T, int B, int LP, bool MULTI>
-hipError_t run(const Q8Probs &p, int k, const uint8_t *x, int batch, hipStream_t s)
+template <int A, int B> struct Most {
+    static constexpr int v = A > B ? A : B;
+};
+
+// T0, T1, T2: the types of a launch, of one unit size.
+template <int T0, int T1, int T2, int B, int LP, bool MULTI>
+__global__ void __launch_bounds__(64 * WAVES, B <= 2 ? 4 : 2)
+gemv_q8_kernel(Q8Call c, const uint8_t *x, int k, int batch, int items, int seg_waves, int groups)
 {
-    constexpr int UE = GemvUnit<T>::UE, RPI = 64 / LP;
+    constexpr int DW = Most<Q8Shape<T0, B, LP, MULTI>::DW, Most<Q8Shape<T1, B, LP, MULTI>::DW, Q8Shape<T2, B, LP, MULTI>::DW>::v>::v;
+    __shared__ __align__(16) uint32_t stage[DW];
+    __shared__ float part[MULTI ? 2 * WAVES * ITEMS * B : 1];
+    const int wg = blockIdx.x;
+    if (wg < c.wg0[1])
+        gemv_q8_body<T0, B, LP, MULTI>(c.t[0], x, k, batch, items, seg_waves, groups, wg, c.wg0[1], stage, part);
+    else if (wg < c.wg0[2])
+        gemv_q8_body<T1, B, LP, MULTI>(c.t[1], x, k, batch, items, seg_waves, groups, wg - c.wg0[1],
+                                       c.wg0[2] - c.wg0[1], stage, part);
+    else
+        gemv_q8_body<T2, B, LP, MULTI>(c.t[2], x, k, batch, items, seg_waves, groups, wg - c.wg0[2],
+                                       c.wg0[3] - c.wg0[2], stage, part);
+}
+
+template <int T0, int T1, int T2, int B, int LP, bool MULTI>
+hipError_t run(const Q8Probs (&p)[Q8_TYPES], int k, const uint8_t *x, int batch, hipStream_t s)
+{
+    constexpr int UE = GemvUnit<T0>::UE, RPI = 64 / LP;
+    static_assert(GemvUnit<T1>::UE == UE && GemvUnit<T2>::UE == UE, "types of one unit size");
     const int units = k / UE, segs = (units + 63) / 64, sw = segs < WAVES ? segs : WAVES, groups = WAVES / sw;
     const int cus = device_cu_count();
     if (cus == 0)
         return hipErrorInvalidDevice;
     int64_t rows = 0;
-    for (int i = 0; i < p.np; ++i)
-        rows += (p.n[i] + RPI - 1) / RPI;
-    const int per_cu = getenv("WGC") ? atoi(getenv("WGC")) : (B <= 2 ? 4 : 2);
-    const int64_t slots = (int64_t)cus * per_cu * groups;
-    int items = (int)(rows / slots);
-    items = getenv("ITEMS") ? atoi(getenv("ITEMS")) : items < 1 ? 1 : items > ITEMS ? ITEMS : items;
-    Q8K a;
-    int64_t blocks = 0;
-    for (int i = 0; i < p.np; ++i) {
-        a.w[i] = p.w[i];
-        a.y[i] = p.y[i];
-        a.n[i] = p.n[i];
-        a.blk0[i] = (int)blocks;
-        blocks += ((int64_t)p.n[i] + items * RPI - 1) / (items * RPI);
+    for (int t = 0; t < Q8_TYPES; ++t)
+        for (int i = 0; i < p[t].np; ++i)
+            rows += p[t].n[i];
+    // Workgroups a compute unit: what x costs each of them stands against what more
+    // waves hide.  Batch 1, 2 x 14336 x 4096 Q4_K: 1, 2, 3, 4 of them 14.8, 13.3, 14.3,
+    // 15.0 us; batch 5: 23.1, 26.4, 29.8, 33.0.
+    const int most = cus * (B <= 2 ? 2 : 1);
+    // rows of one segment: an item a block (more only where blocks would pass 32 bits)
+    int items = rows > (1 << 24) ? ITEMS : 1;
+    // of several: the waves of a row meet once in `items` of them (4096 x 14336 Q6_K, 1,
+    // 2, 4 items: 15.6, 14.3, 14.0 us)
+    if (MULTI)
+        items = rows / ((int64_t)most * groups) < 2 ? 1 : rows / ((int64_t)most * groups) < 4 ? 2 : 4;
+    Q8Call c;
+    const int bytes[Q8_TYPES] = {Q8Shape<T0, B, LP, MULTI>::SEGB, Q8Shape<T1, B, LP, MULTI>::SEGB,
+                                 Q8Shape<T2, B, LP, MULTI>::SEGB};
+    double cost[Q8_TYPES], all = 0;
+    int64_t wanted[Q8_TYPES];
+    for (int t = 0; t < Q8_TYPES; ++t) {
+        int64_t blocks = 0;
+        for (int i = 0; i < p[t].np; ++i) {
+            c.t[t].w[i] = p[t].w[i];
+            c.t[t].y[i] = p[t].y[i];
+            c.t[t].n[i] = p[t].n[i];
+            c.t[t].blk0[i] = (int)blocks;
+            blocks += ((int64_t)p[t].n[i] + items * RPI - 1) / (items * RPI);
+        }
+        c.t[t].np = p[t].np;
+        c.t[t].blk0[p[t].np] = (int)blocks;
+        wanted[t] = (blocks + groups - 1) / groups;
+        all += cost[t] = (double)blocks * bytes[t];
     }
-    a.blk0[p.np] = (int)blocks;
-    a.np = p.np;
-    const int64_t grid = (blocks + groups - 1) / groups;
-    return start(gemv_q8_kernel<T, B, LP, MULTI>, dim3((unsigned)(grid < cus * per_cu ? grid : cus * per_cu)),
-                 dim3(64 * sw * groups), s, a, x, k, batch, items, sw, groups);
+    // workgroups by the types' bytes
+    c.wg0[0] = 0;
+    for (int t = 0; t < Q8_TYPES; ++t) {
+        int64_t n = (int64_t)(most * (cost[t] / all) + 0.5);
+        n = n < 1 ? 1 : n;
+        c.wg0[t + 1] = c.wg0[t] + (int)(n < wanted[t] ? n : wanted[t]);
+    }
+    return start(gemv_q8_kernel<T0, T1, T2, B, LP, MULTI>, dim3(c.wg0[Q8_TYPES]), dim3(64 * sw * groups), s, c, x, k,
+                 batch, items, sw, groups);
 }
 
-template <int T, int B>
-hipError_t by_length(const Q8Probs &p, int k, const uint8_t *x, int batch, hipStream_t s)
+template <int T0, int T1, int T2, int B>
+hipError_t by_length(const Q8Probs (&p)[Q8_TYPES], int k, const uint8_t *x, int batch, hipStream_t s)
 {
-    const int units = k / GemvUnit<T>::UE;
-    return units > 64   ? run<T, B, 64, true>(p, k, x, batch, s)
-           : units > 32 ? run<T, B, 64, false>(p, k, x, batch, s)
-           : units > 16 ? run<T, B, 32, false>(p, k, x, batch, s)
-                        : run<T, B, 16, false>(p, k, x, batch, s);
-}
-
-template <int T>
-hipError_t by_batch(const Q8Probs &p, int k, const uint8_t *x, int batch, hipStream_t s)
-{
-    return batch == 1   ? by_length<T, 1>(p, k, x, batch, s)
-           : batch == 2 ? by_length<T, 2>(p, k, x, batch, s)
-           : batch <= 4 ? by_length<T, 4>(p, k, x, batch, s)
-                        : by_length<T, 8>(p, k, x, batch, s);
+    const int units = k / GemvUnit<T0>::UE;
+    return units > 64   ? run<T0, T1, T2, B, 64, true>(p, k, x, batch, s)
+           : units > 32 ? run<T0, T1, T2, B, 64, false>(p, k, x, batch, s)
+           : units > 16 ? run<T0, T1, T2, B, 32, false>(p, k, x, batch, s)
+                        : run<T0, T1, T2, B, 16, false>(p, k, x, batch, s);
 }
 
 }  // namespace
-
-hipError_t launch_gemv_q8(int type, const Q8Probs &p, int64_t k, size_t, const uint8_t *x, int batch, hipStream_t s)
-{
-    switch (type) {
-    case T_Q4_0: return by_batch<T_Q4_0>(p, (int)k, x, batch, s);
-    case T_Q8_0: return by_batch<T_Q8_0>(p, (int)k, x, batch, s);
-    case T_Q4_K: return by_batch<T_Q4_K>(p, (int)k, x, batch, s);
-    case T_Q6_K: return by_batch<T_Q6_K>(p, (int)k, x, batch, s);
-    case T_Q5_0: return by_batch<T_Q5_0>(p, (int)k, x, batch, s);
-    case T_Q5_K: return by_batch<T_Q5_K>(p, (int)k, x, batch, s);
-    default: return hipErrorInvalidValue;
-    }
-}
-
 }  // namespace qmm

@@ -14,16 +14,20 @@ hipError_t launch_trim(const int32_t *table, int64_t batch, int64_t columns, con
                        hipStream_t s);
 hipError_t launch_norm(const qst_norm_args &a, hipStream_t s);
 
-// Problems of one block type, n > 0 each, at most Q8_PROBS.
-constexpr int Q8_PROBS = 8;
+// Problems of one block type, n > 0 each, at most Q8_PROBS, and one launch's types: the
+// 32-element ones (Q4_0, Q8_0, Q5_0, in this order) or the 256-element ones (Q4_K, Q6_K,
+// Q5_K); one of them at least has a problem.  Batches 1 to 3 and 4 to 8 are apart.
+constexpr int Q8_PROBS = 8, Q8_TYPES = 3;
 struct Q8Probs {
     const uint8_t *w[Q8_PROBS];
     float *y[Q8_PROBS];
     int n[Q8_PROBS];
     int np;
 };
-hipError_t launch_gemv_q8(int type, const Q8Probs &p, int64_t k, size_t rb, const uint8_t *x, int batch,
-                          hipStream_t s);
+hipError_t launch_q8_small1(const Q8Probs (&p)[Q8_TYPES], int k, const uint8_t *x, int batch, hipStream_t s);
+hipError_t launch_q8_small2(const Q8Probs (&p)[Q8_TYPES], int k, const uint8_t *x, int batch, hipStream_t s);
+hipError_t launch_q8_large1(const Q8Probs (&p)[Q8_TYPES], int k, const uint8_t *x, int batch, hipStream_t s);
+hipError_t launch_q8_large2(const Q8Probs (&p)[Q8_TYPES], int k, const uint8_t *x, int batch, hipStream_t s);
 
 constexpr int LORA_TARGETS = 8;
 constexpr int LORA_RANK = 256;
