@@ -219,7 +219,7 @@ int qst_lora(const qst_lora_args *a, const qst_lora_target *targets, void *strea
     bool some = false;
     for (int i = 0; i < a->targets; ++i) {
         const qst_lora_target &t = targets[i];
-        if (t.n < 0 || t.n > INT_MOST)
+        if (t.n < 0 || t.n > (1 << 24))
             return QMM_ERR_SHAPE;
         if (t.n == 0 || a->tokens == 0 || a->batch == 0)
             continue;

@@ -173,6 +173,7 @@ QMM_API int qst_gemv_q8(int nprob, const qst_gemv_problem *probs, int64_t k, con
  * power of two (22 bits of a row's largest); everything is summed in fp32.
  * Values of x and of the weights used must be finite.
  * a: 16-byte aligned, k a multiple of 8; b: rank a multiple of 8, up to 256.
+ * At most 1048575 tokens, and n up to 2^24.
  */
 typedef struct qst_lora_target {
     const void *a;      /* fp16 [adapters][rank][k] */

@@ -157,7 +157,8 @@ def test_lora_refusals(q, step):
     assert call(dtype=2) == q.ERR_TYPE
     for kw in (dict(tokens=-1), dict(tokens=1 << 31), dict(batch=-1), dict(batch=65536), dict(k=0), dict(k=60),
                dict(k=1 << 31), dict(adapters=-1), dict(rank=0), dict(rank=12), dict(rank=264), dict(targets=-1),
-               dict(targets=9), dict(tokens=7), dict(x_stride=60), dict(t=[dict(n=-1)]), dict(t=[dict(n=1 << 31)])):
+               dict(targets=9), dict(tokens=7), dict(x_stride=60), dict(t=[dict(n=-1)]), dict(t=[dict(n=(1 << 24) + 1)]),
+               dict(tokens=1 << 20, batch=1 << 10)):
         assert call(**kw) == q.ERR_SHAPE, kw
     for kw in (dict(x=None), dict(adapter=None), dict(workspace=None), dict(t=[dict(a=None)]), dict(t=[{}, dict(b=None)]),
                dict(t=[dict(y=None)])):
