@@ -40,6 +40,7 @@ struct LoraK {
     int tokens, batch, k, adapters, rank, targets;
     int rank_tiles;            // of 16
     int splits, span;          // parts of k, each `span` long (a multiple of 128)
+    int out_cols;              // columns of y a workgroup: each one reads the inner sums again
     const _Float16 *a[LORA_TARGETS], *b[LORA_TARGETS];
     const float *base[LORA_TARGETS];
     float *y[LORA_TARGETS];
@@ -52,26 +53,59 @@ __device__ __forceinline__ int first_row(const LoraK &l, int b)
 }
 
 struct Tile {
-    int row0, rows;   // rows <= 0: none
-    int ad;           // its request's adapter, as given
+    int rows;         // of the tile; <= 0: none
+    int ad;           // the adapter, as given
+    int row;          // of the lane's column, lane % 16: the tile's row 16 wr + column, or its last
 };
 
-template <int ROWS> __device__ __forceinline__ Tile find_tile(const LoraK &l, int tau)
+// Tile `tau`'s rows.  SHARE (tiles of 16): requests of one row and the same adapter
+// among 64 neighbours meet, so that an adapter is read once for up to 16 of them: the
+// one that is first, 17th, 33rd or 49th of them takes the rows of the 16, the others'
+// tiles are empty.
+template <int ROWS, bool SHARE> __device__ __forceinline__ Tile find_tile(const LoraK &l, int tau, int wr)
 {
-    const int lane = threadIdx.x & 63;
+    const int lane = threadIdx.x & 63, i16 = lane & 15;
     int lo = 0, n = l.batch;          // the last request of [lo, lo + n) that begins at or before tau
-    while (n > 1) {
+    while (n > 64) {
         const int step = (n + 63) >> 6, b = lo + lane * step;
         const bool at = lane * step < n && first_row(l, b) / ROWS + b <= tau;
         const int last = max((int)__popcll(__ballot(at)) - 1, 0);
         lo = __builtin_amdgcn_readfirstlane(lo + last * step);
         n = __builtin_amdgcn_readfirstlane(min(step, n - last * step));
     }
-    const int from = first_row(l, lo), to = first_row(l, lo + 1), at = tau - (from / ROWS + lo);
+    // one request a lane, with all that is to be known of it
+    int b = lo + min(lane, n - 1), from = first_row(l, b), to = first_row(l, b + 1), ad = l.adapter[b];
+    const bool at = lane < n && from / ROWS + b <= tau;
+    int last = max((int)__popcll(__ballot(at)) - 1, 0);
     Tile t;
-    t.ad = l.adapter[lo];
-    t.row0 = from + at * ROWS;
-    t.rows = at < 0 ? 0 : min(ROWS, to - t.row0);
+    int f = __builtin_amdgcn_readlane(from, last);
+    const int i = tau - (f / ROWS + lo + last), row0 = f + i * ROWS;
+    t.ad = __builtin_amdgcn_readlane(ad, last);
+    t.rows = i < 0 ? 0 : min(ROWS, __builtin_amdgcn_readlane(to, last) - row0);
+    t.row = row0 + min(16 * wr + i16, t.rows - 1);
+    if (SHARE && i == 0 && __builtin_amdgcn_readlane(to, last) - f == 1 && t.ad >= 0 && t.ad < l.adapters) {
+        last += lo;
+        if (l.batch > 64) {           // the 64 neighbours, the same for each of them
+            lo = last & ~63;
+            n = min(64, l.batch - lo);
+            b = lo + min(lane, n - 1);
+            from = first_row(l, b);
+            to = first_row(l, b + 1);
+            ad = l.adapter[b];
+        }
+        last -= lo;
+        const uint64_t all = __ballot(lane < n && ad == t.ad && to - from == 1), below = (1ull << lane) - 1;
+        const int place = (int)__popcll(all & ((1ull << last) - 1)), count = (int)__popcll(all);
+        if (place % 16 != 0) {
+            t.rows = 0;
+            return t;
+        }
+        // the rows in order: lane j receives the j-th (the others follow behind)
+        const int mine = (all >> lane) & 1 ? (int)__popcll(all & below) : count + (int)__popcll(~all & below);
+        const int sorted = __builtin_amdgcn_ds_permute(4 * mine, from);
+        t.rows = min(16, count - place);
+        t.row = __builtin_amdgcn_ds_bpermute(4 * (place + min(i16, t.rows - 1)), sorted);
+    }
     return t;
 }
 
@@ -100,79 +134,192 @@ __device__ __forceinline__ f32x4 mma(const h16x8 &w, const F8 &x, f32x4 acc)
     return acc;
 }
 
+// s + the sum of a lane's eight products
+__device__ __forceinline__ float dot(const h16x8 &w, const F8 &x, float s)
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        s = __builtin_fmaf((float)w[j], j < 4 ? x.a[j & 3] : x.b[j & 3], s);
+    return s;
+}
+
 template <typename I> struct FragOf { typedef h16x8 type; };
 template <> struct FragOf<float> { typedef F8 type; };
 
-// The inner sums.  A workgroup of four waves: WR 4, a tile of 64 rows, 16 a wave, and
-// NC of the (target, 16 ranks) columns, for long requests, where x and the weights are
-// each read by as few as can be; WR 1, 16 rows and one column, the waves along k, for
-// few rows, where the loads in flight count.
-template <typename I, int WR, int NC>
+// The inner sums of few rows: a workgroup takes a tile of 16 rows and one column, a
+// target's 16 ranks; its four waves go along k, eight steps of loads in flight.
+template <typename I>
 __global__ void __launch_bounds__(256) lora_in_kernel(LoraK l)
 {
-    constexpr int KW = 4 / WR, U = NC == 1 ? 8 : NC <= 4 ? 4 : 2;   // U steps of 32 in flight
+    constexpr int U = 8;
     typedef typename FragOf<I>::type X;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const Tile t = find_tile<16 * WR>(l, blockIdx.x);
+    const Tile t = find_tile<16, true>(l, blockIdx.x, 0);
     if (t.rows <= 0 || t.ad < 0 || t.ad >= l.adapters)
         return;
-    const int wr = WR == 4 ? wave : 0, wk = WR == 4 ? 0 : wave;
     const int i16 = lane & 15, kg = lane >> 4;
-    if (16 * wr >= t.rows)
-        return;                       // (WR 4: no barrier below)
-    const int row = t.row0 + min(16 * wr + i16, t.rows - 1);
-    const int cols = l.targets * l.rank_tiles, c0 = blockIdx.y * NC;
-    const int k0 = blockIdx.z * l.span + wk * (l.span / KW), k1 = min(k0 + l.span / KW, l.k);
+    const int row = t.row;
+    const int tg = blockIdx.y / l.rank_tiles, r0 = 16 * (blockIdx.y - tg * l.rank_tiles);
+    const int k0 = blockIdx.z * l.span + wave * (l.span / 4), k1 = min(k0 + l.span / 4, l.k);
     const I *x = (const I *)l.x + row * l.xs + 8 * kg;
-    const _Float16 *a[NC];
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-        const int col = min(c0 + c, cols - 1), tg = col / l.rank_tiles, r0 = 16 * (col - tg * l.rank_tiles);
-        a[c] = l.a[tg] + ((int64_t)t.ad * l.rank + min(r0 + i16, l.rank - 1)) * l.k + 8 * kg;
-    }
-    f32x4 acc[NC];
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-        acc[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const _Float16 *a = l.a[tg] + ((int64_t)t.ad * l.rank + min(r0 + i16, l.rank - 1)) * l.k + 8 * kg;
+    __shared__ f32x4 part[3][64];
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
     int kk = k0;
+    if constexpr (sizeof(I) == 4) {
+        // One row of fp32: the matrix instruction of fp32 would work on 15 more that are
+        // not there, 8 of 32 cycles a step where 8 multiply-adds take 4 each (one token
+        // 9.2 -> 8.1 us).  Two to four rows by the products of 4 x 4 are no faster.
+        if (t.rows == 1) {
+            float s = 0.f;
+            for (; kk + 32 * U <= k1; kk += 32 * U) {
+                F8 xf[U];
+                h16x8 af[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    af[u] = frag(a + kk + 32 * u);
+                    xf[u] = frag(x + kk + 32 * u);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    s = dot(af[u], xf[u], s);
+            }
+            for (; kk < k1; kk += 32) {
+                const bool in = kk + 8 * kg < k1;
+                const int at = in ? kk : k1 - 8 - 8 * kg;
+                s = dot(only(frag(a + at), in), only(frag(x + at), in), s);
+            }
+            s += __shfl_xor(s, 16);
+            s += __shfl_xor(s, 32);
+            float *sums = (float *)part;
+            if (lane < 16)
+                sums[16 * wave + lane] = s;
+            __syncthreads();
+            if (threadIdx.x < 16 && r0 + i16 < l.rank)
+                l.h[(((int64_t)blockIdx.z * l.targets + tg) * l.tokens + row) * l.rank + r0 + i16] =
+                    (sums[i16] + sums[16 + i16]) + (sums[32 + i16] + sums[48 + i16]);
+            return;
+        }
+    }
     for (; kk + 32 * U <= k1; kk += 32 * U) {
         X xf[U];
-        h16x8 af[U][NC];
+        h16x8 af[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
+            af[u] = frag(a + kk + 32 * u);
             xf[u] = frag(x + kk + 32 * u);
-#pragma unroll
-            for (int c = 0; c < NC; ++c)
-                af[u][c] = frag(a[c] + kk + 32 * u);
         }
+        __builtin_amdgcn_sched_barrier(0);     // all of them asked for before the first product
 #pragma unroll
         for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int c = 0; c < NC; ++c)
-                acc[c] = mma(af[u][c], xf[u], acc[c]);
+            acc = mma(af[u], xf[u], acc);
     }
     for (; kk < k1; kk += 32) {
         // the last step may end inside: k is a multiple of 8, so a lane's part is whole
         const bool in = kk + 8 * kg < k1;
         const int at = in ? kk : k1 - 8 - 8 * kg;
-        const X xf = only(frag(x + at), in);
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-            acc[c] = mma(only(frag(a[c] + at), in), xf, acc[c]);
+        acc = mma(only(frag(a + at), in), only(frag(x + at), in), acc);
     }
-    if constexpr (WR == 1) {
-        __shared__ f32x4 part[3][64];
-        if (wave > 0)
-            part[wave - 1][lane] = acc[0];
-        __syncthreads();
-        if (wave > 0)
-            return;
-#pragma unroll
-        for (int i = 0; i < 3; ++i)
-            acc[0] += part[i][lane];
-    }
-    if (16 * wr + i16 >= t.rows)
+    if (wave > 0)
+        part[wave - 1][lane] = acc;
+    __syncthreads();
+    if (wave > 0 || i16 >= t.rows)
         return;
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+        acc += part[i][lane];
+    const int r = r0 + 4 * kg;
+    if (r < l.rank)
+        *(f32x4 *)(l.h + (((int64_t)blockIdx.z * l.targets + tg) * l.tokens + row) * l.rank + r) = acc;
+}
+
+// The inner sums of long requests: a tile of 64 rows, 16 a wave, and NC columns (16
+// ranks of a target each).  x and the weights pass through LDS, KS of k at a time, in
+// runs of 256 bytes (fragments taken straight from rows that lie kilobytes apart cost
+// the caches 16 lines an instruction, and every wave its own read of the weights), the
+// next part in registers while one is multiplied.  Workgroups start at different parts,
+// since rows a power of two apart would have all ask the same channels at once.
+template <typename I, int NC>
+__global__ void __launch_bounds__(256) lora_in_wide_kernel(LoraK l)
+{
+    constexpr int KS = 256 / sizeof(I);                       // 128, fp32 64
+    constexpr int XP = KS + 16 / sizeof(I), AP = KS + 8;      // elements between rows in LDS: a run and 16 bytes
+    constexpr int AC = KS / 8;                                // 16-byte chunks of a weight row
+    constexpr int NX = 4, NA = NC * 16 * AC / 256;            // chunks a thread
+    __shared__ __align__(16) I xs[64 * XP];
+    __shared__ __align__(16) _Float16 as[NC * 16 * AP];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const Tile t = find_tile<64, false>(l, blockIdx.x, 0);
+    const int row0 = __builtin_amdgcn_readfirstlane(t.row);
+    if (t.rows <= 0 || t.ad < 0 || t.ad >= l.adapters)
+        return;
+    const int i16 = lane & 15, kg = lane >> 4;
+    const int cols = l.targets * l.rank_tiles, c0 = blockIdx.y * NC;
+    const int k0 = blockIdx.z * l.span, k1 = min(k0 + l.span, l.k), steps = (k1 - k0 + KS - 1) / KS;
+    const I *xp[NX];
+    const _Float16 *ap[NA];
+    constexpr int XC = 16 / sizeof(I);                        // elements of a chunk of x
+#pragma unroll
+    for (int j = 0; j < NX; ++j) {
+        const int id = tid + 256 * j;
+        xp[j] = (const I *)l.x + (row0 + min(id / 16, t.rows - 1)) * l.xs;
+    }
+#pragma unroll
+    for (int j = 0; j < NA; ++j) {
+        const int r = (tid + 256 * j) / AC, col = min(c0 + r / 16, cols - 1), tg = col / l.rank_tiles;
+        ap[j] = l.a[tg] + ((int64_t)t.ad * l.rank + min(16 * (col - tg * l.rank_tiles) + r % 16, l.rank - 1)) * l.k;
+    }
+    u32x4 px[NX], pa[NA];
+    auto load = [&](int kk) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < NX; ++j) {
+            const int at = kk + XC * ((tid + 256 * j) % 16);
+            px[j] = *(const u32x4 *)(xp[j] + min(at, l.k - XC));
+        }
+#pragma unroll
+        for (int j = 0; j < NA; ++j) {
+            const int at = kk + 8 * ((tid + 256 * j) % AC);
+            pa[j] = *(const u32x4 *)(ap[j] + min(at, l.k - 8));
+        }
+    };
+    auto store = [&](int kk) __attribute__((always_inline)) {
+        // zeros past the end of this part of k, on both sides
+#pragma unroll
+        for (int j = 0; j < NX; ++j) {
+            const int id = tid + 256 * j, at = XC * (id % 16);
+            *(u32x4 *)(xs + id / 16 * XP + at) = kk + at < k1 ? px[j] : u32x4{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int j = 0; j < NA; ++j) {
+            const int id = tid + 256 * j, at = 8 * (id % AC);
+            *(u32x4 *)(as + id / AC * AP + at) = kk + at < k1 ? pa[j] : u32x4{0, 0, 0, 0};
+        }
+    };
+    f32x4 acc[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+        acc[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+    int at = (int)(blockIdx.x % (uint32_t)steps);
+    load(k0 + at * KS);
+    for (int i = 0; i < steps; ++i) {
+        store(k0 + at * KS);
+        at = at + 1 == steps ? 0 : at + 1;
+        lds_barrier();
+        if (i + 1 < steps)
+            load(k0 + at * KS);
+#pragma unroll
+        for (int u = 0; u < KS / 32; ++u) {
+            const auto xf = frag(xs + (16 * wave + i16) * XP + 32 * u + 8 * kg);
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+                acc[c] = mma(frag(as + (16 * c + i16) * AP + 32 * u + 8 * kg), xf, acc[c]);
+        }
+        lds_barrier();
+    }
+    if (16 * wave + i16 >= t.rows)
+        return;
+    const int row = row0 + 16 * wave + i16;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
         const int col = c0 + c, tg = col / l.rank_tiles, r = 16 * (col - tg * l.rank_tiles) + 4 * kg;
@@ -181,40 +328,41 @@ __global__ void __launch_bounds__(256) lora_in_kernel(LoraK l)
     }
 }
 
-constexpr int OUT_COLS = 256;   // columns of y a workgroup
+constexpr int TURN = 68;        // floats between rows in LDS: 64 and a bank's shift
 
-// The outputs: OUT_COLS columns of a tile's rows.  NK steps of 32 ranks.
+// The outputs: some columns of a tile's rows.  NK steps of 32 ranks.
 template <int WR, int NK>
 __global__ void __launch_bounds__(256) lora_out_kernel(LoraK l)
 {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int tg = blockIdx.z, n = l.n[tg], j0 = blockIdx.y * OUT_COLS;
+    const int tg = blockIdx.z, n = l.n[tg], j0 = blockIdx.y * l.out_cols;
     if (j0 >= n)
         return;
-    const Tile t = find_tile<16 * WR>(l, blockIdx.x);
+    const int wr = WR == 4 ? wave : 0;
+    const Tile t = find_tile<16 * WR, WR == 1>(l, blockIdx.x, wr);
     if (t.rows <= 0)
         return;
     const float *base = l.base[tg] ? l.base[tg] : l.y[tg];
     float *y = l.y[tg];
     if (t.ad < 0 || t.ad >= l.adapters) {
+        // (such tiles are a request's own rows)
+        const int row0 = __builtin_amdgcn_readfirstlane(t.row) - (WR == 4 ? min(16 * wr, t.rows - 1) : 0);
         if (base != y)
-            for (int i = threadIdx.x; i < t.rows * OUT_COLS; i += 256) {
-                const int j = j0 + i % OUT_COLS;
-                const int64_t at = (int64_t)(t.row0 + i / OUT_COLS) * n + j;
+            for (int i = threadIdx.x; i < t.rows * l.out_cols; i += 256) {
+                const int j = j0 + i % l.out_cols;
+                const int64_t at = (int64_t)(row0 + i / l.out_cols) * n + j;
                 if (j < n)
                     y[at] = base[at];
             }
         return;
     }
-    const int wr = WR == 4 ? wave : 0;
     const int i16 = lane & 15, kg = lane >> 4;
     if (16 * wr >= t.rows)
         return;
-    const bool mine = 16 * wr + i16 < t.rows;
-    const int row = t.row0 + min(16 * wr + i16, t.rows - 1);
+    const int row = t.row;
     const int live = rank_of(l, t.ad);
     const float scale = l.scale ? l.scale[t.ad] : 1.f;
-    const int most = min(j0 + OUT_COLS, n);
+    const int most = min(j0 + l.out_cols, n);
 
     // h of the lane's row, ranks 32 c + 8 kg .. + 7, and what of them counts
     float h[NK][8];
@@ -231,6 +379,7 @@ __global__ void __launch_bounds__(256) lora_out_kernel(LoraK l)
         for (int i = 0; i < 8; ++i)
             h[c][i] = 0.f;
     }
+#pragma unroll 4
     for (int z = 0; z < l.splits; ++z)
 #pragma unroll
         for (int c = 0; c < NK; ++c) {
@@ -260,43 +409,88 @@ __global__ void __launch_bounds__(256) lora_out_kernel(LoraK l)
             lo[c][i] = (_Float16)(v - (float)hi[c][i]);
         }
 
+    // 64 columns at a time: four products of 16, whose results pass through the wave's
+    // part of LDS, so that y is read and written in runs of 256 bytes
     const bool vec = (n & 3) == 0;
     const _Float16 *b = l.b[tg] + (int64_t)t.ad * n * l.rank;
-    for (int j = j0 + (WR == 4 ? 0 : 16 * wave); j < most; j += WR == 4 ? 16 : 64) {
-        const _Float16 *p = b + (int64_t)min(j + i16, n - 1) * l.rank;
-        const int jj = j + 4 * kg;
-        const int64_t to = (int64_t)row * n + jj;
-        h16x8 w[NK];
+    const int rows = t.rows - 16 * wr;
+    __shared__ __align__(16) float turn[4][16 * TURN];
+    float *mine = turn[wave];
+    int64_t to_row[4];                // rows 4 p + kg of the wave's, in y
 #pragma unroll
-        for (int c = 0; c < NK; ++c)
-            w[c] = __builtin_bit_cast(h16x8, *(const u32x4 *)(p + at[c]) & mask[c]);
-        f32x4 old = {0.f, 0.f, 0.f, 0.f};
-        if (mine) {
-            if (vec && jj < n) {
-                old = *(const f32x4 *)(base + to);
-            } else {
+    for (int p = 0; p < 4; ++p)
+        to_row[p] = (int64_t)__shfl(row, 4 * p + kg) * n;
+    for (int j = j0 + (WR == 4 ? 0 : 64 * wave); j < most; j += WR == 4 ? 64 : 256) {
+        // (high ranks: their 16 columns' weights one product at a time, for the registers)
+        constexpr int QS = NK <= 2 ? 4 : 1;
+        h16x8 w[QS][NK];
+        auto weights = [&](int q, h16x8 *to) __attribute__((always_inline)) {
+            const _Float16 *p = b + (int64_t)min(j + 16 * q + i16, n - 1) * l.rank;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    old[i] = jj + i < n ? base[to + i] : 0.f;
-            }
+            for (int c = 0; c < NK; ++c)
+                to[c] = __builtin_bit_cast(h16x8, *(const u32x4 *)(p + at[c]) & mask[c]);
+        };
+        if constexpr (QS == 4) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                weights(q, w[q]);
         }
-        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+        // y: rows 4 p + kg of the wave's, columns j + 4 i16 .. + 3
+        const int jj = j + 4 * i16;
+        f32x4 old[4];
 #pragma unroll
-        for (int c = 0; c < NK; ++c) {
-            acc = mma(w[c], lo[c], acc);
-            acc = mma(w[c], hi[c], acc);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            old[i] = __builtin_fmaf(__builtin_ldexpf(acc[i], -e), scale, old[i]);
-        if (mine) {
-            if (vec && jj < n) {
-                *(f32x4 *)(y + to) = old;
+        for (int p = 0; p < 4; ++p) {
+            const int64_t to = to_row[p] + jj;
+            old[p] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (4 * p + kg >= rows)
+                continue;
+            if (vec) {
+                if (jj < n)
+                    old[p] = *(const f32x4 *)(base + to);
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (jj + i < n)
-                        y[to + i] = old[i];
+                        old[p][i] = base[to + i];
+            }
+        }
+#pragma unroll QS
+        for (int q = 0; q < 4; ++q) {
+            if constexpr (QS == 1)
+                weights(q, w[0]);
+            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < NK; ++c) {
+                acc = mma(w[QS == 4 ? q : 0][c], lo[c], acc);
+                acc = mma(w[QS == 4 ? q : 0][c], hi[c], acc);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                acc[i] = __builtin_ldexpf(acc[i], -e);
+            *(f32x4 *)(mine + i16 * TURN + 16 * q + 4 * kg) = acc;
+        }
+        wave_lds_sync();
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const f32x4 d = *(const f32x4 *)(mine + (4 * p + kg) * TURN + 4 * i16);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                old[p][i] = __builtin_fmaf(d[i], scale, old[p][i]);
+        }
+        wave_lds_sync();
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const int64_t to = to_row[p] + jj;
+            if (4 * p + kg >= rows)
+                continue;
+            if (vec) {
+                if (jj < n)
+                    *(f32x4 *)(y + to) = old[p];
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (jj + i < n)
+                        y[to + i] = old[p][i];
             }
         }
     }
@@ -316,11 +510,14 @@ Cut cut(const qst_lora_args &a)
     c.tiles = (int)(a.tokens / (c.wide ? 64 : 16) + a.batch);
     c.rank_tiles = (a.rank + 15) / 16;
     c.cols = a.targets * c.rank_tiles;
-    c.nc = !c.wide ? 1 : c.cols <= 2 ? 2 : c.cols <= 4 ? 4 : 8;
-    // parts of k: 1024 workgroups, a wave with 256 of k at least
+    const int passes = c.cols > 8 ? (c.cols + 7) / 8 : 1, each = (c.cols + passes - 1) / passes;
+    c.nc = !c.wide ? 1 : each <= 2 ? 2 : each <= 4 ? 4 : each <= 6 ? 6 : 8;
+    // parts of k: 512 workgroups (tiles of 16, many of which are empty: 1024), 1024 of k at least (a chunk of 512 rows, 256, 512, 1024
+    // and 2048 of k: 29.0, 23.5, 24.2, 31.0 us: each part's sums are read again by every
+    // workgroup of the outputs; one token: 512, 1024, 2048: 7.5, 7.7, 9.0)
     const int64_t groups = (int64_t)c.tiles * ((c.cols + c.nc - 1) / c.nc);
-    const int64_t least = c.wide ? 256 : 1024;
-    const int64_t most = (a.k + least - 1) / least, want = groups > 0 ? (1024 + groups - 1) / groups : 1;
+    const int64_t least = 1024;
+    const int64_t most = (a.k + least - 1) / least, goal = c.wide ? 512 : 1024, want = groups > 0 ? (goal + groups - 1) / groups : 1;
     int64_t s = want < most ? want : most;
     s = s < 1 ? 1 : s > 64 ? 64 : s;
     c.span = (int)(((a.k + s - 1) / s + 127) / 128 * 128);
@@ -333,16 +530,17 @@ hipError_t inner(const LoraK &k, const Cut &c, hipStream_t s)
 {
     const dim3 grid(c.tiles, (c.cols + c.nc - 1) / c.nc, c.splits), block(256);
     if (!c.wide)
-        return start(lora_in_kernel<I, 1, 1>, grid, block, s, k);
-    return c.nc == 2   ? start(lora_in_kernel<I, 4, 2>, grid, block, s, k)
-           : c.nc == 4 ? start(lora_in_kernel<I, 4, 4>, grid, block, s, k)
-                       : start(lora_in_kernel<I, 4, 8>, grid, block, s, k);
+        return start(lora_in_kernel<I>, grid, block, s, k);
+    return c.nc == 2   ? start(lora_in_wide_kernel<I, 2>, grid, block, s, k)
+           : c.nc == 4 ? start(lora_in_wide_kernel<I, 4>, grid, block, s, k)
+           : c.nc == 6 ? start(lora_in_wide_kernel<I, 6>, grid, block, s, k)
+                       : start(lora_in_wide_kernel<I, 8>, grid, block, s, k);
 }
 
 template <int WR>
 hipError_t outer(const LoraK &k, int tiles, int n, hipStream_t s)
 {
-    const dim3 grid(tiles, (n + OUT_COLS - 1) / OUT_COLS, k.targets), block(256);
+    const dim3 grid(tiles, (n + k.out_cols - 1) / k.out_cols, k.targets), block(256);
     return k.rank <= 32    ? start(lora_out_kernel<WR, 1>, grid, block, s, k)
            : k.rank <= 64  ? start(lora_out_kernel<WR, 2>, grid, block, s, k)
            : k.rank <= 128 ? start(lora_out_kernel<WR, 4>, grid, block, s, k)
@@ -360,7 +558,7 @@ hipError_t launch_lora(const qst_lora_args &a, const qst_lora_target *t, hipStre
 {
     const Cut c = cut(a);
     LoraK k{a.x, a.adapter, a.qstart, a.scale, a.ranks, (float *)a.workspace, a.x_stride, (int)a.tokens, (int)a.batch,
-            (int)a.k, a.adapters, a.rank, a.targets, c.rank_tiles, c.splits, c.span, {}, {}, {}, {}, {}};
+            (int)a.k, a.adapters, a.rank, a.targets, c.rank_tiles, c.splits, c.span, 256, {}, {}, {}, {}, {}};
     int most = 0;
     for (int i = 0; i < a.targets; ++i) {
         k.a[i] = (const _Float16 *)t[i].a;
@@ -369,6 +567,16 @@ hipError_t launch_lora(const qst_lora_args &a, const qst_lora_target *t, hipStre
         k.y[i] = t[i].y;
         k.n[i] = (int)t[i].n;
         most = k.n[i] > most ? k.n[i] : most;
+    }
+    // tiles of 64 rows, a wave 16 of them: 512 columns where that leaves enough workgroups
+    // (prompts of 6653 rows, three targets: 512 columns 76 us, 256 86), down to 64
+    if (c.wide) {
+        int64_t all = 0;
+        for (int i = 0; i < a.targets; ++i)
+            all += t[i].n;
+        k.out_cols = 512;
+        while (k.out_cols > 64 && c.tiles * all / k.out_cols < 1024)
+            k.out_cols /= 2;
     }
     if (a.adapters > 0) {
         const hipError_t e = a.dtype == QKV_HALF ? inner<_Float16>(k, c, s) : inner<float>(k, c, s);

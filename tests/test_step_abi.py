@@ -178,6 +178,8 @@ def test_lora_workspace_looks_at_sizes_alone(q, step):
     assert q.lib.qst_lora_workspace(ctypes.addressof(a)) > 0
     assert q.lib.qst_lora_workspace(ctypes.addressof(lora_args(step, rank=4))) == -1
     assert q.lib.qst_lora_workspace(None) == -1
+    for kw in (dict(targets=0), dict(tokens=0), dict(batch=0), dict(adapters=0)):
+        assert q.lib.qst_lora_workspace(ctypes.addressof(lora_args(step, **kw))) >= 0
 
 
 # ---------------------------------------------------------------- the binding --
