@@ -14,10 +14,12 @@ As the rest of the binding this module only checks and marshals arguments.
 from __future__ import annotations
 
 import ctypes
+import functools
+import struct
 
 import torch
 
-from . import _call, _check_w, _I, _I64, _launch, _out, _P, Q8_0, lib, row_bytes
+from . import _call, _I, _I64, _launch, _P, Q8_0, lib, row_bytes
 
 _I32C = ctypes.c_int32
 SIGNATURES = {
@@ -64,27 +66,38 @@ class LoraArgs(ctypes.Structure):
         + [(n, _I32C) for n in ("adapters", "rank", "dtype", "targets")]
 
 
+# These calls cost the host about as much as their kernels: the structs above are
+# written as bytes (a pointer that is not given is 0), one condition checks a tensor,
+# and its message is only made when it fails.
+_PLAN, _NORM = struct.Struct("@15q"), struct.Struct("@12qf3i")
+_PROBLEM, _TARGET, _LORA = struct.Struct("@3q2i"), struct.Struct("@5q"), struct.Struct("@11q4i")
+
 _F32, _F16, _I32, _U8 = torch.float32, torch.float16, torch.int32, torch.uint8
 _DTYPES = {_F32: 0, _F16: 1}
 _OUT_Q8 = 16 + Q8_0
+_row_bytes = functools.lru_cache(maxsize=4096)(row_bytes)
 
 
 def _ints(t, what, device, shape):
-    if t.dtype is not _I32 or t.device != device or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype is not _I32 or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError("%s must be a contiguous int32 tensor of shape %s on %s" % (what, shape, device))
+
+
+def _tensor(t, what, device, dtype, shape):
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s" % (what, dtype, shape, device))
 
 
 def _pool(table, free, count):
     """(device, batch, columns, pages) of a table and its pool, checked."""
-    dev = table.device
-    if not table.is_cuda or table.dim() != 2 or free.dim() != 1:
+    dev, size = table.device, table.shape
+    if not table.is_cuda or len(size) != 2 or len(free.shape) != 1:
         raise ValueError("table must be a device tensor [batch, columns] and free [pages]")
-    B, cols = table.shape
     pages = free.shape[0]
-    _ints(table, "table", dev, (B, cols))
+    _ints(table, "table", dev, size)
     _ints(free, "free", dev, (pages,))
     _ints(count, "count", dev, (1,))
-    return dev, B, cols, pages
+    return dev, size[0], size[1], pages
 
 
 def kv_plan(table, ctx, fresh, free, count, tokens, page_size=64, out=None):
@@ -102,15 +115,18 @@ def kv_plan(table, ctx, fresh, free, count, tokens, page_size=64, out=None):
     _ints(ctx, "ctx", dev, (B,))
     if fresh is not None:
         _ints(fresh, "fresh", dev, (B,))
-    shapes = ((B + 1,), (tokens,), (tokens,), (B,), (1,))
     if out is None:
-        out = tuple(torch.empty(s, dtype=_I32, device=dev) for s in shapes)
+        out = (torch.empty(B + 1, dtype=_I32, device=dev), torch.empty(tokens, dtype=_I32, device=dev),
+               torch.empty(tokens, dtype=_I32, device=dev), torch.empty(B, dtype=_I32, device=dev),
+               torch.empty(1, dtype=_I32, device=dev))
     else:
-        for t, s, name in zip(out, shapes, ("qstart", "slots", "pos", "granted", "left")):
-            _ints(t, name, dev, s)
-    a = PlanArgs(table.data_ptr(), ctx.data_ptr(), fresh.data_ptr() if fresh is not None else None, free.data_ptr(),
-                 count.data_ptr(), *[t.data_ptr() for t in out], B, cols, pages, page_size, tokens)
-    status = _launch(lib.qst_plan, dev, ctypes.addressof(a))
+        for t, n, name in zip(out, (B + 1, tokens, tokens, B, 1), ("qstart", "slots", "pos", "granted", "left")):
+            _ints(t, name, dev, (n,))
+    qstart, slots, pos, granted, left = out
+    a = _PLAN.pack(table.data_ptr(), ctx.data_ptr(), fresh.data_ptr() if fresh is not None else 0, free.data_ptr(),
+                   count.data_ptr(), qstart.data_ptr(), slots.data_ptr(), pos.data_ptr(), granted.data_ptr(),
+                   left.data_ptr(), B, cols, pages, page_size, tokens)
+    status = _launch(lib.qst_plan, dev, a)
     if status:
         _call(status, "qst_plan")
     return out
@@ -169,13 +185,17 @@ def rms_norm(x, weight=None, residual=None, eps=1e-6, dtype=None, qtype=None, su
         scode, ss = _values(sum_out, "sum_out", shape, dev)
         if scode != rcode:
             raise ValueError("sum_out must have the residual's type (without one: x's)")
-    if weight is not None and (weight.dtype is not _F32 or tuple(weight.shape) != (D,) or weight.device != dev
+    if weight is not None and (weight.dtype is not _F32 or weight.shape != (D,) or weight.device != dev
                                or not weight.is_contiguous()):
         raise ValueError("weight must be a contiguous float32 tensor [%d] on %s" % (D, dev))
     if qtype is not None:
         if qtype != Q8_0 or dtype is not None or D % 32:
             raise ValueError("qtype must be Q8_0, dim a multiple of 32 and dtype None")
-        out = _out(out, (T, row_bytes(Q8_0, H * D)), _U8, dev)
+        shape = (T, _row_bytes(Q8_0, H * D))
+        if out is None:
+            out = torch.empty(shape, dtype=_U8, device=dev)
+        else:
+            _tensor(out, "out", dev, _U8, shape)
         ocode, os_ = _OUT_Q8, 0
     else:
         if out is None:
@@ -183,10 +203,10 @@ def rms_norm(x, weight=None, residual=None, eps=1e-6, dtype=None, qtype=None, su
         ocode, os_ = _values(out, "out", shape, dev)
         if dtype is not None and out.dtype is not dtype:
             raise ValueError("out must be of type %s" % dtype)
-    a = NormArgs(x.data_ptr(), residual.data_ptr() if residual is not None else None,
-                 sum_out.data_ptr() if sum_out is not None else None, weight.data_ptr() if weight is not None else None,
-                 out.data_ptr(), xs, rs, ss, os_, T, H, D, eps, code, rcode, ocode)
-    status = _launch(lib.qst_norm, dev, ctypes.addressof(a))
+    a = _NORM.pack(x.data_ptr(), residual.data_ptr() if residual is not None else 0,
+                   sum_out.data_ptr() if sum_out is not None else 0, weight.data_ptr() if weight is not None else 0,
+                   out.data_ptr(), xs, rs, ss, os_, T, H, D, eps, code, rcode, ocode)
+    status = _launch(lib.qst_norm, dev, a)
     if status:
         _call(status, "qst_norm")
     return out if residual is None else (out, sum_out)
@@ -198,24 +218,23 @@ def gemv_q8_multi(ws, qtypes, ns, k, x, outs=None):
     outputs [B, n_i]."""
     if not len(ws) == len(qtypes) == len(ns):
         raise ValueError("ws, qtypes and ns must have the same length")
-    dev = x.device
-    if x.dtype is not _U8 or not x.is_cuda or x.dim() != 2 or not x.is_contiguous() \
-            or x.shape[1] != row_bytes(Q8_0, k) or k % 32:
-        raise ValueError("x must be a contiguous uint8 device tensor [B, %d] of Q8_0 blocks" % row_bytes(Q8_0, k))
-    B, n_probs = x.shape[0], len(ws)
+    dev, size = x.device, x.shape
+    if x.dtype is not _U8 or not x.is_cuda or len(size) != 2 or k % 32 or size[1] != _row_bytes(Q8_0, k) \
+            or not x.is_contiguous():
+        raise ValueError("x must be a contiguous uint8 device tensor [B, row_bytes(Q8_0, %d)] of Q8_0 blocks" % k)
+    B, n_probs = size[0], len(ws)
     if outs is None:
         outs = [None] * n_probs
     if len(outs) != n_probs:
         raise ValueError("outs must have one tensor per problem")
-    for w, t, n in zip(ws, qtypes, ns):
-        _check_w(w, t, n, k)
-        if w.device != dev:
-            raise ValueError("x and the weights must be on the same device")
-    outs = [_out(o, (B, n), _F32, dev) for o, n in zip(outs, ns)]
-    probs = (GemvProblem * max(n_probs, 1))()
-    for i, (w, t, n, o) in enumerate(zip(ws, qtypes, ns, outs)):
-        probs[i] = GemvProblem(w.data_ptr(), o.data_ptr(), n, t, 0)
-    status = _launch(lib.qst_gemv_q8, dev, n_probs, ctypes.addressof(probs), k, x.data_ptr(), B)
+    for w, t, n, o in zip(ws, qtypes, ns, outs):
+        if w.dtype is not _U8 or w.device != dev or not w.is_contiguous() or w.numel() != n * _row_bytes(t, k):
+            raise ValueError("weights must be contiguous uint8 tensors of n * row_bytes bytes on %s" % dev)
+        if o is not None:
+            _tensor(o, "outs", dev, _F32, (B, n))
+    outs = [torch.empty((B, n), dtype=_F32, device=dev) if o is None else o for o, n in zip(outs, ns)]
+    probs = b"".join([_PROBLEM.pack(w.data_ptr(), o.data_ptr(), n, t, 0) for w, t, n, o in zip(ws, qtypes, ns, outs)])
+    status = _launch(lib.qst_gemv_q8, dev, n_probs, probs, k, x.data_ptr(), B)
     if status:
         _call(status, "qst_gemv_q8")
     return outs
@@ -226,50 +245,54 @@ def gemv_q8(w, qtype, n, k, x, out=None):
     return gemv_q8_multi([w], [qtype], [n], k, x, outs=None if out is None else [out])[0]
 
 
-def _lora(x, targets, adapter, qstart, scale, ranks):
-    """(qst_lora_args without workspace, its targets) of a call, checked."""
-    dev = x.device
+def _lora(x, targets, adapter, qstart, scale, ranks, workspace):
+    """(qst_lora_args, its targets) of a call as bytes, checked."""
+    dev, size, stride = x.device, x.shape, x.stride()
     code = _DTYPES.get(x.dtype)
-    if code is None or not x.is_cuda or x.dim() != 2 or (x.stride(1) != 1 and x.shape[1] > 1):
+    if code is None or not x.is_cuda or len(size) != 2 or (stride[1] != 1 and size[1] > 1):
         raise ValueError("x must be a float32 or float16 device tensor [tokens, k] with contiguous rows")
-    if adapter.dim() != 1:
+    if len(adapter.shape) != 1:
         raise ValueError("adapter must have one entry per request")
-    T, k = x.shape
+    T, k = size
     B = adapter.shape[0]
     _ints(adapter, "adapter", dev, (B,))
     if qstart is not None:
         _ints(qstart, "qstart", dev, (B + 1,))
-    tab = (LoraTarget * max(len(targets), 1))()
-    n_ad, rank = (targets[0][0].shape[0], targets[0][0].shape[1]) if targets else (0, 8)
-    for i, t in enumerate(targets):
-        a, b, y, base = t if len(t) == 4 else (*t, None)
+    n_ad, rank = targets[0][0].shape[:2] if targets else (0, 8)
+    tab = []
+    for t in targets:
+        a, b, y = t[:3]
+        base = t[3] if len(t) > 3 else None
         n = y.shape[-1]
-        for m, what, shape in ((a, "a", (n_ad, rank, k)), (b, "b", (n_ad, n, rank))):
-            if m.dtype is not _F16 or m.device != dev or tuple(m.shape) != shape or not m.is_contiguous():
-                raise ValueError("%s of target %d must be a contiguous float16 tensor %s on %s" % (what, i, shape, dev))
-        _out(y, (T, n), _F32, dev)
+        _tensor(a, "a", dev, _F16, (n_ad, rank, k))
+        _tensor(b, "b", dev, _F16, (n_ad, n, rank))
+        _tensor(y, "y", dev, _F32, (T, n))
         if base is not None:
-            _out(base, (T, n), _F32, dev)
-        tab[i] = LoraTarget(a.data_ptr(), b.data_ptr(), base.data_ptr() if base is not None else None, y.data_ptr(), n)
-    if scale is not None and (scale.dtype is not _F32 or scale.device != dev or tuple(scale.shape) != (n_ad,)
-                              or not scale.is_contiguous()):
-        raise ValueError("scale must be a contiguous float32 tensor [%d] on %s" % (n_ad, dev))
+            _tensor(base, "base", dev, _F32, (T, n))
+        tab.append(_TARGET.pack(a.data_ptr(), b.data_ptr(), base.data_ptr() if base is not None else 0, y.data_ptr(), n))
+    if scale is not None:
+        _tensor(scale, "scale", dev, _F32, (n_ad,))
     if ranks is not None:
         _ints(ranks, "ranks", dev, (n_ad,))
-    return LoraArgs(x.data_ptr(), adapter.data_ptr(), qstart.data_ptr() if qstart is not None else None,
-                    scale.data_ptr() if scale is not None else None, ranks.data_ptr() if ranks is not None else None,
-                    None, 0, x.stride(0), T, B, k, n_ad, rank, code, len(targets)), tab
+    ws, ws_bytes = (workspace.data_ptr(), workspace.numel()) if workspace is not None else (0, 0)
+    return _LORA.pack(x.data_ptr(), adapter.data_ptr(), qstart.data_ptr() if qstart is not None else 0,
+                      scale.data_ptr() if scale is not None else 0, ranks.data_ptr() if ranks is not None else 0, ws,
+                      ws_bytes, stride[0], T, B, k, n_ad, rank, code, len(targets)), b"".join(tab)
+
+
+def _workspace(x, targets, a):
+    with torch.cuda.device(x.device):
+        n = lib.qst_lora_workspace(a)
+    if n < 0:
+        raise ValueError("no adapters of these sizes: x %s, %d targets, first a %s"
+                         % (tuple(x.shape), len(targets), tuple(targets[0][0].shape) if targets else None))
+    return torch.empty(n, dtype=_U8, device=x.device)
 
 
 def lora_workspace(x, targets, adapter):
     """A workspace tensor for lora() calls of these sizes (one call at a time may
     use it)."""
-    a, _ = _lora(x, targets, adapter, None, None, None)
-    with torch.cuda.device(x.device):
-        n = lib.qst_lora_workspace(ctypes.addressof(a))
-    if n < 0:
-        raise ValueError("no adapters of these sizes: x %s, rank %d, %d targets" % (tuple(x.shape), a.rank, a.targets))
-    return torch.empty(n, dtype=_U8, device=x.device)
+    return _workspace(x, targets, _lora(x, targets, adapter, None, None, None, None)[0])
 
 
 def lora(x, targets, adapter, qstart=None, scale=None, ranks=None, workspace=None):
@@ -281,13 +304,12 @@ def lora(x, targets, adapter, qstart=None, scale=None, ranks=None, workspace=Non
     [batch]: each request's, or -1; qstart int32 [batch + 1] first rows of the
     requests (None: equal shares).  scale float32 and ranks int32 [adapters]
     (None: 1, and all of rank)."""
-    a, tab = _lora(x, targets, adapter, qstart, scale, ranks)
     dev = x.device
     if workspace is None:
-        workspace = lora_workspace(x, targets, adapter)
+        workspace = _workspace(x, targets, _lora(x, targets, adapter, qstart, scale, ranks, None)[0])
     elif workspace.dtype is not _U8 or workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on %s" % dev)
-    a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
-    status = _launch(lib.qst_lora, dev, ctypes.addressof(a), ctypes.addressof(tab))
+    a, tab = _lora(x, targets, adapter, qstart, scale, ranks, workspace)
+    status = _launch(lib.qst_lora, dev, a, tab)
     if status:
         _call(status, "qst_lora")

@@ -52,6 +52,11 @@ def test_structs_have_the_layout_of_the_header(step, tmp_path):
     subprocess.run(["gcc", "-std=c99", "-Wall", "-Werror", str(src), "-o", exe], check=True)
     got = [int(x) for x in subprocess.run([exe], capture_output=True, text=True, check=True).stdout.split()]
     assert got == want
+    # ... and so have the bytes that calls are made of
+    for packed, py in ((step._PLAN, step.PlanArgs), (step._NORM, step.NormArgs), (step._PROBLEM, step.GemvProblem),
+                       (step._TARGET, step.LoraTarget), (step._LORA, step.LoraArgs)):
+        values = list(range(1, len(py._fields_) + 1))
+        assert packed.pack(*values) == bytes(py(*values))
 
 
 def struct(cls, d, **kw):
