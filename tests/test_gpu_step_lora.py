@@ -164,3 +164,23 @@ def test_starts_from_outside_touch_nothing():
     for starts in ([0, 4, 900, 1000, 2 ** 31 - 1], [-50, 4, 8, 12, 16], [0, 12, 4, 16, 2], [16] * 5, [-9] * 5):
         c.qstart = np.array(starts, np.int32)
         c.run()
+
+
+@pytest.mark.parametrize("dtype", [F32, F16])
+@pytest.mark.parametrize("lens,n_ad", [([1] * 64, 1), ([1] * 150, 2), ([1] * 40, 3), ([1, 1, 30, 1, 0, 1, 1, 2, 1] * 9, 2),
+                                       ([1] * 17 + [0] * 200 + [1] * 60, 1), ([1] * 6000, 3)])
+def test_equal_adapters_of_single_rows(lens, n_ad, dtype):
+    """They share tiles, up to 16 of 64 neighbours, whatever lies between."""
+    c = Case(len(lens), lens, 72, [33], 24, n_ad, dtype, extra=2)
+    c.check(c.run())
+    c.adapter[::3] = -1
+    c.check(c.run(inplace=False), inplace=False)
+
+
+def test_long_requests_end_inside_tiles():
+    """64 rows a tile where requests are long on average, beside short and empty ones."""
+    for dtype in (F32, F16):
+        for rank, outs in ((8, [5]), (24, [700, 33]), (72, [64, 130]), (256, [70])):
+            c = Case(rank, [63, 64, 65, 1, 0, 129, 200], 328, outs, rank, 3, dtype, extra=1)
+            c.check(c.run())
+            c.check(c.run(inplace=False), inplace=False)
