@@ -371,9 +371,9 @@ template <int T, int B, int LP, bool MULTI> struct Q8Shape {
     static constexpr bool EVEN = T == T_Q4_K || T == T_Q5_K;     // rows of whole 16-byte chunks
     static constexpr int BYTES = SEGB + (EVEN ? 0 : 16);
     static constexpr int STAGE = BYTES / 4 + 4;                  // dwords of a wave (+ 4: reads realign past the end)
-    // x passes through before the first item, XR rows of it at a time
-    static constexpr int XR = MULTI ? 1 : B, XSEGS = MULTI ? WAVES : 1;
-    static constexpr int XDW = XR * XSEGS * XLay<T>::ROW;
+    // x passes through before the first item: all rows of a segment, or of several as
+    // many as make WAVES of them
+    static constexpr int XDW = (MULTI ? WAVES : B) * XLay<T>::ROW;
     static constexpr int DW = WAVES * STAGE > XDW ? WAVES * STAGE : XDW;
 };
 
@@ -385,7 +385,7 @@ __device__ __forceinline__ void gemv_q8_body(const Q8Type &P, const uint8_t *x, 
     using S = Q8Shape<T, B, LP, MULTI>;
     using X = XUnit<T, B>;
     using XL = XLay<T>;
-    constexpr int UE = S::UE, SEGB = S::SEGB, RPI = 64 / LP, BYTES = S::BYTES, NCH = (BYTES + 1023) / 1024, XR = S::XR;
+    constexpr int UE = S::UE, SEGB = S::SEGB, RPI = 64 / LP, BYTES = S::BYTES, NCH = (BYTES + 1023) / 1024;
     constexpr bool EVEN = S::EVEN;
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -433,23 +433,26 @@ __device__ __forceinline__ void gemv_q8_body(const Q8Type &P, const uint8_t *x, 
 
     X xu;
     const int nt = 64 * (MULTI ? seg_waves * groups : WAVES), segs = MULTI ? seg_waves : 1;
-    const int per_row = segs * 64 * XL::NB;
+    const int per_row = segs * 64 * XL::NB, xr = MULTI ? WAVES / seg_waves : B;      // rows of x at a time
     constexpr int XM = MULTI ? 2 : (B * 64 * XL::NB + 64 * WAVES - 1) / (64 * WAVES);
     XStage<T, XM> t;
     auto load_seg = [&](int round, bool first) __attribute__((always_inline)) {
         const int unit = (MULTI ? 64 * (round * seg_waves + sw) : 0) + unit0;
         const int mine_unit = unit < units ? unit0 : 0;
 #pragma unroll
-        for (int r0 = 0; r0 < B; r0 += XR) {
-            if (!first || r0 > 0) {
-                t.load(x, nblocks, round * per_row, per_row, XR, r0, batch - 1, threadIdx.x, nt);
-                lds_barrier();            // what was there has been read
+        for (int b = 0; b < B; ++b) {
+            const int r = MULTI ? b % xr : b;
+            if (r == 0) {
+                if (!first && b == 0)
+                    t.load(x, nblocks, round * per_row, per_row, xr, 0, batch - 1, threadIdx.x, nt);
+                if (!first || b > 0)
+                    lds_barrier();            // what was there has been read
+                t.store(stage, per_row, xr, threadIdx.x, nt);
+                if (b + xr < B)               // the next rows are on their way meanwhile
+                    t.load(x, nblocks, round * per_row, per_row, xr, b + xr, batch - 1, threadIdx.x, nt);
+                lds_barrier();
             }
-            t.store(stage, per_row, XR, threadIdx.x, nt);
-            lds_barrier();
-#pragma unroll
-            for (int r = 0; r < XR; ++r)
-                take_x<T, B>(xu, r0 + r, stage + (r * segs + sw) * XL::ROW, mine_unit);
+            take_x<T, B>(xu, b, stage + (r * segs + sw) * XL::ROW, mine_unit);
         }
     };
 
@@ -459,7 +462,7 @@ __device__ __forceinline__ void gemv_q8_body(const Q8Type &P, const uint8_t *x, 
     Cur cc = cl;
     // x is asked for first, so that the wait for it leaves the items in flight (many
     // rows of several segments have no registers for both)
-    t.load(x, nblocks, 0, per_row, XR, 0, batch - 1, threadIdx.x, nt);
+    t.load(x, nblocks, 0, per_row, xr, 0, batch - 1, threadIdx.x, nt);
     __builtin_amdgcn_sched_barrier(0);
     if (MULTI && B >= 6)
         load_seg(0, true);
@@ -567,7 +570,7 @@ template <int A, int B> struct Most {
 
 // T0, T1, T2: the types of a launch, of one unit size.
 template <int T0, int T1, int T2, int B, int LP, bool MULTI>
-__global__ void __launch_bounds__(64 * WAVES, B <= 2 ? 4 : 2)
+__global__ void __launch_bounds__(64 * WAVES, B <= (MULTI ? 1 : 2) ? 4 : 2)
 gemv_q8_kernel(Q8Call c, const uint8_t *x, int k, int batch, int items, int seg_waves, int groups)
 {
     constexpr int DW = Most<Q8Shape<T0, B, LP, MULTI>::DW, Most<Q8Shape<T1, B, LP, MULTI>::DW, Q8Shape<T2, B, LP, MULTI>::DW>::v>::v;
@@ -600,7 +603,7 @@ hipError_t run(const Q8Probs (&p)[Q8_TYPES], int k, const uint8_t *x, int batch,
     // Workgroups a compute unit: what x costs each of them stands against what more
     // waves hide.  Batch 1, 2 x 14336 x 4096 Q4_K: 1, 2, 3, 4 of them 14.8, 13.3, 14.3,
     // 15.0 us; batch 5: 23.1, 26.4, 29.8, 33.0.
-    const int most = cus * (B <= 2 ? 2 : 1);
+    const int most = cus * (B <= (MULTI ? 1 : 2) ? 2 : 1);
     // rows of one segment: an item a block (more only where blocks would pass 32 bits)
     int items = rows > (1 << 24) ? ITEMS : 1;
     // of several: the waves of a row meet once in `items` of them (4096 x 14336 Q6_K, 1,
