@@ -464,17 +464,17 @@ __device__ __forceinline__ void gemv_q8_body(const Q8Type &P, const uint8_t *x, 
     // rows of several segments have no registers for both)
     t.load(x, nblocks, 0, per_row, xr, 0, batch - 1, threadIdx.x, nt);
     __builtin_amdgcn_sched_barrier(0);
-    if (MULTI && B >= 6)
+    if (MULTI && B >= 5)
         load_seg(0, true);
     load(cl, pf[0]);
     next(cl);
     load(cl, pf[1]);
     next(cl);
-    if (!(MULTI && B >= 6))
+    if (!(MULTI && B >= 5))
         load_seg(0, true);
     lds_barrier();                        // the stage belongs to the items now
 
-    constexpr int PB = B == 3 ? 4 : B == 6 ? 8 : B;       // the sums' values: more are zero
+    constexpr int PB = B == 3 ? 4 : B > 4 ? 8 : B;       // the sums' values: more are zero
     float acc[PB];
     auto work = [&](const Cur &c, u32x4 *f) __attribute__((always_inline)) {
         const int n = P.n[c.p];

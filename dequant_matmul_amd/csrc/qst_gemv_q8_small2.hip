@@ -5,9 +5,10 @@ namespace qmm {
 
 hipError_t launch_q8_small2(const Q8Probs (&p)[Q8_TYPES], int k, const uint8_t *x, int batch, hipStream_t s)
 {
-    return batch == 4 ? by_length<T_Q4_0, T_Q8_0, T_Q5_0, 4>(p, k, x, batch, s)
-           : batch <= 6 ? by_length<T_Q4_0, T_Q8_0, T_Q5_0, 6>(p, k, x, batch, s)
-                      : by_length<T_Q4_0, T_Q8_0, T_Q5_0, 8>(p, k, x, batch, s);
+    return batch == 4   ? by_length<T_Q4_0, T_Q8_0, T_Q5_0, 4>(p, k, x, batch, s)
+           : batch == 5 ? by_length<T_Q4_0, T_Q8_0, T_Q5_0, 5>(p, k, x, batch, s)
+           : batch == 6 ? by_length<T_Q4_0, T_Q8_0, T_Q5_0, 6>(p, k, x, batch, s)
+                        : by_length<T_Q4_0, T_Q8_0, T_Q5_0, 8>(p, k, x, batch, s);
 }
 
 }  // namespace qmm
