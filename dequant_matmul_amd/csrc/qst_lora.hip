@@ -143,95 +143,96 @@ __device__ __forceinline__ float dot(const h16x8 &w, const F8 &x, float s)
     return s;
 }
 
+__device__ __forceinline__ float dot(const h16x8 &w, const h16x8 &x, float s)
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        s = __builtin_fmaf((float)w[j], (float)x[j], s);
+    return s;
+}
+
 template <typename I> struct FragOf { typedef h16x8 type; };
 template <> struct FragOf<float> { typedef F8 type; };
 
-// The inner sums of few rows: a workgroup takes a tile of 16 rows and one column, a
-// target's 16 ranks; its four waves go along k, eight steps of loads in flight.
+// The inner sums of a tile of few rows, a target's ranks r0 .. r0 + 15, over k0 .. k1, eight
+// steps of loads in flight: rank r0 + 4 kg + i of the lane's column, row `row` of x.
 template <typename I>
-__global__ void __launch_bounds__(256) lora_in_kernel(LoraK l)
+__device__ __forceinline__ f32x4 inner_sums(const LoraK &l, const Tile &t, int tg, int r0, int k0, int k1)
 {
     constexpr int U = 8;
     typedef typename FragOf<I>::type X;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const Tile t = find_tile<16, true>(l, blockIdx.x, 0);
-    if (t.rows <= 0 || t.ad < 0 || t.ad >= l.adapters)
-        return;
-    const int i16 = lane & 15, kg = lane >> 4;
-    const int row = t.row;
-    const int tg = blockIdx.y / l.rank_tiles, r0 = 16 * (blockIdx.y - tg * l.rank_tiles);
-    const int k0 = blockIdx.z * l.span + wave * (l.span / 4), k1 = min(k0 + l.span / 4, l.k);
-    const I *x = (const I *)l.x + row * l.xs + 8 * kg;
+    const int lane = threadIdx.x & 63, i16 = lane & 15, kg = lane >> 4;
+    const I *x = (const I *)l.x + t.row * l.xs + 8 * kg;
     const _Float16 *a = l.a[tg] + ((int64_t)t.ad * l.rank + min(r0 + i16, l.rank - 1)) * l.k + 8 * kg;
-    __shared__ f32x4 part[3][64];
+    // a group of whole steps, and single ones (the last may end inside: k is a multiple of
+    // 8, so a lane's part is whole)
+    auto go = [&](auto add) __attribute__((always_inline)) {
+        int kk = k0;
+        for (; kk + 32 * U <= k1; kk += 32 * U) {
+            X xf[U];
+            h16x8 af[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                af[u] = frag(a + kk + 32 * u);
+                xf[u] = frag(x + kk + 32 * u);
+            }
+            __builtin_amdgcn_sched_barrier(0);     // all of them asked for before the first product
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                add(af[u], xf[u]);
+        }
+        for (; kk < k1; kk += 32) {
+            const bool in = kk + 8 * kg < k1;
+            const int at = in ? kk : k1 - 8 - 8 * kg;
+            add(only(frag(a + at), in), only(frag(x + at), in));
+        }
+    };
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-    int kk = k0;
     if constexpr (sizeof(I) == 4) {
         // One row of fp32: the matrix instruction of fp32 would work on 15 more that are
         // not there, 8 of 32 cycles a step where 8 multiply-adds take 4 each (one token
         // 9.2 -> 8.1 us).  Two to four rows by the products of 4 x 4 are no faster.
         if (t.rows == 1) {
             float s = 0.f;
-            for (; kk + 32 * U <= k1; kk += 32 * U) {
-                F8 xf[U];
-                h16x8 af[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    af[u] = frag(a + kk + 32 * u);
-                    xf[u] = frag(x + kk + 32 * u);
-                }
-                __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    s = dot(af[u], xf[u], s);
-            }
-            for (; kk < k1; kk += 32) {
-                const bool in = kk + 8 * kg < k1;
-                const int at = in ? kk : k1 - 8 - 8 * kg;
-                s = dot(only(frag(a + at), in), only(frag(x + at), in), s);
-            }
+            go([&](const h16x8 &w, const X &v) __attribute__((always_inline)) { s = dot(w, v, s); });
             s += __shfl_xor(s, 16);
             s += __shfl_xor(s, 32);
-            float *sums = (float *)part;
-            if (lane < 16)
-                sums[16 * wave + lane] = s;
-            __syncthreads();
-            if (threadIdx.x < 16 && r0 + i16 < l.rank)
-                l.h[(((int64_t)blockIdx.z * l.targets + tg) * l.tokens + row) * l.rank + r0 + i16] =
-                    (sums[i16] + sums[16 + i16]) + (sums[32 + i16] + sums[48 + i16]);
-            return;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                acc[i] = __shfl(s, 4 * kg + i);
+            return acc;
         }
     }
-    for (; kk + 32 * U <= k1; kk += 32 * U) {
-        X xf[U];
-        h16x8 af[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            af[u] = frag(a + kk + 32 * u);
-            xf[u] = frag(x + kk + 32 * u);
-        }
-        __builtin_amdgcn_sched_barrier(0);     // all of them asked for before the first product
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            acc = mma(af[u], xf[u], acc);
-    }
-    for (; kk < k1; kk += 32) {
-        // the last step may end inside: k is a multiple of 8, so a lane's part is whole
-        const bool in = kk + 8 * kg < k1;
-        const int at = in ? kk : k1 - 8 - 8 * kg;
-        acc = mma(only(frag(a + at), in), only(frag(x + at), in), acc);
-    }
+    go([&](const h16x8 &w, const X &v) __attribute__((always_inline)) { acc = mma(w, v, acc); });
+    return acc;
+}
+
+// The waves' sums of a workgroup, in wave 0.
+__device__ __forceinline__ f32x4 join_waves(f32x4 acc, f32x4 (*part)[64])
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     if (wave > 0)
         part[wave - 1][lane] = acc;
     __syncthreads();
-    if (wave > 0 || i16 >= t.rows)
+    return wave > 0 ? acc : (acc + part[0][lane]) + (part[1][lane] + part[2][lane]);
+}
+
+// The inner sums of few rows: a workgroup takes a tile of 16 rows and one column, a
+// target's 16 ranks; its four waves go along k.
+template <typename I>
+__global__ void __launch_bounds__(256) lora_in_kernel(LoraK l)
+{
+    __shared__ f32x4 part[3][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const Tile t = find_tile<16, true>(l, blockIdx.x, 0);
+    if (t.rows <= 0 || t.ad < 0 || t.ad >= l.adapters)
         return;
-#pragma unroll
-    for (int i = 0; i < 3; ++i)
-        acc += part[i][lane];
-    const int r = r0 + 4 * kg;
-    if (r < l.rank)
-        *(f32x4 *)(l.h + (((int64_t)blockIdx.z * l.targets + tg) * l.tokens + row) * l.rank + r) = acc;
+    const int tg = blockIdx.y / l.rank_tiles, r0 = 16 * (blockIdx.y - tg * l.rank_tiles);
+    const int k0 = blockIdx.z * l.span + wave * (l.span / 4), k1 = min(k0 + l.span / 4, l.k);
+    const f32x4 acc = join_waves(inner_sums<I>(l, t, tg, r0, k0, k1), part);
+    const int r = r0 + 4 * (lane >> 4);
+    if (wave == 0 && (lane & 15) < t.rows && r < l.rank)
+        *(f32x4 *)(l.h + (((int64_t)blockIdx.z * l.targets + tg) * l.tokens + t.row) * l.rank + r) = acc;
 }
 
 // The inner sums of long requests: a tile of 64 rows, 16 a wave, and NC columns (16
@@ -330,36 +331,16 @@ __global__ void __launch_bounds__(256) lora_in_wide_kernel(LoraK l)
 
 constexpr int TURN = 68;        // floats between rows in LDS: 64 and a bank's shift
 
-// The outputs: some columns of a tile's rows.  NK steps of 32 ranks.
-template <int WR, int NK>
-__global__ void __launch_bounds__(256) lora_out_kernel(LoraK l)
+// The outputs of a tile's rows, columns j0 .. j0 + out_cols of a target.  NK steps of 32
+// ranks; sums(c, r): ranks r .. r + 7 of the inner sums of the lane's row, r = 32 c + 8 kg
+// or the last 8.
+template <int WR, int NK, int WAVES, class H>
+__device__ __forceinline__ void outputs(const LoraK &l, const Tile &t, int wr, int tg, int j0, float (*turn)[16 * TURN], H sums)
 {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int tg = blockIdx.z, n = l.n[tg], j0 = blockIdx.y * l.out_cols;
-    if (j0 >= n)
-        return;
-    const int wr = WR == 4 ? wave : 0;
-    const Tile t = find_tile<16 * WR, WR == 1>(l, blockIdx.x, wr);
-    if (t.rows <= 0)
-        return;
+    const int n = l.n[tg], i16 = lane & 15, kg = lane >> 4, row = t.row;
     const float *base = l.base[tg] ? l.base[tg] : l.y[tg];
     float *y = l.y[tg];
-    if (t.ad < 0 || t.ad >= l.adapters) {
-        // (such tiles are a request's own rows)
-        const int row0 = __builtin_amdgcn_readfirstlane(t.row) - (WR == 4 ? min(16 * wr, t.rows - 1) : 0);
-        if (base != y)
-            for (int i = threadIdx.x; i < t.rows * l.out_cols; i += 256) {
-                const int j = j0 + i % l.out_cols;
-                const int64_t at = (int64_t)(row0 + i / l.out_cols) * n + j;
-                if (j < n)
-                    y[at] = base[at];
-            }
-        return;
-    }
-    const int i16 = lane & 15, kg = lane >> 4;
-    if (16 * wr >= t.rows)
-        return;
-    const int row = t.row;
     const int live = rank_of(l, t.ad);
     const float scale = l.scale ? l.scale[t.ad] : 1.f;
     const int most = min(j0 + l.out_cols, n);
@@ -379,15 +360,7 @@ __global__ void __launch_bounds__(256) lora_out_kernel(LoraK l)
         for (int i = 0; i < 8; ++i)
             h[c][i] = 0.f;
     }
-#pragma unroll 4
-    for (int z = 0; z < l.splits; ++z)
-#pragma unroll
-        for (int c = 0; c < NK; ++c) {
-            const F8 f = frag(l.h + (((int64_t)z * l.targets + tg) * l.tokens + row) * l.rank + at[c]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                h[c][i] += i < 4 ? f.a[i & 3] : f.b[i & 3];
-        }
+    sums(at, h);
     float top = 0.f;
 #pragma unroll
     for (int c = 0; c < NK; ++c)
@@ -414,13 +387,12 @@ __global__ void __launch_bounds__(256) lora_out_kernel(LoraK l)
     const bool vec = (n & 3) == 0;
     const _Float16 *b = l.b[tg] + (int64_t)t.ad * n * l.rank;
     const int rows = t.rows - 16 * wr;
-    __shared__ __align__(16) float turn[4][16 * TURN];
     float *mine = turn[wave];
     int64_t to_row[4];                // rows 4 p + kg of the wave's, in y
 #pragma unroll
     for (int p = 0; p < 4; ++p)
         to_row[p] = (int64_t)__shfl(row, 4 * p + kg) * n;
-    for (int j = j0 + (WR == 4 ? 0 : 64 * wave); j < most; j += WR == 4 ? 64 : 256) {
+    for (int j = j0 + (WR == 4 ? 0 : 64 * wave); j < most; j += WR == 4 ? 64 : 64 * WAVES) {
         // (high ranks: their 16 columns' weights one product at a time, for the registers)
         constexpr int QS = NK <= 2 ? 4 : 1;
         h16x8 w[QS][NK];
@@ -496,6 +468,144 @@ __global__ void __launch_bounds__(256) lora_out_kernel(LoraK l)
     }
 }
 
+// y = base for the rows of a tile without an adapter (a request's own rows).
+template <int WR> __device__ __forceinline__ void copy_rows(const LoraK &l, const Tile &t, int wr, int tg, int j0)
+{
+    const float *base = l.base[tg];
+    float *y = l.y[tg];
+    if (base == nullptr || base == y)
+        return;
+    const int n = l.n[tg], row0 = __builtin_amdgcn_readfirstlane(t.row) - (WR == 4 ? min(16 * wr, t.rows - 1) : 0);
+    for (int i = threadIdx.x; i < t.rows * l.out_cols; i += blockDim.x) {
+        const int j = j0 + i % l.out_cols;
+        const int64_t at = (int64_t)(row0 + i / l.out_cols) * n + j;
+        if (j < n)
+            y[at] = base[at];
+    }
+}
+
+template <int WR, int NK>
+__global__ void __launch_bounds__(256) lora_out_kernel(LoraK l)
+{
+    __shared__ __align__(16) float turn[4][16 * TURN];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wr = WR == 4 ? wave : 0;
+    const int tg = blockIdx.z, j0 = blockIdx.y * l.out_cols;
+    if (j0 >= l.n[tg])
+        return;
+    const Tile t = find_tile<16 * WR, WR == 1>(l, blockIdx.x, wr);
+    if (t.rows <= 0)
+        return;
+    if (t.ad < 0 || t.ad >= l.adapters) {
+        copy_rows<WR>(l, t, wr, tg, j0);
+        return;
+    }
+    if (16 * wr >= t.rows)
+        return;
+    outputs<WR, NK, 4>(l, t, wr, tg, j0, turn, [&](const int (&at)[NK], float (&h)[NK][8]) __attribute__((always_inline)) {
+#pragma unroll 4
+        for (int z = 0; z < l.splits; ++z)
+#pragma unroll
+            for (int c = 0; c < NK; ++c) {
+                const F8 f = frag(l.h + (((int64_t)z * l.targets + tg) * l.tokens + t.row) * l.rank + at[c]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    h[c][i] += i < 4 ? f.a[i & 3] : f.b[i & 3];
+            }
+    });
+}
+
+// Both in one launch, for the smallest calls: every workgroup of the outputs makes the
+// inner sums of its tile itself, which are read from memory once and from the caches by
+// the others.  16 waves: they share k, and 1024 columns.
+constexpr int ONE_WAVES = 16;
+template <typename I, int NK>
+__global__ void __launch_bounds__(64 * ONE_WAVES) lora_one_kernel(LoraK l)
+{
+    constexpr int HP = 32 * NK + 4;              // floats between rows of inner sums
+    __shared__ __align__(16) float turn[ONE_WAVES][16 * TURN];
+    __shared__ __align__(16) float hs[16 * HP];
+    const int lane = threadIdx.x & 63, i16 = lane & 15, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int tg = blockIdx.z, j0 = blockIdx.y * l.out_cols;
+    if (j0 >= l.n[tg])
+        return;
+    const Tile t = find_tile<16, true>(l, blockIdx.x, 0);
+    if (t.rows <= 0)
+        return;
+    if (t.ad < 0 || t.ad >= l.adapters) {
+        copy_rows<1>(l, t, 0, tg, j0);
+        return;
+    }
+    if (t.rows == 1) {
+        // one row: a wave takes four ranks and a quarter of k, 512 of it at a time in whole
+        // runs of each rank's row, so that x is read by four waves and no lane twice
+        const int q = wave & 3, kq = wave >> 2, steps = (l.k + 511) / 512;
+        const I *x = (const I *)l.x + __builtin_amdgcn_readfirstlane(t.row) * l.xs;
+        const _Float16 *a = l.a[tg] + (int64_t)t.ad * l.rank * l.k;
+        float *sums = turn[0];                   // [rank][4 parts of k]
+        for (int r0 = 4 * q; r0 < l.rank; r0 += 16) {
+            float s[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int j = steps * kq / 4; j < steps * (kq + 1) / 4; j += 2) {
+                // two steps in flight; past the end of k or of the part: zeros
+                typename FragOf<I>::type xf[2];
+                h16x8 af[2][4];
+                bool in[2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int kk = 512 * (j + u) + 8 * lane;
+                    in[u] = kk < l.k && j + u < steps * (kq + 1) / 4;
+                    const int at = min(kk, l.k - 8);
+                    xf[u] = frag(x + at);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        af[u][i] = frag(a + (int64_t)(r0 + i) * l.k + at);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        s[i] = in[u] ? dot(af[u][i], xf[u], s[i]) : s[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                s[i] = wave_sum(s[i]);
+                if (lane == 0)
+                    sums[4 * (r0 + i) + kq] = s[i];
+            }
+        }
+        __syncthreads();
+        if ((int)threadIdx.x < l.rank) {
+            const f32x4 v = *(const f32x4 *)(sums + 4 * threadIdx.x);
+            hs[threadIdx.x] = (v[0] + v[1]) + (v[2] + v[3]);
+        }
+    } else {
+        for (int r0 = 0; r0 < l.rank; r0 += 16) {
+            const int k0 = wave * (l.span / ONE_WAVES), k1 = min(k0 + l.span / ONE_WAVES, l.k);
+            *(f32x4 *)(turn[wave] + 4 * lane) = inner_sums<I>(l, t, tg, r0, k0, k1);
+            __syncthreads();
+            if (threadIdx.x < 256) {
+                // lane, i of the accumulators: row lane % 16, rank 4 (lane / 16) + i
+                float v = 0.f;
+#pragma unroll
+                for (int w = 0; w < ONE_WAVES; ++w)
+                    v += turn[w][threadIdx.x];
+                hs[(threadIdx.x / 4 % 16) * HP + r0 + threadIdx.x / 64 * 4 + threadIdx.x % 4] = v;
+            }
+            __syncthreads();
+        }
+    }
+    __syncthreads();
+    outputs<1, NK, ONE_WAVES>(l, t, 0, tg, j0, turn, [&](const int (&at)[NK], float (&h)[NK][8]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int c = 0; c < NK; ++c) {
+            const F8 f = frag(hs + (t.rows == 1 ? 0 : i16 * HP) + at[c]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                h[c][i] = i < 4 ? f.a[i & 3] : f.b[i & 3];
+        }
+    });
+}
+
 // How a call is cut up, from its sizes alone.
 struct Cut {
     bool wide;        // tiles of 64 rows, else 16
@@ -547,6 +657,14 @@ hipError_t outer(const LoraK &k, int tiles, int n, hipStream_t s)
                            : start(lora_out_kernel<WR, 8>, grid, block, s, k);
 }
 
+// A single token each of up to four requests, and 256 KB of A at most (4096 wide, rank 8,
+// 16, 64: 6.1, 6.4, 15.8 us, by two launches 7.9, 8.1, 9.3; 14336 wide, rank 16: 10.4 and
+// 9.2).  Rows that meet in a tile are slower here: four of one adapter 11.7 and 9.5 us.
+bool one_launch(const qst_lora_args &a)
+{
+    return a.tokens <= a.batch && a.tokens <= 4 && a.rank <= 64 && (int64_t)a.rank * a.k <= 131072;
+}
+
 }  // namespace
 
 int64_t lora_workspace(const qst_lora_args &a)
@@ -577,6 +695,17 @@ hipError_t launch_lora(const qst_lora_args &a, const qst_lora_target *t, hipStre
         k.out_cols = 512;
         while (k.out_cols > 64 && c.tiles * all / k.out_cols < 1024)
             k.out_cols /= 2;
+    }
+    if (a.adapters > 0 && one_launch(a)) {
+        k.splits = 1;
+        k.span = (int)((a.k + 32 * ONE_WAVES - 1) / (32 * ONE_WAVES) * (32 * ONE_WAVES));
+        k.out_cols = 64 * ONE_WAVES;
+        const dim3 grid(c.tiles, (most + k.out_cols - 1) / k.out_cols, a.targets), block(64 * ONE_WAVES);
+        if (a.dtype == QKV_HALF)
+            return a.rank <= 32 ? start(lora_one_kernel<_Float16, 1>, grid, block, s, k)
+                                : start(lora_one_kernel<_Float16, 2>, grid, block, s, k);
+        return a.rank <= 32 ? start(lora_one_kernel<float, 1>, grid, block, s, k)
+                            : start(lora_one_kernel<float, 2>, grid, block, s, k);
     }
     if (a.adapters > 0) {
         const hipError_t e = a.dtype == QKV_HALF ? inner<_Float16>(k, c, s) : inner<float>(k, c, s);

@@ -116,13 +116,15 @@ def kv_plan(table, ctx, fresh, free, count, tokens, page_size=64, out=None):
     if fresh is not None:
         _ints(fresh, "fresh", dev, (B,))
     if out is None:
-        out = (torch.empty(B + 1, dtype=_I32, device=dev), torch.empty(tokens, dtype=_I32, device=dev),
-               torch.empty(tokens, dtype=_I32, device=dev), torch.empty(B, dtype=_I32, device=dev),
-               torch.empty(1, dtype=_I32, device=dev))
+        # pieces of one buffer, the rows' 16-byte aligned
+        pad = -tokens % 4
+        slots, _, pos, _, qstart, granted, left = torch.empty(
+            2 * (tokens + pad + B + 1), dtype=_I32, device=dev).split_with_sizes((tokens, pad, tokens, pad, B + 1, B, 1))
+        out = (qstart, slots, pos, granted, left)
     else:
         for t, n, name in zip(out, (B + 1, tokens, tokens, B, 1), ("qstart", "slots", "pos", "granted", "left")):
             _ints(t, name, dev, (n,))
-    qstart, slots, pos, granted, left = out
+        qstart, slots, pos, granted, left = out
     a = _PLAN.pack(table.data_ptr(), ctx.data_ptr(), fresh.data_ptr() if fresh is not None else 0, free.data_ptr(),
                    count.data_ptr(), qstart.data_ptr(), slots.data_ptr(), pos.data_ptr(), granted.data_ptr(),
                    left.data_ptr(), B, cols, pages, page_size, tokens)

@@ -184,3 +184,24 @@ def test_long_requests_end_inside_tiles():
             c = Case(rank, [63, 64, 65, 1, 0, 129, 200], 328, outs, rank, 3, dtype, extra=1)
             c.check(c.run())
             c.check(c.run(inplace=False), inplace=False)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16])
+@pytest.mark.parametrize("lens", [[1], [1, 1], [1, 1, 1, 1], [0, 1, 0, 2], [2, 0, 0, 0, 1], [0, 4, 0, 0]])
+@pytest.mark.parametrize("k,rank,outs", [(8, 8, [1]), (520, 24, [1025, 7]), (1000, 40, [64, 2100]), (4096, 16, [4096]),
+                                         (2048, 64, [300, 1, 33]), (3096, 32, [70])])
+def test_the_smallest_calls(k, rank, outs, lens, dtype):
+    """One launch where as many requests as tokens bring up to four."""
+    for n_ad in (1, 3):
+        c = Case(k + rank + n_ad, lens, k, outs, rank, n_ad, dtype, extra=0,
+                 ranks=None if n_ad == 1 else [rank - 3, 0, 5])
+        c.check(c.run())
+        c.check(c.run(inplace=False), inplace=False)
+    c.adapter[:] = 0
+    for a, b in zip(c.a, c.b):
+        a[0, rank - 3:], b[0, :, rank - 3:] = float("nan"), float("inf")
+    ys = c.run()
+    for a, b in zip(c.a, c.b):
+        a.nan_to_num_(0, 0, 0)
+        b.nan_to_num_(0, 0, 0)
+    c.check(ys)
