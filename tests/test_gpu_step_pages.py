@@ -156,3 +156,20 @@ def test_trim_undoes_plan():
     after = dev(have) + dev(new) * granted
     back = q.kv_trim(tab, after, dev(have), f, left)
     assert int(back[0]) == count and np.array_equal(f.cpu().numpy(), free) and int(left[0]) < count
+
+
+def test_outputs_at_any_word():
+    """slots and pos that are not 16-byte aligned, rows that are not in fours."""
+    rng = np.random.default_rng(12)
+    for B, tq, tokens in ((5, 900, 4000), (70, 200, 9001), (3, 40, 50)):
+        table, have, new, free, count, _ = problem(rng, B, 300, tq, 64, waits=0.0)
+        want = step_ref.plan(table, have, new, free, count, tokens, 64)
+        for s_at, p_at in ((1, 0), (0, 3), (2, 1)):
+            bufs = [torch.full((tokens + 8,), 77, dtype=torch.int32, device=DEV) for _ in range(2)]
+            slots, pos = bufs[0][s_at:s_at + tokens], bufs[1][p_at:p_at + tokens]
+            rest = [torch.empty(n, dtype=torch.int32, device=DEV) for n in (B + 1, B, 1)]
+            q.kv_plan(dev(table), dev(have), dev(new), dev(free), dev([count]), tokens, out=(rest[0], slots, pos, *rest[1:]))
+            assert np.array_equal(slots.cpu().numpy(), want[2]) and np.array_equal(pos.cpu().numpy(), want[3])
+            for b, at in zip(bufs, (s_at, p_at)):
+                b = b.cpu()
+                assert bool((b[:at] == 77).all()) and bool((b[at + tokens:] == 77).all())
