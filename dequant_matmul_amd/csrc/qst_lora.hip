@@ -41,6 +41,7 @@ struct LoraK {
     int rank_tiles;            // of 16
     int splits, span;          // parts of k, each `span` long (a multiple of 128)
     int out_cols;              // columns of y a workgroup: each one reads the inner sums again
+    int block0[LORA_TARGETS + 1];   // first of such blocks of each target
     const _Float16 *a[LORA_TARGETS], *b[LORA_TARGETS];
     const float *base[LORA_TARGETS];
     float *y[LORA_TARGETS];
@@ -154,12 +155,14 @@ __device__ __forceinline__ float dot(const h16x8 &w, const h16x8 &x, float s)
 template <typename I> struct FragOf { typedef h16x8 type; };
 template <> struct FragOf<float> { typedef F8 type; };
 
-// The inner sums of a tile of few rows, a target's ranks r0 .. r0 + 15, over k0 .. k1, eight
-// steps of loads in flight: rank r0 + 4 kg + i of the lane's column, row `row` of x.
+// The inner sums of a tile of few rows, a target's ranks r0 .. r0 + 15, over k0 .. k1:
+// rank r0 + 4 kg + i of the lane's column, row `row` of x.
 template <typename I>
 __device__ __forceinline__ f32x4 inner_sums(const LoraK &l, const Tile &t, int tg, int r0, int k0, int k1)
 {
-    constexpr int U = 8;
+    // steps of loads in flight (fp32: 4 leave seven waves a SIMD, where 8 leave four: 53
+    // tokens 28.4 and 30.2 us)
+    constexpr int U = sizeof(I) == 4 ? 4 : 8;
     typedef typename FragOf<I>::type X;
     const int lane = threadIdx.x & 63, i16 = lane & 15, kg = lane >> 4;
     const I *x = (const I *)l.x + t.row * l.xs + 8 * kg;
@@ -468,6 +471,16 @@ __device__ __forceinline__ void outputs(const LoraK &l, const Tile &t, int wr, i
     }
 }
 
+// The target and first column of a block of columns.
+__device__ __forceinline__ int block_of(const LoraK &l, int block, int *j0)
+{
+    int tg = 0;
+    while (tg + 1 < l.targets && block >= l.block0[tg + 1])
+        ++tg;
+    *j0 = (block - l.block0[tg]) * l.out_cols;
+    return tg;
+}
+
 // y = base for the rows of a tile without an adapter (a request's own rows).
 template <int WR> __device__ __forceinline__ void copy_rows(const LoraK &l, const Tile &t, int wr, int tg, int j0)
 {
@@ -489,9 +502,8 @@ __global__ void __launch_bounds__(256) lora_out_kernel(LoraK l)
 {
     __shared__ __align__(16) float turn[4][16 * TURN];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wr = WR == 4 ? wave : 0;
-    const int tg = blockIdx.z, j0 = blockIdx.y * l.out_cols;
-    if (j0 >= l.n[tg])
-        return;
+    int j0;
+    const int tg = block_of(l, blockIdx.y, &j0);
     const Tile t = find_tile<16 * WR, WR == 1>(l, blockIdx.x, wr);
     if (t.rows <= 0)
         return;
@@ -525,9 +537,8 @@ __global__ void __launch_bounds__(64 * ONE_WAVES) lora_one_kernel(LoraK l)
     __shared__ __align__(16) float turn[ONE_WAVES][16 * TURN];
     __shared__ __align__(16) float hs[16 * HP];
     const int lane = threadIdx.x & 63, i16 = lane & 15, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int tg = blockIdx.z, j0 = blockIdx.y * l.out_cols;
-    if (j0 >= l.n[tg])
-        return;
+    int j0;
+    const int tg = block_of(l, blockIdx.y, &j0);
     const Tile t = find_tile<16, true>(l, blockIdx.x, 0);
     if (t.rows <= 0)
         return;
@@ -647,10 +658,23 @@ hipError_t inner(const LoraK &k, const Cut &c, hipStream_t s)
                        : start(lora_in_wide_kernel<I, 8>, grid, block, s, k);
 }
 
-template <int WR>
-hipError_t outer(const LoraK &k, int tiles, int n, hipStream_t s)
+// Blocks of out_cols columns, target after target; their number (a grid's second
+// dimension: wider ones where they would be more than 65535).
+int set_blocks(LoraK &k)
 {
-    const dim3 grid(tiles, (n + k.out_cols - 1) / k.out_cols, k.targets), block(256);
+    for (;; k.out_cols *= 2) {
+        k.block0[0] = 0;
+        for (int i = 0; i < k.targets; ++i)
+            k.block0[i + 1] = k.block0[i] + (k.n[i] + k.out_cols - 1) / k.out_cols;
+        if (k.block0[k.targets] <= 65535)
+            return k.block0[k.targets];
+    }
+}
+
+template <int WR>
+hipError_t outer(LoraK &k, int tiles, hipStream_t s)
+{
+    const dim3 grid(tiles, set_blocks(k)), block(256);
     return k.rank <= 32    ? start(lora_out_kernel<WR, 1>, grid, block, s, k)
            : k.rank <= 64  ? start(lora_out_kernel<WR, 2>, grid, block, s, k)
            : k.rank <= 128 ? start(lora_out_kernel<WR, 4>, grid, block, s, k)
@@ -676,15 +700,13 @@ hipError_t launch_lora(const qst_lora_args &a, const qst_lora_target *t, hipStre
 {
     const Cut c = cut(a);
     LoraK k{a.x, a.adapter, a.qstart, a.scale, a.ranks, (float *)a.workspace, a.x_stride, (int)a.tokens, (int)a.batch,
-            (int)a.k, a.adapters, a.rank, a.targets, c.rank_tiles, c.splits, c.span, 256, {}, {}, {}, {}, {}};
-    int most = 0;
+            (int)a.k, a.adapters, a.rank, a.targets, c.rank_tiles, c.splits, c.span, 256, {}, {}, {}, {}, {}, {}};
     for (int i = 0; i < a.targets; ++i) {
         k.a[i] = (const _Float16 *)t[i].a;
         k.b[i] = (const _Float16 *)t[i].b;
         k.base[i] = t[i].base;
         k.y[i] = t[i].y;
         k.n[i] = (int)t[i].n;
-        most = k.n[i] > most ? k.n[i] : most;
     }
     // tiles of 64 rows, a wave 16 of them: 512 columns where that leaves enough workgroups
     // (prompts of 6653 rows, three targets: 512 columns 76 us, 256 86), down to 64
@@ -700,7 +722,7 @@ hipError_t launch_lora(const qst_lora_args &a, const qst_lora_target *t, hipStre
         k.splits = 1;
         k.span = (int)((a.k + 32 * ONE_WAVES - 1) / (32 * ONE_WAVES) * (32 * ONE_WAVES));
         k.out_cols = 64 * ONE_WAVES;
-        const dim3 grid(c.tiles, (most + k.out_cols - 1) / k.out_cols, a.targets), block(64 * ONE_WAVES);
+        const dim3 grid(c.tiles, set_blocks(k)), block(64 * ONE_WAVES);
         if (a.dtype == QKV_HALF)
             return a.rank <= 32 ? start(lora_one_kernel<_Float16, 1>, grid, block, s, k)
                                 : start(lora_one_kernel<_Float16, 2>, grid, block, s, k);
@@ -712,7 +734,7 @@ hipError_t launch_lora(const qst_lora_args &a, const qst_lora_target *t, hipStre
         if (e != hipSuccess)
             return e;
     }
-    return c.wide ? outer<4>(k, c.tiles, most, s) : outer<1>(k, c.tiles, most, s);
+    return c.wide ? outer<4>(k, c.tiles, s) : outer<1>(k, c.tiles, s);
 }
 
 }  // namespace qmm

@@ -85,3 +85,17 @@ def test_adapters_past_4_gib(lens):
         want = (x[rows].double() @ a[-1].double().T) @ b[-1].double().T
         bar = (x[rows].double().abs() @ a[-1].double().abs().T) @ b[-1].double().abs().T
         assert bool(((y[rows].double() - want).abs() <= 100 * 2.0 ** -24 * bar).all())
+
+
+def test_adapters_of_the_widest_targets():
+    """More blocks of columns than a grid's second dimension takes."""
+    n, k, rank = 1 << 24, 8, 8
+    a, b = torch.randn(1, rank, k, device=DEV).half(), torch.zeros(1, n, rank, dtype=torch.float16, device=DEV)
+    b[0, -5:], b[0, :5] = 1.0, 2.0
+    x = torch.randn(3, k, device=DEV)
+    ys = [torch.zeros(3, n, device=DEV) for _ in range(8)]
+    q.lora(x, [(a, b, y) for y in ys], torch.zeros(3, dtype=I32, device=DEV))
+    h = (x.double() @ a[0].double().T).sum(-1)
+    for y in ys:
+        assert bool(((y[:, -5:].double() - h[:, None]).abs() < 1e-4).all())
+        assert bool(((y[:, :5].double() - 2 * h[:, None]).abs() < 1e-4).all()) and not y[:, 5:-5].any()
