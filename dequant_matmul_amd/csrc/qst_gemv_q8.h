@@ -4,10 +4,14 @@
 //   y[b][j] = sum over blocks of  d_w d_x sum_i q_i x_i      (Q4_0, Q5_0, Q6_K: q less its offset)
 //                                 d_x (d sc Q - dmin m S)    (Q4_K, Q5_K: Q = sum q x, S = sum x)
 //
-// Bound: reading the weights.  v_dot4_i32_i8 takes four products an instruction and
-// needs no conversion of codes, about 1 instruction a weight and lane for the whole
-// decoding and 1/4 more per row of x, so up to batch 8 the arithmetic stays below
-// the time of the bytes.
+// Bound: reading the weights for one to three rows of x, instructions for more.
+// v_dot4_i32_i8 takes four products an instruction and needs no conversion of codes;
+// a row of x costs 16 of them and 12 others for a lane's 64 weights of Q4_K, and its
+// part of x 20 registers, which leave two waves a SIMD from batch 5 on.
+//
+// Measured, Q4_K 2 x 14336 x 4096, 1, 2, 4, 5, 8 rows: 13.1 (5.0 TB/s), 14.4, 19.4,
+// 21.7, 28.7 us (the bytes alone 13 at 5.09 TB/s); Q6_K 4096 x 14336, 1 and 8 rows:
+// 15.3, 29.9 us; 128256 x 4096, one row: 70 to 72 us (6.0 TB/s).
 //
 // Work split, as of the fp32 GEMV (qmm_gemv.hip): lane-units of 32 elements (64 of
 // the 256-element types), 64 of them, a segment, to a wave, one a lane.  A wave
@@ -326,9 +330,9 @@ template <int D> __device__ __forceinline__ float add_rows(float v)
     return u + v;
 }
 
-// Sums of v[0 .. B), B a power of two, over groups of LP lanes.  Each of the first log2 B steps halves
-// the values a lane carries: lane bits 0, 1 and 3 say which is left (value bits 0, 1
-// and 2).  The tree, over lane bits 0, 1, 3, 2, 4, 5, is the same for every B.
+// Sums of v[0 .. B), B a power of two, over groups of LP lanes.  Each of the first
+// log2 B steps halves the values a lane carries: lane bits 0, 1 and 3 say which is
+// left (value bits 0, 1 and 2).  The tree, over lane bits 0, 1, 3, 2, 4, 5, is the same for every B.
 template <int B, int LP> __device__ __forceinline__ float sum_lanes(float (&v)[B], int lane)
 {
     float t[B > 1 ? B / 2 : 1];

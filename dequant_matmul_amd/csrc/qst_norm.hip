@@ -16,7 +16,7 @@
 //
 // Measured: 8191 rows of 4096, fp32 + fp16 residual -> fp16, 335 MB, 59 us (5.7
 // TB/s); 2047 x 32 heads of 128, fp32 -> fp16, 50 MB, 9.4 us (5.4 TB/s); one row
-// of 4096 to Q8_0 under 3 us.
+// of 4096 to Q8_0 and its decoding to fp16, two launches, 4.9 us.
 #include "qmm_device.h"
 #include "qst_launch.h"
 

@@ -146,6 +146,7 @@ QMM_API int qst_norm(const qst_norm_args *a, void *stream);
  * of qmm_gemv, and a row of zero weights gives 0.  k a multiple of the weight
  * type's block; k 0 writes zeros; problems of n 0 are skipped.  Results do not
  * depend on the other problems of the call, nor on the batch's other rows.
+ * No y may overlap another, x or the weights.
  */
 typedef struct qst_gemv_problem {
     const void *w;   /* n rows of qmm_row_bytes(type, k) bytes */
@@ -171,7 +172,8 @@ QMM_API int qst_gemv_q8(int nprob, const qst_gemv_problem *probs, int64_t k, con
  * x fp32 enters the products as it is, fp16 the fp16 matrix cores; the inner
  * sums stay in fp32 and enter the second product as two fp16 parts of a common
  * power of two (22 bits of a row's largest); everything is summed in fp32.
- * Values of x and of the weights used must be finite.
+ * Values of x, of the weights used and of scale must be finite.  The targets' y
+ * are distinct, and overlap nothing else but their own base where it is y itself.
  * a: 16-byte aligned, k a multiple of 8; b: rank a multiple of 8, up to 256.
  * At most 1048575 tokens, and n up to 2^24.
  */
