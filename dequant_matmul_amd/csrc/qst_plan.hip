@@ -19,6 +19,7 @@
 //
 // Measured: 7 single tokens 2.7 us, 512 5.2, 2000 8.4 (two chunks); 120 prompts, 184000
 // rows 7.7 us; 24 drafted trees cut 2.4 us; 1000 ended requests, 375000 pages 4.9 us.
+#include "qst_index.h"
 #include "qst_launch.h"
 
 namespace qmm {
@@ -224,7 +225,7 @@ template <int NT> __global__ void __launch_bounds__(NT) plan_kernel(PlanK a)
                 slot[j] = -1;
                 pos[j] = 0;
                 if (f != NONE && row >= lo && row < hi) {
-                    const int held = (ci + pm) >> a.shift;
+                    const int held = pages_of(ci, a.shift);
                     const int page = at < held ? olds[i] : a.free[F - 1 - f - (at - held)];
                     slot[j] = page >= 0 && page < a.pages ? (page << a.shift) + (p & pm) : -1;
                     pos[j] = p;
