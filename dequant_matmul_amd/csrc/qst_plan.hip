@@ -4,8 +4,8 @@
 // Two prefix sums over the requests, of their new tokens and of the pages that
 // these need, decide everything: where a request's rows begin, whether the pool
 // still has its pages and which entries of the stack they are.  The sums
-// saturate just above what can be used (tokens + 1, pages + 1), so 32 bits hold
-// them for any lengths; saturated addition of such numbers is associative.
+// saturate just above what can be used (tokens + 1, pages + 1, at most 2^31), so 32
+// bits hold them for any lengths; saturated addition of such numbers is associative.
 //
 // Bound: the launch and two round trips for a few requests; the writes of 8 bytes a
 // row (4 read and 4 written a page) for many.  One launch: every workgroup makes the
@@ -25,11 +25,6 @@
 namespace qmm {
 
 namespace {
-
-__device__ __forceinline__ uint32_t sat_add(uint32_t a, uint32_t b, uint32_t cap)
-{
-    return min(a + b, cap);      // a, b <= cap <= 2^31
-}
 
 template <int CTRL, int ROWS> __device__ __forceinline__ uint32_t shifted(uint32_t v)   // 0 from outside
 {

@@ -56,3 +56,33 @@ def test_rows_of_the_last_small_page():
     assert granted.tolist() == [1] and int(left[0]) == 2
     p = np.arange(c, c + n)
     assert slots.tolist() == (3 * 64 + p % 64).tolist() and pos.tolist() == p.tolist()
+
+
+@pytest.mark.parametrize("lens,wide", [([2 ** 31 - 1] * 4 + [1], False), ([2 ** 30, 2 ** 30, 2 ** 30, 2 ** 30, 64, 0], False),
+                                       ([5, 2 ** 31 - 8, 2, 1], True)])
+def test_the_most_tokens(lens, wide):
+    """tokens = 2^31 - 1, and lengths whose sum is past that: no later request comes out
+    at an earlier row.  `wide`: the table's rows hold them all, and nothing is short."""
+    T, B = 2 ** 31 - 1, len(lens)
+    cols = 2 ** 31 // 2 ** 30 if wide else 4
+    page = 2 ** 30 if wide else 64
+    pages = 1 if wide else 100
+    table = torch.zeros(B, cols, dtype=I32, device=DEV)
+    ctx = dev([3 if wide else 0] * B)         # (wide: on their one old page)
+    free, count = torch.arange(pages, dtype=I32, device=DEV), dev([pages])
+    qstart, slots, pos, granted, left = q.kv_plan(table, ctx, dev(lens), free, count, T, page_size=page)
+    starts = [min(sum(lens[:i]), T) for i in range(B + 1)]
+    assert qstart.tolist() == starts
+    fits = [3 * wide + n <= min(cols * page, T) and sum(lens[:i + 1]) <= T for i, n in enumerate(lens)]
+    need = [-(-(3 * wide + n) // page) - wide if f else 0 for n, f in zip(lens, fits)]
+    ok = [int(f and (w == 0 or sum(need[:i + 1]) <= pages)) for i, (f, w) in enumerate(zip(fits, need))]
+    assert granted.tolist() == ok and int(left[0]) == pages - sum(w for w, o in zip(need, ok) if o)
+    for b in range(B):
+        lo, hi = starts[b], starts[b + 1]
+        if not ok[b] and hi > lo:
+            assert int(slots[lo:hi].max()) == -1 and int(pos[lo:hi].max()) == 0
+        elif hi > lo:
+            assert int(pos[lo]) == 3 * wide and int(pos[hi - 1]) == 3 * wide + hi - lo - 1
+            assert int(slots[lo:hi].min()) >= 0
+    if starts[-1] < T:
+        assert int(slots[starts[-1]:].max()) == -1
