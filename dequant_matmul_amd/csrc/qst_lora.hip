@@ -704,22 +704,28 @@ int64_t lora_workspace(const qst_lora_args &a)
 
 hipError_t launch_lora(const qst_lora_args &a, const qst_lora_target *t, hipStream_t s)
 {
-    const Cut c = cut(a);
+    Cut c = cut(a);
     LoraK k{a.x, a.adapter, a.qstart, a.scale, a.ranks, (float *)a.workspace, a.x_stride, (int)a.tokens, (int)a.batch,
-            (int)a.k, a.adapters, a.rank, a.targets, c.rank_tiles, c.splits, c.span, 256, {}, {}, {}, {}, {}, {}};
+            (int)a.k, a.adapters, a.rank, 0, c.rank_tiles, c.splits, c.span, 256, {}, {}, {}, {}, {}, {}};
+    // targets without columns are left out, whose pointers may be anything.  (The parts of
+    // k are those of all targets: the workspace is sized by them, and fewer targets could
+    // ask for more parts than it has room for.)
     for (int i = 0; i < a.targets; ++i) {
-        k.a[i] = (const _Float16 *)t[i].a;
-        k.b[i] = (const _Float16 *)t[i].b;
-        k.base[i] = t[i].base;
-        k.y[i] = t[i].y;
-        k.n[i] = (int)t[i].n;
+        if (t[i].n == 0)
+            continue;
+        k.a[k.targets] = (const _Float16 *)t[i].a;
+        k.b[k.targets] = (const _Float16 *)t[i].b;
+        k.base[k.targets] = t[i].base;
+        k.y[k.targets] = t[i].y;
+        k.n[k.targets++] = (int)t[i].n;
     }
+    c.cols = k.targets * c.rank_tiles;
     // tiles of 64 rows, a wave 16 of them: 512 columns where that leaves enough workgroups
     // (prompts of 6653 rows, three targets: 512 columns 76 us, 256 86), down to 64
     if (c.wide) {
         int64_t all = 0;
-        for (int i = 0; i < a.targets; ++i)
-            all += t[i].n;
+        for (int i = 0; i < k.targets; ++i)
+            all += k.n[i];
         k.out_cols = 512;
         while (k.out_cols > 64 && c.tiles * all / k.out_cols < 1024)
             k.out_cols /= 2;

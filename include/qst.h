@@ -172,6 +172,7 @@ QMM_API int qst_gemv_q8(int nprob, const qst_gemv_problem *probs, int64_t k, con
  * x fp32 enters the products as it is, fp16 the fp16 matrix cores; the inner
  * sums stay in fp32 and enter the second product as two fp16 parts of a common
  * power of two (22 bits of a row's largest); everything is summed in fp32.
+ * Targets of n 0 are skipped, their pointers not looked at.
  * Values of x, of the weights used and of scale must be finite.  The targets' y
  * are distinct, and overlap nothing else but their own base where it is y itself.
  * a: 16-byte aligned, k a multiple of 8; b: rank a multiple of 8, up to 256.
