@@ -196,7 +196,7 @@ static int check_lora(const qst_lora_args *a)
     if (!good_dtype(a->dtype))
         return QMM_ERR_TYPE;
     if (a->tokens < 0 || a->tokens > INT_MOST / qmm::LORA_TARGETS / qmm::LORA_RANK || a->batch < 0 ||
-        a->batch > 65535 || a->k < 8 || a->k > INT_MOST || a->k % 8 != 0 || a->adapters < 0 || a->rank < 8 ||
+        a->batch > 65535 || a->k < 8 || a->k > qmm::LORA_K || a->k % 8 != 0 || a->adapters < 0 || a->rank < 8 ||
         a->rank > qmm::LORA_RANK || a->rank % 8 != 0 || a->targets < 0 || a->targets > qmm::LORA_TARGETS)
         return QMM_ERR_SHAPE;
     return QMM_OK;

@@ -31,6 +31,9 @@ hipError_t launch_q8_large2(const Q8Probs (&p)[Q8_TYPES], int k, const uint8_t *
 
 constexpr int LORA_TARGETS = 8;
 constexpr int LORA_RANK = 256;
+// A part of k ends at most 64 x 128 past it (64 parts, each a multiple of 128 long), and a
+// loop looks at most 512 ahead: what they compare stays below 2^31.
+constexpr int64_t LORA_K = (1ll << 31) - (1 << 14);
 int64_t lora_workspace(const qst_lora_args &a);
 hipError_t launch_lora(const qst_lora_args &a, const qst_lora_target *t, hipStream_t s);
 

@@ -176,7 +176,7 @@ QMM_API int qst_gemv_q8(int nprob, const qst_gemv_problem *probs, int64_t k, con
  * Values of x, of the weights used and of scale must be finite.  The targets' y
  * are distinct, and overlap nothing else but their own base where it is y itself.
  * a: 16-byte aligned, k a multiple of 8; b: rank a multiple of 8, up to 256.
- * At most 1048575 tokens, and n up to 2^24.
+ * At most 1048575 tokens, n up to 2^24 and k up to 2^31 - 2^14.
  */
 typedef struct qst_lora_target {
     const void *a;      /* fp16 [adapters][rank][k] */

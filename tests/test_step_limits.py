@@ -1,0 +1,38 @@
+"""Limits of the sizes that the entries of include/qst.h take (CPU only: every call
+here ends in validation)."""
+import ctypes
+
+import pytest
+
+import test_abi
+
+A = 1 << 20          # never dereferenced
+
+
+@pytest.fixture(scope="module")
+def q():
+    return test_abi._lib()
+
+
+@pytest.fixture(scope="module")
+def step(q):
+    from dequant_matmul_amd import step
+    return step
+
+
+def lora_args(step, **kw):
+    d = dict(x=A, adapter=A, workspace=A, workspace_bytes=1 << 60, x_stride=1 << 31, tokens=1, batch=1, k=64, adapters=1,
+             rank=8, dtype=0, targets=1)
+    d.update(kw)
+    return step.LoraArgs(**d)
+
+
+@pytest.mark.parametrize("k,good", [(8, True), (2 ** 31 - 2 ** 14, True), (2 ** 31 - 2 ** 14 + 8, False),
+                                    (2 ** 31 - 8, False), (2 ** 31, False), (0, False), (12, False)])
+def test_k_of_adapters(q, step, k, good):
+    """No part of k ends past 2^31."""
+    a = lora_args(step, k=k)
+    assert (q.lib.qst_lora_workspace(ctypes.addressof(a)) > 0) == good
+    if not good:
+        t = step.LoraTarget(A, A, None, A, 8)
+        assert q.lib.qst_lora(ctypes.addressof(a), ctypes.addressof(t), None) == q.ERR_SHAPE
