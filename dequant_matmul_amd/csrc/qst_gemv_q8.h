@@ -32,6 +32,7 @@
 
 #include "qmm_device.h"
 #include "qmm_gemv_unit.h"
+#include "qst_index.h"
 #include "qst_launch.h"
 
 namespace qmm {
@@ -427,7 +428,7 @@ __device__ __forceinline__ void gemv_q8_body(const Q8Type &P, const uint8_t *x, 
         bytes = c.blk < total && row0 < n ? max(bytes, (int64_t)0) : 0;
         const int shift = EVEN ? 0 : (int)(from & 15);
         // whole chunks only: the bytes behind the matrix's last one are not touched
-        const int64_t whole = EVEN ? bytes : min((bytes + shift + 15) & ~(int64_t)15, (end - from + shift) & ~(int64_t)15);
+        const int64_t whole = EVEN ? bytes : whole_chunks(bytes, shift, end - from + shift);
         const uint8_t *base = P.w[c.p] + (bytes > 0 ? from - shift : 0);
         const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void *)base, (short)0, bytes > 0 ? (int)whole : 0, 0x00020000);
 #pragma unroll
@@ -494,10 +495,11 @@ __device__ __forceinline__ void gemv_q8_body(const Q8Type &P, const uint8_t *x, 
                 *(u32x4 *)(mine + 4 * o) = f[i];
         }
         if constexpr (!EVEN) {
-            // the matrix's last bytes, where they fill no chunk
+            // the matrix's last bytes, where they fill no chunk (a wave whose segment lies
+            // behind its row's end has no bytes)
             const int64_t left = end - from + shift;
-            const int tail = (int)(left & 15);
-            if (tail != 0 && left < BYTES && c.blk < total && row0 < n) {
+            const int tail = last_bytes(c.blk < total && row0 < n && 64 * seg < units, left, BYTES);
+            if (tail != 0) {
                 wave_lds_sync();
                 const int at = (int)(left & ~(int64_t)15) / 2 + lane;
                 if (2 * lane < tail)

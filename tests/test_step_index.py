@@ -49,3 +49,45 @@ for (int d = 1; d < 8; d *= 2)
 for (int i = 0; i < 8; ++i)
     printf("%u\\n", v[i]);"""
     assert [v for v, in run(tmp_path, body)] == [2 ** 31 - 1] + [2 ** 31] * 7
+
+
+# (bytes of a block, its elements, elements of a lane's unit) of the types whose rows
+# begin anywhere
+Q4_0, Q8_0, Q5_0, Q6_K = (18, 32, 32), (34, 32, 32), (22, 32, 32), (210, 256, 64)
+
+
+@pytest.mark.parametrize("bb,be,ue", [Q4_0, Q8_0, Q5_0, Q6_K])
+def test_items_stay_inside_the_matrix_and_their_part_of_lds(bb, be, ue, tmp_path):
+    """Every item of rows of up to 20 segments, in rounds of as many waves as the kernel
+    takes: whole chunks and last bytes lie inside the matrix, hold all of the item, and
+    land in the wave's own part."""
+    body = """
+const int64_t BB = %d, BE = %d, UE = %d, SEGB = 64 * UE / BE * BB;
+const int64_t MOST = SEGB + 16;
+long seen = 0, bad = 0, tails = 0, behind = 0;
+for (int64_t blocks = 1; blocks <= 20 * 64 * UE / BE; blocks += blocks < 70 ? 1 : 13)
+    for (int64_t n = 1; n <= 5; ++n) {
+        const int64_t rb = blocks * BB, units = blocks * BE / UE, segs = (units + 63) / 64;
+        const int64_t waves = segs < 8 ? segs : 8, rounds = (segs + waves - 1) / waves;
+        const int64_t rpi = units > 32 ? 1 : units > 16 ? 2 : 4, end = n * rb;
+        for (int64_t row0 = 0; row0 < n; row0 += rpi)
+            for (int64_t seg = 0; seg < rounds * waves; ++seg) {
+                const int64_t from = row0 * rb + seg * SEGB;
+                const int shift = (int)(from & 15);
+                int64_t bytes = rpi > 1 ? (rpi * rb < end - from ? rpi * rb : end - from)
+                                        : (SEGB < rb - seg * SEGB ? SEGB : rb - seg * SEGB);
+                bytes = bytes > 0 ? bytes : 0;
+                const int64_t left = end - from + shift, whole = whole_chunks(bytes, shift, left);
+                const int tail = last_bytes(64 * seg < units, left, (int)MOST);
+                const int64_t to = left & ~(int64_t)15;
+                ++seen, tails += tail != 0, behind += left < 0;
+                bad += whole < 0 || whole %% 16 != 0 || whole > MOST + 15;
+                bad += bytes > 0 && (from - shift < 0 || from - shift + whole > end);
+                bad += bytes > 0 && whole < bytes + shift && whole + tail < bytes + shift;
+                bad += bytes == 0 && whole != 0;
+                bad += tail != 0 && (to < 0 || to + tail > MOST || end - tail < 0);
+            }
+    }
+printf("%%ld %%ld %%ld %%ld\\n", seen, bad, tails, behind);""" % (bb, be, ue)
+    (seen, bad, tails, behind), = run(tmp_path, body)
+    assert bad == 0 and seen > 1000 and tails > 10 and behind > 10
