@@ -159,40 +159,66 @@ __global__ void __launch_bounds__(LPR < 256 ? 256 : LPR) norm_kernel(NormK a)
                 for (int j = 0; j < 8; ++j)
                     s[c][j] += t[c][j];
         }
-        float q = 0.f;
+        // the row's sum of (s by)^2
+        auto squares = [&](float by) __attribute__((always_inline)) {
+            float q = 0.f;
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
+            for (int c = 0; c < NC; ++c)
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                q = has[c] ? __builtin_fmaf(s[c][j], s[c][j], q) : q;
-        if constexpr (LPR <= 64) {
+                for (int j = 0; j < 8; ++j) {
+                    const float v = s[c][j] * by;
+                    q = has[c] ? __builtin_fmaf(v, v, q) : q;
+                }
+            if constexpr (LPR <= 64) {
 #pragma unroll
-            for (int d = 1; d < LPR; d *= 2)
-                q += __shfl_xor(q, d);
-        } else {
-            __shared__ float part[LPR / 64];
-            q = wave_sum(q);
-            __syncthreads();           // the row before has been summed
-            if ((threadIdx.x & 63) == 0)
-                part[threadIdx.x >> 6] = q;
-            __syncthreads();
-            q = 0.f;
+                for (int d = 1; d < LPR; d *= 2)
+                    q += __shfl_xor(q, d);
+            } else {
+                __shared__ float part[LPR / 64];
+                q = wave_sum(q);
+                __syncthreads();           // the sum before has been read
+                if ((threadIdx.x & 63) == 0)
+                    part[threadIdx.x >> 6] = q;
+                __syncthreads();
+                q = 0.f;
 #pragma unroll
-            for (int i = 0; i < LPR / 64; ++i)
-                q += part[i];
+                for (int i = 0; i < LPR / 64; ++i)
+                    q += part[i];
+            }
+            return q;
+        };
+        float q = squares(1.f), g;
+        if (a.sum) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                if (!live || !has[c])
+                    continue;
+                if (a.res)
+                    store8<VEC>((R *)a.sum + tok * a.ss + head, at[c], a.dim, s[c]);
+                else
+                    store8<VEC>((X *)a.sum + tok * a.ss + head, at[c], a.dim, s[c]);
+            }
         }
-        const float g = 1.f / sqrtf(q / (float)a.dim + a.eps);
+        if ((sizeof(X) == 4 || sizeof(R) == 4) && q > 3.40282347e38f) {
+            // Squares past fp32: the row is brought down by 2^80, where 65536 of the largest
+            // numbers' squares have a sum and what gets lost is too small beside them.  All
+            // lanes of a row have the same sum and go the same way.  (2^-40 goes to either
+            // factor of the result: neither leaves fp32.)
+            q = squares(0x1p-80f);
+            g = 0x1p-40f / sqrtf(q / (float)a.dim + a.eps * 0x1p-80f * 0x1p-80f);
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    s[c][j] *= 0x1p-40f;
+        } else {
+            g = 1.f / sqrtf(q / (float)a.dim + a.eps);
+        }
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             const int i = at[c];
             if (!live || !has[c])
                 continue;
-            if (a.sum) {
-                if (a.res)
-                    store8<VEC>((R *)a.sum + tok * a.ss + head, i, a.dim, s[c]);
-                else
-                    store8<VEC>((X *)a.sum + tok * a.ss + head, i, a.dim, s[c]);
-            }
             float y[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j)

@@ -111,7 +111,8 @@ typedef enum qst_out { QST_F32 = QKV_F32, QST_HALF = QKV_HALF, QST_Q8_0 = 16 + Q
  * residual of its own type and stride if `sum` is not the same buffer; nothing
  * else may overlap.  Pointers are aligned to their elements; x, residual, sum,
  * weight and out 16-byte aligned with dim and strides multiples of 8 are faster.
- * The squares are summed in fp32: their mean has to be finite.
+ * The squares are summed in fp32, those of larger rows by a power of two below:
+ * any finite s has its norm.
  */
 typedef struct qst_norm_args {
     const void *x;
