@@ -293,7 +293,8 @@ def _workspace(x, targets, a):
 
 def lora_workspace(x, targets, adapter):
     """A workspace tensor for lora() calls of these sizes (one call at a time may
-    use it)."""
+    use it).  Calls of fewer tokens can need more: uint8 [4 targets tokens rank
+    min(64, ceil(k / 1024))] is enough for any up to these."""
     return _workspace(x, targets, _lora(x, targets, adapter, None, None, None, None)[0])
 
 

@@ -206,8 +206,11 @@ typedef struct qst_lora_args {
 } qst_lora_args;
 
 /* Bytes of workspace for a call of these sizes (pointers are not looked at; the
- * targets' n neither); -1 for invalid sizes.  It does not shrink with `batch`
- * alone: a workspace kept for calls of several sizes has the largest of theirs. */
+ * targets' n neither); -1 for invalid sizes.  A call of fewer tokens, or of another
+ * batch, can need more than a larger one (its products are cut along k into more
+ * parts): a workspace kept for calls of several sizes has the largest of theirs, or
+ * 4 targets tokens rank min(64, ceil(k / 1024)) bytes, which no call of as many or
+ * fewer targets and tokens passes, whatever its batch. */
 QMM_API int64_t qst_lora_workspace(const qst_lora_args *a);
 
 QMM_API int qst_lora(const qst_lora_args *a, const qst_lora_target *targets, void *stream);

@@ -75,3 +75,33 @@ def test_targets_without_columns(place, lens, k, rank, dtype):
             assert bool(((y[rows].double() - want[rows]).abs() <= bar[rows]).all())
         none = torch.cat([torch.full((n,), int(adapter[i]) < 0) for i, n in enumerate(lens)])
         assert not y[none.to(DEV)].any()
+
+
+@pytest.mark.parametrize("dtype", [F32, F16])
+@pytest.mark.parametrize("rank", [8, 40, 136])
+@pytest.mark.parametrize("k", [64, 2056])
+@pytest.mark.parametrize("starts", [
+    [0, 4, 8, 12, 16], [0, 4, 900, 1000, 2 ** 31 - 1], [-50, 4, 8, 12, 16], [0, 12, 4, 16, 2], [16] * 5, [-9] * 5, [0, 16],
+    [-2 ** 31, 2 ** 31 - 1], [3, 200], [0, 1, 2, 3, 4], list(range(0, 200, 3)), list(range(0, -200, -3)),
+    [0] * 70 + [2 ** 31 - 1] * 60])
+def test_workspace_and_outputs_between_guards(starts, k, rank, dtype):
+    """Row starts in and out of order, inside and outside of the tokens, with a workspace
+    of the least size: nothing around it or the outputs is written."""
+    for T in (16, 150):
+        gen = torch.Generator().manual_seed(T + k)
+        x = torch.randn(T, k, generator=gen).to(dtype).to(DEV)
+        n_ad, n = 2, 70
+        a = (torch.randn(n_ad, rank, k, generator=gen) / k ** 0.5).half().to(DEV)
+        b = torch.randn(n_ad, n, rank, generator=gen).half().to(DEV)
+        adapter = torch.arange(len(starts) - 1, dtype=I32, device=DEV) % 3
+        qstart = torch.tensor(starts, dtype=I32, device=DEV)
+        out = torch.full((T * n + 32,), 5.0, device=DEV)
+        y = out[16:-16].view(T, n)
+        targets = [(a, b, None, y, n)]
+        need = call(x, targets, adapter, qstart, None, rank, n_ad)
+        buf = torch.full((need + 512,), 77, dtype=torch.uint8, device=DEV)
+        assert call(x, targets, adapter, qstart, buf[256:256 + need], rank, n_ad) == q.OK
+        torch.cuda.synchronize()
+        assert bool((buf[:256] == 77).all()) and bool((buf[256 + need:] == 77).all())
+        assert bool((out[:16] == 5).all()) and bool((out[-16:] == 5).all())
+        assert call(x, targets, adapter, qstart, buf[256:256 + need - 16], rank, n_ad) == q.ERR_WORKSPACE

@@ -36,3 +36,18 @@ def test_k_of_adapters(q, step, k, good):
     if not good:
         t = step.LoraTarget(A, A, None, A, 8)
         assert q.lib.qst_lora(ctypes.addressof(a), ctypes.addressof(t), None) == q.ERR_SHAPE
+
+
+def test_the_bound_of_the_workspace(q, step):
+    """What the header gives as the most for any smaller call of a step, over sizes on
+    either side of every rule; and that a smaller call can need more than a larger one."""
+    def need(**kw):
+        return q.lib.qst_lora_workspace(ctypes.addressof(lora_args(step, **kw)))
+    for targets in (1, 3, 8):
+        for rank in (8, 24, 64, 128, 256):
+            for k in (8, 1024, 1032, 4096, 14336, 65544, 1 << 20):
+                for tokens in (1, 2, 16, 53, 512, 3000, 8192, 100000):
+                    bound = 4 * targets * tokens * rank * min(64, -(-k // 1024))
+                    for batch in (1, 4, 16, 60, 200, 65535):
+                        assert 0 < need(targets=targets, rank=rank, k=k, tokens=tokens, batch=batch) <= bound
+    assert need(targets=3, rank=32, k=14336, tokens=3000, batch=1) > need(targets=3, rank=32, k=14336, tokens=8192, batch=4)
