@@ -69,8 +69,17 @@ class LoraArgs(ctypes.Structure):
 # These calls cost the host about as much as their kernels: the structs above are
 # written as bytes (a pointer that is not given is 0), one condition checks a tensor,
 # and its message is only made when it fails.
-_PLAN, _NORM = struct.Struct("@15q"), struct.Struct("@12qf3i")
-_PROBLEM, _TARGET, _LORA = struct.Struct("@3q2i"), struct.Struct("@5q"), struct.Struct("@11q4i")
+def _bytes_of(struct_class):
+    """The struct.Struct that writes the fields of a ctypes structure in order."""
+    code = {_P: "q", _I64: "q", _I32C: "i", ctypes.c_float: "f"}
+    s = struct.Struct("@" + "".join(code[t] for _, t in struct_class._fields_))
+    if s.size != ctypes.sizeof(struct_class):
+        raise TypeError("fields of %s leave gaps" % struct_class.__name__)
+    return s
+
+
+_PLAN, _NORM, _LORA = _bytes_of(PlanArgs), _bytes_of(NormArgs), _bytes_of(LoraArgs)
+_PROBLEM, _TARGET = _bytes_of(GemvProblem), _bytes_of(LoraTarget)
 
 _F32, _F16, _I32, _U8 = torch.float32, torch.float16, torch.int32, torch.uint8
 _DTYPES = {_F32: 0, _F16: 1}

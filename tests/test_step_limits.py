@@ -51,3 +51,12 @@ def test_the_bound_of_the_workspace(q, step):
                     for batch in (1, 4, 16, 60, 200, 65535):
                         assert 0 < need(targets=targets, rank=rank, k=k, tokens=tokens, batch=batch) <= bound
     assert need(targets=3, rank=32, k=14336, tokens=3000, batch=1) > need(targets=3, rank=32, k=14336, tokens=8192, batch=4)
+
+
+def test_calls_are_packed_as_the_structs(step):
+    """The bytes that a call hands over lie where the structs' fields do."""
+    for packer, struct in ((step._PLAN, step.PlanArgs), (step._NORM, step.NormArgs), (step._LORA, step.LoraArgs),
+                           (step._PROBLEM, step.GemvProblem), (step._TARGET, step.LoraTarget)):
+        values = [0.5 if t is ctypes.c_float else i + 1 for i, (_, t) in enumerate(struct._fields_)]
+        s = struct.from_buffer_copy(packer.pack(*values))
+        assert [getattr(s, name) for name, _ in struct._fields_] == values
