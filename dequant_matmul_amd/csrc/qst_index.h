@@ -7,10 +7,11 @@
 
 namespace qmm {
 
-// a + b, no more than cap (of any value up to 2^32 - 1).
-constexpr uint32_t sat_add(uint32_t a, uint32_t b, uint32_t cap)
+// a + b, no more than cap, of a, b <= cap.  WIDE: a cap of 2^31 and more, where two sums
+// at the cap pass 32 bits (a saturating addition: no DPP form, 3 to 7 % of a plan).
+template <bool WIDE = false> constexpr uint32_t sat_add(uint32_t a, uint32_t b, uint32_t cap)
 {
-    const uint32_t s = a + b, t = s < a ? 0xffffffffu : s;     // (one addition that saturates)
+    const uint32_t s = a + b, t = WIDE && s < a ? 0xffffffffu : s;
     return t < cap ? t : cap;
 }
 

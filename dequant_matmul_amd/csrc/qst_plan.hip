@@ -32,26 +32,27 @@ template <int CTRL, int ROWS> __device__ __forceinline__ uint32_t shifted(uint32
 }
 
 // Sums over the lanes up to this one, capped.
-__device__ __forceinline__ uint32_t wave_scan(uint32_t v, uint32_t cap)
+template <bool WIDE = false> __device__ __forceinline__ uint32_t wave_scan(uint32_t v, uint32_t cap)
 {
-    v = sat_add(v, shifted<0x111, 0xf>(v), cap);     // row_shr 1, 2, 4, 8
-    v = sat_add(v, shifted<0x112, 0xf>(v), cap);
-    v = sat_add(v, shifted<0x114, 0xf>(v), cap);
-    v = sat_add(v, shifted<0x118, 0xf>(v), cap);
-    v = sat_add(v, shifted<0x142, 0xa>(v), cap);     // lane 15 to row 1, 47 to row 3
-    v = sat_add(v, shifted<0x143, 0xc>(v), cap);     // lane 31 to rows 2 and 3
+    v = sat_add<WIDE>(v, shifted<0x111, 0xf>(v), cap);     // row_shr 1, 2, 4, 8
+    v = sat_add<WIDE>(v, shifted<0x112, 0xf>(v), cap);
+    v = sat_add<WIDE>(v, shifted<0x114, 0xf>(v), cap);
+    v = sat_add<WIDE>(v, shifted<0x118, 0xf>(v), cap);
+    v = sat_add<WIDE>(v, shifted<0x142, 0xa>(v), cap);     // lane 15 to row 1, 47 to row 3
+    v = sat_add<WIDE>(v, shifted<0x143, 0xc>(v), cap);     // lane 31 to rows 2 and 3
     return v;
 }
 
-// Two sums at once over the threads before this one, each with its cap; all[0], all[1]
+// Two sums at once over the threads before this one, each with its cap (WIDE: of the first); all[0], all[1]
 // receive the totals.
 struct Two {
     uint32_t a, b;
 };
-template <int NT> __device__ __forceinline__ Two block_scan(Two v, Two cap, uint32_t *part, Two *all)
+template <int NT, bool WIDE = false>
+__device__ __forceinline__ Two block_scan(Two v, Two cap, uint32_t *part, Two *all)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const Two w = {wave_scan(v.a, cap.a), wave_scan(v.b, cap.b)};
+    const Two w = {wave_scan<WIDE>(v.a, cap.a), wave_scan(v.b, cap.b)};
     Two up = {shifted<0x138, 0xf>(w.a), shifted<0x138, 0xf>(w.b)};     // wave_shr 1: 0 to lane 0
     if constexpr (NT == 64) {
         *all = Two{(uint32_t)__builtin_amdgcn_readlane((int)w.a, 63), (uint32_t)__builtin_amdgcn_readlane((int)w.b, 63)};
@@ -67,9 +68,9 @@ template <int NT> __device__ __forceinline__ Two block_scan(Two v, Two cap, uint
 #pragma unroll
     for (int i = 0; i < NT / 64; ++i) {
         const Two p = {part[2 * i], part[2 * i + 1]};
-        up.a = i < wave ? sat_add(up.a, p.a, cap.a) : up.a;
+        up.a = i < wave ? sat_add<WIDE>(up.a, p.a, cap.a) : up.a;
         up.b = i < wave ? sat_add(up.b, p.b, cap.b) : up.b;
-        total.a = sat_add(total.a, p.a, cap.a);
+        total.a = sat_add<WIDE>(total.a, p.a, cap.a);
         total.b = sat_add(total.b, p.b, cap.b);
     }
     *all = total;
@@ -132,7 +133,8 @@ struct PlanK {
     int vec;         // slots and pos take 16-byte stores
 };
 
-template <int NT> __global__ void __launch_bounds__(NT) plan_kernel(PlanK a)
+// WIDE: of 2^31 - 1 tokens.
+template <int NT, bool WIDE = false> __global__ void __launch_bounds__(NT) plan_kernel(PlanK a)
 {
     __shared__ uint32_t part[NT / 32], begins[NT], firsts[NT];
     __shared__ int ctxs[NT], olds[NT];
@@ -164,9 +166,9 @@ template <int NT> __global__ void __launch_bounds__(NT) plan_kernel(PlanK a)
         if (in && fits && (c & pm) != 0)
             old = a.table[(int64_t)b * a.columns + (c >> a.shift)];
         Two all;
-        const Two before = block_scan<NT>(Two{min((uint32_t)n, tcap), min((uint32_t)need, pcap)}, Two{tcap, pcap}, part, &all);
-        const uint32_t begin = sat_add(row_base, before.a, tcap), first = sat_add(page_base, before.b, pcap);
-        const uint32_t end = sat_add(begin, min((uint32_t)n, tcap), tcap);
+        const Two before = block_scan<NT, WIDE>(Two{min((uint32_t)n, tcap), min((uint32_t)need, pcap)}, Two{tcap, pcap}, part, &all);
+        const uint32_t begin = sat_add<WIDE>(row_base, before.a, tcap), first = sat_add(page_base, before.b, pcap);
+        const uint32_t end = sat_add<WIDE>(begin, min((uint32_t)n, tcap), tcap);
         const uint32_t upto = sat_add(first, min((uint32_t)need, pcap), pcap);
         // requests whose rows end past `tokens` are the last ones, so the pages they
         // would need are in the sums of none that is served
@@ -184,7 +186,7 @@ template <int NT> __global__ void __launch_bounds__(NT) plan_kernel(PlanK a)
         const bool many = each_entry<NT>(Run{(int64_t)b * a.columns + have, F - 1 - first, ok ? need : 0}, mine, live, runs,
                                          [&](const Run &r, int i) { a.table[r.at + i] = a.free[r.top - i]; }, n > FEW);
         taken = max(taken, ok && need > 0 ? upto : 0u);
-        const uint32_t stop = sat_add(row_base, all.a, tcap);
+        const uint32_t stop = sat_add<WIDE>(row_base, all.a, tcap);
         if (gridDim.x == 1 && !many) {
             // a few rows each (decoding): by the request's own thread
             const uint32_t last = min(end, (uint32_t)a.tokens);
@@ -363,7 +365,8 @@ hipError_t launch_plan(const qst_plan_args &a, hipStream_t s)
     // 4096 rows a workgroup of 1024; more only where there would be more than 1024 of them
     const int groups = share_out(a.tokens, 4096, 1024);
     k.share = (int)(((a.tokens + groups - 1) / groups + 3) & ~(int64_t)3);
-    const hipError_t e = groups > 1 || a.batch > 256 ? start(plan_kernel<1024>, dim3(groups), dim3(1024), s, k)
+    const hipError_t e = a.tokens == 0x7fffffff ? start(plan_kernel<1024, true>, dim3(groups), dim3(1024), s, k)
+                         : groups > 1 || a.batch > 256 ? start(plan_kernel<1024>, dim3(groups), dim3(1024), s, k)
                          : a.batch > 64 || a.tokens > 512 ? start(plan_kernel<256>, dim3(1), dim3(256), s, k)
                                                           : start(plan_kernel<64>, dim3(1), dim3(64), s, k);
     if (e != hipSuccess || groups == 1 || a.left != a.count)

@@ -36,7 +36,7 @@ def test_sums_stay_at_their_cap(tmp_path):
     caps = [0, 1, 5, 2 ** 31 - 1, 2 ** 31, 2 ** 32 - 1]
     cases = [(a, b, c) for c in caps for a in {0, 1, c // 2, c // 2 + 1, c - 1, c} for b in {0, 1, c // 2, c - 1, c}
              if 0 <= a <= c and 0 <= b <= c]
-    body = "\n".join('printf("%%u\\n", sat_add(%du, %du, %du));' % c for c in cases)
+    body = "\n".join('printf("%%u\\n", sat_add<%s>(%du, %du, %du));' % (str(c[2] >= 2 ** 31).lower(), *c) for c in cases)
     assert run(tmp_path, body) == [[min(a + b, c)] for a, b, c in cases]
 
 
@@ -45,7 +45,7 @@ def test_sums_of_pairs_of_the_longest_requests(tmp_path):
     body = """uint32_t v[8] = {0x7fffffffu, 0x7fffffffu, 0x7fffffffu, 0x7fffffffu, 1, 0, 0, 0}, cap = 0x80000000u;
 for (int d = 1; d < 8; d *= 2)
     for (int i = 7; i >= d; --i)
-        v[i] = sat_add(v[i], v[i - d], cap);
+        v[i] = sat_add<true>(v[i], v[i - d], cap);
 for (int i = 0; i < 8; ++i)
     printf("%u\\n", v[i]);"""
     assert [v for v, in run(tmp_path, body)] == [2 ** 31 - 1] + [2 ** 31] * 7
