@@ -4,7 +4,11 @@
 //   y[b][j] = sum over blocks of  d_w d_x sum_i q_i x_i      (Q4_0, Q5_0, Q6_K: q less its offset)
 //                                 d_x (d sc Q - dmin m S)    (Q4_K, Q5_K: Q = sum q x, S = sum x)
 //
-// Bound: reading the weights for one to three rows of x, instructions for more.
+// Bound: reading the weights for one to three rows of x where a row of weights is one
+// segment (below), instructions for more.  Rows of several segments have waves that are
+// part empty (14336 is three and a half) and meet every few rows; the 32-element types,
+// whose segments are half as long, take the same time whatever their bytes (28672 x
+// 4096, one row: 25 us of 66 MB in Q4_0, 27 of 125 in Q8_0).
 // v_dot4_i32_i8 takes four products an instruction and needs no conversion of codes;
 // a row of x costs 16 of them and 12 others for a lane's 64 weights of Q4_K, and its
 // part of x 20 registers, which leave two waves a SIMD from batch 5 on.

@@ -5,8 +5,8 @@
 //
 // Two launches: the inner sums of every row, target and rank, cut along k where
 // there are few rows, and the outputs; up to four single tokens of low rank take one.
-// Bound: a few rows, round trips in turn (request, adapter, A, B) and the adapters'
-// bytes; a prompt, y's.
+// Bound: a few rows, round trips in turn (request, adapter, A, B); a decode batch, A's
+// bytes as they are read, 64 at a time from rows kilobytes apart; a prompt, y's.
 //
 // Measured: one token, rank 16, two targets of a 4096 wide fp32 x 6.6 us; 53 tokens of
 // 24 adapters, rank 64, 28 us (17 and 12 for the two launches); prompts of 6653 rows,
